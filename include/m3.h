@@ -298,6 +298,101 @@ m3_status m3_scan_fwd_reflect(const m3_dims* dims, const void* u,
                               const float* theta, const m3_carry* init,
                               void* y, m3_carry* final_state, void* stream);
 
+/* ------------------------------------------------------ gated delta rule --
+ * A second recurrent layer with the same kind of state (S in R^{N x P} a head,
+ * float32), for stacks that mix it with the scan above.  Per batch b and head
+ * h (keys and queries of group g = h / (nheads/ngroups)):
+ *   a_t = e^{g_t}
+ *   u_t = beta_t (v_t - a_t S_{t-1}^T k_t)
+ *   S_t = a_t S_{t-1} + k_t u_t^T
+ *   y_t = scale S_t^T q_t
+ * The transition is a contraction for |k_t| <= 1, 0 <= beta_t <= 2 and
+ * g_t <= 0 (keys normalised by the caller, for example by m3_rms_norm_fwd);
+ * other values are computed as written and may grow.
+ * g_t = -infinity resets the state before the token (log decays below -1e4
+ * count as -1e4, where e^g is zero in float32).
+ *
+ * Layouts (C order, densely packed, 16-byte aligned):
+ *   q, k     [batch][seqlen][ngroups][dstate]     io dtype
+ *   v, y     [batch][seqlen][nheads][headdim]     io dtype
+ *   g, beta  [batch][seqlen][nheads]              float32
+ *   states   [batch][nheads][dstate][headdim]     float32
+ *   lengths  [batch]                              int32, device memory
+ * dims->rank must be 1 and dstate at most 256 (M3_ERR_UNSUPPORTED otherwise);
+ * dims->chunk is ignored.  `g` may be NULL (no decay).
+ * `lengths` may be NULL (every sequence has seqlen tokens).  Otherwise sequence
+ * b has lengths[b] tokens (values outside 0..seqlen count as the nearer bound):
+ * its final state is the one after its last token, rows of y behind it are left
+ * as they were, and gradients behind it are zero.
+ * Arithmetic is float32. */
+
+/* Bytes of device workspace m3_delta_fwd needs (host-only; at least 256: the
+ * status word that m3_device_status reads). */
+m3_status m3_delta_workspace_size(const m3_dims* dims, size_t* bytes);
+
+/* Prefill: y for every token from `init_h` (NULL = zeros), and the state after
+ * the last token into `final_h` (may be NULL; may be the buffer of init_h).
+ * `workspace` as for m3_scan_fwd. */
+m3_status m3_delta_fwd(const m3_dims* dims, const void* q, const void* k, const void* v,
+                       const float* g, const float* beta, float scale, const int* lengths,
+                       const float* init_h, void* y, float* final_h,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* One decode token (layouts without the seqlen axis): reads the state h_in and
+ * writes h_out, which may be the same buffer (otherwise they must not overlap).
+ * dims->seqlen is ignored.  No workspace. */
+m3_status m3_delta_step(const m3_dims* dims, const float* h_in, float* h_out,
+                        const void* q, const void* k, const void* v,
+                        const float* g, const float* beta, float scale, void* y, void* stream);
+
+/* Bytes of device workspace m3_delta_bwd needs (host-only). */
+m3_status m3_delta_bwd_workspace_size(const m3_dims* dims, size_t* bytes);
+
+/* Gradient of m3_delta_fwd: of J = sum <dy_t, y_t> + <d_final_h, final state>
+ * (over the tokens of each sequence; rows of dy behind its end are not read
+ * as gradient) with respect to every input.  dq, dk (summed over the heads of
+ * a group), dv, dg and dbeta are written in the io dtype, in which the
+ * projections' backward products take them; sums are float32 and rounded once
+ * at the end.  dg may be NULL; d_final_h and d_init_h (float32) may be NULL.
+ * Results do not depend on the order in which blocks run.  Outputs must not
+ * overlap inputs. */
+m3_status m3_delta_bwd(const m3_dims* dims, const void* q, const void* k, const void* v,
+                       const float* g, const float* beta, float scale, const int* lengths,
+                       const float* init_h, const void* dy, const float* d_final_h,
+                       void* dq, void* dk, void* dv, void* dg, void* dbeta, float* d_init_h,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* -------------------------------------------------- root-mean-square norm --
+ * The norm before and inside the recurrent layers (the residual stream; keys,
+ * queries, B and C with width = dstate).  For every row of `width` elements:
+ *   s = x + residual                       (residual NULL: s = x)
+ *   y = weight * s * (mean(s^2) + eps)^(-1/2)      (weight NULL: ones)
+ * x, residual, sum, y [rows][width] io dtype; weight [width] float32.  Any of
+ * sum, y and y8 may be NULL, not all three.  y is normalised from the unrounded
+ * float32 sum.  `sum` may be the buffer of x or of residual.
+ * y8 [rows][width] is e4m3 (1 byte), y8 * scale stands for y: scale is
+ * max|y| / 448 over `scale_block` columns, 0 = the whole row
+ * (scale [rows], float32) or 128 (scale [rows][ceil(width/128)]); other values
+ * return M3_ERR_UNSUPPORTED.  A block of zeros has the scale 1e-30 / 448.
+ * Pointers 16-byte aligned; no workspace.  rows = 0 is a valid empty call. */
+m3_status m3_rms_norm_fwd(long long rows, int width, int io_dtype, const void* x, const void* residual,
+                          const float* weight, float eps, void* sum, void* y,
+                          void* y8, float* scale, int scale_block, void* stream);
+
+/* Bytes of device workspace m3_rms_norm_bwd needs (host-only): parts of the
+ * weight's gradient. */
+m3_status m3_rms_norm_bwd_workspace_size(long long rows, int width, int io_dtype, size_t* bytes);
+
+/* Gradient of m3_rms_norm_fwd at its input s (`sum`, or x without a residual):
+ *   dx = d_sum + ds,  ds the gradient of <dy, y>;   dweight = sum over rows
+ * dx (io dtype) is the gradient of x and of residual alike.  d_sum (NULL: none)
+ * is the gradient that reaches the stored sum through the residual stream.
+ * dweight [width] float32 may be NULL.  dx may be the buffer of dy or d_sum.
+ * Sums are float32 and added in a fixed order. */
+m3_status m3_rms_norm_bwd(long long rows, int width, int io_dtype, const void* s, const float* weight,
+                          float eps, const void* dy, const void* d_sum, void* dx, float* dweight,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* How m3_scan_fwd will run `dims` (host-only, nothing launched): the number
  * of kernel launches one call makes, the segments each (batch, head)
  * sequence is cut into, the chunk length the kernels use, and the path
@@ -333,7 +428,8 @@ m3_status m3_selftest_bounded_wait(void* workspace, size_t workspace_bytes, void
  * the first failure recorded by the lowest-numbered source file that has one
  * (site = file * 1000 + check: 1 tile prefill, 2 SIMT prefill and segment
  * combine, 3 decode step, 4 rope, 5 transition variants, 6 backward,
- * 7 phase prologues, 8 persistent prefill, 9 this self-test; for a span the
+ * 7 phase prologues, 8 persistent prefill, 9 this self-test, 10 delta rule,
+ * 11 norm; for a span the
  * index is its last element).  `clear` != 0 resets the records after reading.
  * M3_ERR_INVALID_ARG for a NULL `out`, M3_ERR_CUDA if the device cannot be
  * read.  Host call; the release build touches no device. */

@@ -92,6 +92,18 @@ def _load():
     lib.m3_scan_fwd_damped.restype = I
     lib.m3_scan_fwd_reflect.argtypes = [D, V, V, V, V, V, V, V, V, C, V, C, V]
     lib.m3_scan_fwd_reflect.restype = I
+    F = ctypes.c_float
+    lib.m3_delta_workspace_size.argtypes = [D, ctypes.POINTER(S)]
+    lib.m3_delta_fwd.argtypes = [D, V, V, V, V, V, F, V, V, V, V, V, S, V]
+    lib.m3_delta_step.argtypes = [D, V, V, V, V, V, V, V, F, V, V]
+    lib.m3_delta_bwd_workspace_size.argtypes = [D, ctypes.POINTER(S)]
+    lib.m3_delta_bwd.argtypes = [D, V, V, V, V, V, F, V, V, V, V, V, V, V, V, V, V, V, S, V]
+    lib.m3_rms_norm_fwd.argtypes = [LL, I, I, V, V, V, F, V, V, V, V, I, V]
+    lib.m3_rms_norm_bwd_workspace_size.argtypes = [LL, I, I, ctypes.POINTER(S)]
+    lib.m3_rms_norm_bwd.argtypes = [LL, I, I, V, V, F, V, V, V, V, V, S, V]
+    for f in ("m3_delta_workspace_size", "m3_delta_fwd", "m3_delta_step", "m3_delta_bwd_workspace_size",
+              "m3_delta_bwd", "m3_rms_norm_fwd", "m3_rms_norm_bwd_workspace_size", "m3_rms_norm_bwd"):
+        getattr(lib, f).restype = I
     lib.m3_status_string.argtypes = [I]
     lib.m3_status_string.restype = ctypes.c_char_p
     for f in ("m3_scan_workspace_size", "m3_scan_fwd", "m3_step", "m3_rope_bc", "m3_device_status"):
@@ -106,7 +118,9 @@ ABI_SYMBOLS = ("m3_scan_workspace_size", "m3_scan_fwd", "m3_step", "m3_rope_bc",
                "m3_scan_plan", "m3_device_status", "m3_selftest_bounded_wait", "m3_debug_bounds_report",
                "m3_selftest_bounds_check", "m3_scan_fwd_static",
                "m3_static_forget_device", "m3_scan_bwd_workspace_size", "m3_scan_bwd", "m3_scan_phase_workspace_size",
-               "m3_scan_fwd_phase", "m3_scan_fwd_damped", "m3_scan_fwd_reflect", "m3_status_string")
+               "m3_scan_fwd_phase", "m3_scan_fwd_damped", "m3_scan_fwd_reflect", "m3_delta_workspace_size",
+               "m3_delta_fwd", "m3_delta_step", "m3_delta_bwd_workspace_size", "m3_delta_bwd", "m3_rms_norm_fwd",
+               "m3_rms_norm_bwd_workspace_size", "m3_rms_norm_bwd", "m3_status_string")
 
 
 @dataclasses.dataclass
@@ -356,6 +370,142 @@ def m3_scan_fwd_reflect(dims: Dims, u, x, B, C, dt, A, lam, theta, y,
     _check(st, "m3_scan_fwd_reflect")
 
 
+# ------------------------------------------------- gated delta rule, norm --
+def _dev(*tensors) -> torch.device:
+    """The one device all given tensors are on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("m3 takes device tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"m3 takes tensors of one device, got {dev} and {t.device}")
+    return dev
+
+
+def _arg(t: Optional[torch.Tensor], what: str, dtype: torch.dtype, numel: int):
+    """Device pointer of a contiguous tensor of the expected type and size."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{what} is {dtype}, got {t.dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{what} has {numel} elements for these dims, got {t.numel()}")
+    return _ptr(t)
+
+
+def _on(dev: torch.device, stream, call):
+    """``call(stream)`` with ``dev`` current (streams and launches are a device's)."""
+    if dev is None or dev.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(dev):
+        return call(_stream(stream))
+
+
+def _io_torch(dims: Dims) -> torch.dtype:
+    return torch.bfloat16 if dims.io_dtype == M3_BF16 else torch.float32
+
+
+def _size_query(fn, what: str, *args) -> int:
+    n = ctypes.c_size_t(0)
+    _check(fn(*args, ctypes.byref(n)), what)
+    return int(n.value)
+
+
+def m3_delta_workspace_size(dims: Dims) -> int:
+    return _size_query(_lib.m3_delta_workspace_size, "m3_delta_workspace_size", ctypes.byref(dims.c()))
+
+
+def m3_delta_bwd_workspace_size(dims: Dims) -> int:
+    return _size_query(_lib.m3_delta_bwd_workspace_size, "m3_delta_bwd_workspace_size", ctypes.byref(dims.c()))
+
+
+def m3_delta_fwd(dims: Dims, q, k, v, g, beta, y, workspace, scale: float = 1.0, lengths=None, init_h=None,
+                 final_h=None, stream=None) -> None:
+    """Gated delta rule over whole sequences (see include/m3.h): writes ``y``
+    and, if given, ``final_h``.  ``g`` may be None (no decay); ``lengths`` is
+    an int32 device tensor [batch] or None."""
+    dev = _dev(q, k, v, g, beta, y, workspace, lengths, init_h, final_h)
+    io, tok = _io_torch(dims), dims.batch * dims.seqlen
+    nk, nv, ng = tok * dims.ngroups * dims.dstate, tok * dims.nheads * dims.headdim, tok * dims.nheads
+    nh = dims.batch * dims.nheads * dims.dstate * dims.headdim
+    args = (_arg(q, "q", io, nk), _arg(k, "k", io, nk), _arg(v, "v", io, nv), _arg(g, "g", torch.float32, ng),
+            _arg(beta, "beta", torch.float32, ng), float(scale), _arg(lengths, "lengths", torch.int32, dims.batch),
+            _arg(init_h, "init_h", torch.float32, nh), _arg(y, "y", io, nv),
+            _arg(final_h, "final_h", torch.float32, nh), _ptr(workspace), workspace.numel() * workspace.element_size())
+    _check(_on(dev, stream, lambda st: _lib.m3_delta_fwd(ctypes.byref(dims.c()), *args, st)), "m3_delta_fwd")
+
+
+def m3_delta_step(dims: Dims, h, q, k, v, g, beta, y, scale: float = 1.0, h_out=None, stream=None) -> None:
+    """One decode token of the gated delta rule; the state ``h`` is updated in
+    place, or left alone and the new one written to ``h_out`` if given."""
+    out = h if h_out is None else h_out
+    dev = _dev(h, out, q, k, v, g, beta, y)
+    io = _io_torch(dims)
+    nk, ng = dims.batch * dims.ngroups * dims.dstate, dims.batch * dims.nheads
+    nv, nh = ng * dims.headdim, ng * dims.dstate * dims.headdim
+    args = (_arg(h, "h", torch.float32, nh), _arg(out, "h_out", torch.float32, nh), _arg(q, "q", io, nk),
+            _arg(k, "k", io, nk), _arg(v, "v", io, nv), _arg(g, "g", torch.float32, ng),
+            _arg(beta, "beta", torch.float32, ng), float(scale), _arg(y, "y", io, nv))
+    _check(_on(dev, stream, lambda st: _lib.m3_delta_step(ctypes.byref(dims.c()), *args, st)), "m3_delta_step")
+
+
+def m3_delta_bwd(dims: Dims, q, k, v, g, beta, dy, grads: dict, workspace, scale: float = 1.0, lengths=None,
+                 init_h=None, d_final_h=None, d_init_h=None, stream=None) -> None:
+    """Gradient of m3_delta_fwd (see include/m3.h).  ``grads`` holds the output
+    tensors dq, dk, dv, dg, dbeta in the io dtype (dg may be absent)."""
+    outs = [grads[n] for n in ("dq", "dk", "dv")] + [grads.get("dg"), grads["dbeta"]]
+    dev = _dev(q, k, v, g, beta, dy, *outs, workspace, lengths, init_h, d_final_h, d_init_h)
+    io, tok = _io_torch(dims), dims.batch * dims.seqlen
+    nk, nv, ng = tok * dims.ngroups * dims.dstate, tok * dims.nheads * dims.headdim, tok * dims.nheads
+    nh = dims.batch * dims.nheads * dims.dstate * dims.headdim
+    args = (_arg(q, "q", io, nk), _arg(k, "k", io, nk), _arg(v, "v", io, nv), _arg(g, "g", torch.float32, ng),
+            _arg(beta, "beta", torch.float32, ng), float(scale), _arg(lengths, "lengths", torch.int32, dims.batch),
+            _arg(init_h, "init_h", torch.float32, nh), _arg(dy, "dy", io, nv),
+            _arg(d_final_h, "d_final_h", torch.float32, nh), _arg(outs[0], "dq", io, nk), _arg(outs[1], "dk", io, nk),
+            _arg(outs[2], "dv", io, nv), _arg(outs[3], "dg", io, ng), _arg(outs[4], "dbeta", io, ng),
+            _arg(d_init_h, "d_init_h", torch.float32, nh), _ptr(workspace),
+            workspace.numel() * workspace.element_size())
+    _check(_on(dev, stream, lambda st: _lib.m3_delta_bwd(ctypes.byref(dims.c()), *args, st)), "m3_delta_bwd")
+
+
+def m3_rms_norm_fwd(x, eps: float, residual=None, weight=None, sum=None, y=None, y8=None, scale=None,
+                    scale_block: int = 0, stream=None) -> None:
+    """Root-mean-square norm of the rows (last axis) of ``x`` plus ``residual``
+    (see include/m3.h): writes whichever of ``sum``, ``y`` (io dtype) and ``y8``
+    with ``scale`` (float8_e4m3fn, float32) are given."""
+    dev = _dev(x, residual, weight, sum, y, y8, scale)
+    io, width, n = x.dtype, x.shape[-1], x.numel()
+    rows = n // width if width else 0
+    blocks = -(-width // scale_block) if scale_block > 0 else 1
+    args = (_arg(x, "x", io, n), _arg(residual, "residual", io, n), _arg(weight, "weight", torch.float32, width),
+            float(eps), _arg(sum, "sum", io, n), _arg(y, "y", io, n), _arg(y8, "y8", torch.float8_e4m3fn, n),
+            _arg(scale, "scale", torch.float32, rows * blocks), int(scale_block))
+    code = io_dtype_of(x)
+    _check(_on(dev, stream, lambda st: _lib.m3_rms_norm_fwd(rows, width, code, *args, st)), "m3_rms_norm_fwd")
+
+
+def m3_rms_norm_bwd_workspace_size(rows: int, width: int, io_dtype: int) -> int:
+    return _size_query(_lib.m3_rms_norm_bwd_workspace_size, "m3_rms_norm_bwd_workspace_size", int(rows), int(width),
+                       int(io_dtype))
+
+
+def m3_rms_norm_bwd(s, dy, eps: float, dx, workspace, weight=None, d_sum=None, dweight=None, stream=None) -> None:
+    """Gradient of m3_rms_norm_fwd at its input ``s`` (the stored sum): writes
+    ``dx`` (io dtype) and, if given, ``dweight`` (float32)."""
+    dev = _dev(s, dy, dx, workspace, weight, d_sum, dweight)
+    io, width, n = s.dtype, s.shape[-1], s.numel()
+    rows = n // width if width else 0
+    args = (_arg(s, "s", io, n), _arg(weight, "weight", torch.float32, width), float(eps), _arg(dy, "dy", io, n),
+            _arg(d_sum, "d_sum", io, n), _arg(dx, "dx", io, n), _arg(dweight, "dweight", torch.float32, width),
+            _ptr(workspace), workspace.numel() * workspace.element_size())
+    code = io_dtype_of(s)
+    _check(_on(dev, stream, lambda st: _lib.m3_rms_norm_bwd(rows, width, code, *args, st)), "m3_rms_norm_bwd")
+
+
 def raw_lib():
     """The ctypes handle (for calls that pass raw pointers)."""
     return _lib
@@ -366,5 +516,7 @@ __all__ = ["Dims", "Carry", "M3Error", "m3_scan_workspace_size", "m3_scan_fwd", 
            "m3_selftest_bounds_check", "DEBUG_BOUNDS", "m3_scan_fwd_static",
            "m3_static_forget_device", "m3_scan_bwd_workspace_size", "m3_scan_bwd", "m3_status_string",
            "m3_scan_phase_workspace_size", "m3_scan_fwd_phase", "m3_scan_fwd_damped", "m3_scan_fwd_reflect",
+           "m3_delta_workspace_size", "m3_delta_fwd", "m3_delta_step", "m3_delta_bwd_workspace_size", "m3_delta_bwd",
+           "m3_rms_norm_fwd", "m3_rms_norm_bwd_workspace_size", "m3_rms_norm_bwd",
            "M3_DAMP_UNDER", "M3_DAMP_CRITICAL", "M3_DAMP_OVER", "io_dtype_of", "ABI_SYMBOLS",
            "M3_F32", "M3_BF16", "raw_lib", "LIB_PATH"]

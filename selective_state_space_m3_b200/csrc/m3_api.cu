@@ -25,6 +25,8 @@ cudaError_t bounds_take_seq(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_bwd(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_phase(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_scan_ws(BoundsRecord* out, bool clear);
+cudaError_t bounds_take_delta(BoundsRecord* out, bool clear);
+cudaError_t bounds_take_norm(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_api(BoundsRecord* out, bool clear);
 
 // the check itself, on one index the caller chose (m3_selftest_bounds_check)
@@ -629,6 +631,195 @@ m3_status m3_selftest_bounded_wait(void* workspace, size_t workspace_bytes, void
                : M3_ERR_CUDA;
 }
 
+// ------------------------------------------------------- gated delta rule --
+// shape checks that the delta rule adds to check_dims
+static m3_status check_delta(const m3_dims* d, bool need_seq) {
+    m3_status s = check_dims(d, need_seq);
+    if (s != M3_OK) return s;
+    if (d->rank != 1 || d->dstate > 256) return M3_ERR_UNSUPPORTED;
+    // launch grids are one-dimensional
+    const long long kMax = 0x7fffffffLL, bh = (long long)d->batch * d->nheads;
+    if (bh > kMax || bh * delta_tiles(*d) > kMax) return M3_ERR_UNSUPPORTED;
+    if (need_seq && (long long)d->batch * d->seqlen * d->ngroups > kMax) return M3_ERR_UNSUPPORTED;
+    return M3_OK;
+}
+
+static DeltaParams delta_params(const m3_dims& d, const void* q, const void* k, const void* v, const float* g,
+                                const float* beta, float scale, const int* lengths) {
+    DeltaParams p;
+    memset(&p, 0, sizeof(p));
+    p.batch = d.batch; p.seqlen = d.seqlen; p.nheads = d.nheads; p.ngroups = d.ngroups;
+    p.headdim = d.headdim; p.dstate = d.dstate; p.scale = scale;
+    p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta; p.lengths = lengths;
+    return p;
+}
+
+// a call without tokens: the state (or its gradient) passes through
+static m3_status state_passthrough(const m3_dims& d, const float* in, float* out, cudaStream_t st) {
+    if (!out || d.batch == 0 || in == out) return M3_OK;
+    const size_t bytes = (size_t)d.batch * d.nheads * d.dstate * d.headdim * sizeof(float);
+    const cudaError_t e = in ? cudaMemcpyAsync(out, in, bytes, cudaMemcpyDeviceToDevice, st) : cudaMemsetAsync(out, 0, bytes, st);
+    return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+}
+
+m3_status m3_delta_workspace_size(const m3_dims* d, size_t* bytes) {
+    if (!bytes) return M3_ERR_INVALID_ARG;
+    const m3_status s = check_delta(d, true);
+    if (s != M3_OK) return s;
+    *bytes = kWorkspaceHeaderBytes;
+    return M3_OK;
+}
+
+m3_status m3_delta_fwd(const m3_dims* d, const void* q, const void* k, const void* v, const float* g,
+                       const float* beta, float scale, const int* lengths, const float* init_h, void* y,
+                       float* final_h, void* workspace, size_t ws_bytes, void* stream) {
+    const NvtxRange range("m3_delta_fwd");
+    size_t need = 0;
+    const m3_status s = m3_delta_workspace_size(d, &need);
+    if (s != M3_OK) return s;
+    const bool work = d->batch > 0 && d->seqlen > 0;
+    if (work && !ptrs_ok({q, k, v, beta, y})) return M3_ERR_INVALID_ARG;
+    if (!opt_ptrs_ok({g, lengths, init_h, final_h})) return M3_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || ws_bytes < need) return M3_ERR_WORKSPACE;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (!work) return state_passthrough(*d, init_h, final_h, st);
+    DeltaParams p = delta_params(*d, q, k, v, g, beta, scale, lengths);
+    p.init_h = init_h;
+    p.y = y;
+    p.final_h = final_h;
+    return launch_delta_seq(*d, p, st) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+}
+
+m3_status m3_delta_step(const m3_dims* d, const float* h_in, float* h_out, const void* q, const void* k,
+                        const void* v, const float* g, const float* beta, float scale, void* y, void* stream) {
+    const NvtxRange range("m3_delta_step");
+    const m3_status s = check_delta(d, false);
+    if (s != M3_OK) return s;
+    if (d->batch == 0) return M3_OK;
+    if (!ptrs_ok({h_in, h_out, q, k, v, beta, y}) || !opt_ptrs_ok({g})) return M3_ERR_INVALID_ARG;
+    m3_dims one = *d;
+    one.seqlen = 1;
+    DeltaParams p = delta_params(one, q, k, v, g, beta, scale, nullptr);
+    p.init_h = h_in;
+    p.y = y;
+    p.final_h = h_out;
+    return launch_delta_step(one, p, (cudaStream_t)stream) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+}
+
+struct DeltaBwdLayout {
+    int KB, nck;
+    size_t ckpt, part_qk, part_g, total;
+};
+
+static DeltaBwdLayout delta_bwd_layout(const m3_dims& d) {
+    DeltaBwdLayout l;
+    l.KB = delta_block_tokens(d);
+    l.nck = d.seqlen > 0 ? (int)(((long long)d.seqlen + l.KB - 1) / l.KB) : 0;
+    const size_t units = (size_t)d.batch * d.nheads, NP = (size_t)d.dstate * d.headdim;
+    const size_t toks = units * d.seqlen * delta_tiles(d);
+    size_t off = kWorkspaceHeaderBytes;
+    l.ckpt = off;    off = round256(off + units * l.nck * NP * sizeof(float));
+    l.part_qk = off; off = round256(off + toks * 2 * d.dstate * sizeof(float));
+    l.part_g = off;  off = round256(off + toks * 2 * sizeof(float));
+    l.total = off;
+    return l;
+}
+
+m3_status m3_delta_bwd_workspace_size(const m3_dims* d, size_t* bytes) {
+    if (!bytes) return M3_ERR_INVALID_ARG;
+    const m3_status s = check_delta(d, true);
+    if (s != M3_OK) return s;
+    *bytes = delta_bwd_layout(*d).total;
+    return M3_OK;
+}
+
+m3_status m3_delta_bwd(const m3_dims* d, const void* q, const void* k, const void* v, const float* g,
+                       const float* beta, float scale, const int* lengths, const float* init_h, const void* dy,
+                       const float* d_final_h, void* dq, void* dk, void* dv, void* dg, void* dbeta,
+                       float* d_init_h, void* workspace, size_t ws_bytes, void* stream) {
+    const NvtxRange range("m3_delta_bwd");
+    size_t need = 0;
+    const m3_status s = m3_delta_bwd_workspace_size(d, &need);
+    if (s != M3_OK) return s;
+    const bool work = d->batch > 0 && d->seqlen > 0;
+    if (work && !ptrs_ok({q, k, v, beta, dy, dq, dk, dv, dbeta})) return M3_ERR_INVALID_ARG;
+    if (!opt_ptrs_ok({g, lengths, init_h, d_final_h, dg, d_init_h})) return M3_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || ws_bytes < need) return M3_ERR_WORKSPACE;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (!work) return state_passthrough(*d, d_final_h, d_init_h, st);
+    const DeltaBwdLayout l = delta_bwd_layout(*d);
+    char* ws = static_cast<char*>(workspace);
+    DeltaParams p = delta_params(*d, q, k, v, g, beta, scale, lengths);
+    p.init_h = init_h;
+    p.dy = dy;
+    p.d_final_h = d_final_h;
+    p.dq = dq; p.dk = dk; p.dv = dv; p.dg = dg; p.dbeta = dbeta; p.d_init_h = d_init_h;
+    p.KB = l.KB;
+    p.nck = l.nck;
+    p.ckpt = reinterpret_cast<float*>(ws + l.ckpt);
+    p.part_qk = reinterpret_cast<float*>(ws + l.part_qk);
+    p.part_g = reinterpret_cast<float*>(ws + l.part_g);
+    return launch_delta_seq_bwd(*d, p, st) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+}
+
+// -------------------------------------------------- root-mean-square norm --
+static m3_status check_norm(long long rows, int width, int io_dtype) {
+    if (rows < 0 || width < 1 || (io_dtype != M3_F32 && io_dtype != M3_BF16)) return M3_ERR_INVALID_ARG;
+    if (rows > 0x7fffffffLL) return M3_ERR_UNSUPPORTED;
+    return M3_OK;
+}
+
+m3_status m3_rms_norm_fwd(long long rows, int width, int io_dtype, const void* x, const void* residual,
+                          const float* weight, float eps, void* sum, void* y, void* y8, float* scale,
+                          int scale_block, void* stream) {
+    const NvtxRange range("m3_rms_norm_fwd");
+    const m3_status s = check_norm(rows, width, io_dtype);
+    if (s != M3_OK) return s;
+    if (!(eps >= 0.f) || (!sum && !y && !y8) || (y8 && !scale && rows > 0)) return M3_ERR_INVALID_ARG;
+    if (y8 && scale_block != 0 && scale_block != 128) return M3_ERR_UNSUPPORTED;
+    if (rows == 0) return M3_OK;
+    if (!ptrs_ok({x}) || !opt_ptrs_ok({residual, weight, sum, y, y8, scale})) return M3_ERR_INVALID_ARG;
+    NormParams p;
+    memset(&p, 0, sizeof(p));
+    p.rows = rows; p.width = width; p.eps = eps;
+    p.x = x; p.residual = residual; p.weight = weight; p.sum = sum; p.y = y;
+    p.y8 = static_cast<uint8_t*>(y8); p.scale = scale; p.block = y8 ? scale_block : 0;
+    return launch_norm(io_dtype, p, (cudaStream_t)stream) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+}
+
+m3_status m3_rms_norm_bwd_workspace_size(long long rows, int width, int io_dtype, size_t* bytes) {
+    if (!bytes) return M3_ERR_INVALID_ARG;
+    const m3_status s = check_norm(rows, width, io_dtype);
+    if (s != M3_OK) return s;
+    *bytes = round256(kWorkspaceHeaderBytes + (size_t)norm_bwd_parts(rows, width, io_dtype) * width * sizeof(float));
+    return M3_OK;
+}
+
+m3_status m3_rms_norm_bwd(long long rows, int width, int io_dtype, const void* s_in, const float* weight, float eps,
+                          const void* dy, const void* d_sum, void* dx, float* dweight, void* workspace,
+                          size_t ws_bytes, void* stream) {
+    const NvtxRange range("m3_rms_norm_bwd");
+    size_t need = 0;
+    const m3_status s = m3_rms_norm_bwd_workspace_size(rows, width, io_dtype, &need);
+    if (s != M3_OK) return s;
+    if (!(eps >= 0.f)) return M3_ERR_INVALID_ARG;
+    if (rows > 0 && !ptrs_ok({s_in, dy, dx})) return M3_ERR_INVALID_ARG;
+    if (!opt_ptrs_ok({weight, d_sum, dweight})) return M3_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || ws_bytes < need) return M3_ERR_WORKSPACE;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (rows == 0) {
+        if (dweight && cudaMemsetAsync(dweight, 0, sizeof(float) * width, st) != cudaSuccess) return M3_ERR_CUDA;
+        return M3_OK;
+    }
+    NormParams p;
+    memset(&p, 0, sizeof(p));
+    p.rows = rows; p.width = width; p.eps = eps;
+    p.x = s_in; p.weight = weight; p.dy = dy; p.d_sum = d_sum; p.dx = dx; p.dweight = dweight;
+    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWorkspaceHeaderBytes);
+    p.parts = norm_bwd_parts(rows, width, io_dtype);
+    return launch_norm_bwd(io_dtype, p, st) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+}
+
 m3_status m3_debug_bounds_report(m3_bounds_report* out, int clear) {
     if (!out) return M3_ERR_INVALID_ARG;
     memset(out, 0, sizeof(*out));
@@ -637,7 +828,8 @@ m3_status m3_debug_bounds_report(m3_bounds_report* out, int clear) {
     // in file order (site = file * 1000 + check)
     const Take takes[] = {bounds_take_scan_tc, bounds_take_scan_simt, bounds_take_step,
                           bounds_take_rope,    bounds_take_seq,       bounds_take_bwd,
-                          bounds_take_phase,   bounds_take_scan_ws,   bounds_take_api};
+                          bounds_take_phase,   bounds_take_scan_ws,   bounds_take_delta,
+                          bounds_take_norm,    bounds_take_api};
     out->enabled = 1;
     if (cudaDeviceSynchronize() != cudaSuccess) return M3_ERR_CUDA;
     for (Take take : takes) {
