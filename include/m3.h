@@ -62,7 +62,8 @@
  * chunk) instead of the planner's choice; M3_TC_KERNEL=persistent runs the
  * tensor-core prefill on the persistent warp-specialised kernel (one CTA per
  * SM, tiles pipelined across roles) instead of the default tile kernel.
- * M3_SEQ_COLS=1|2 runs the transition variants with 1 or 2 state columns per
+ * M3_DELTA_PATH=token keeps the gated delta rule on its token-by-token
+ * kernels.  M3_SEQ_COLS=1|2 runs the transition variants with 1 or 2 state columns per
  * warp instead of 4 (for comparison; measured slower).
  * Buffer extents cannot be checked through plain pointers: every buffer must
  * hold at least the elements its layout gives for `dims` (nothing is read
@@ -324,7 +325,10 @@ m3_status m3_scan_fwd_reflect(const m3_dims* dims, const void* u,
  * b has lengths[b] tokens (values outside 0..seqlen count as the nearer bound):
  * its final state is the one after its last token, rows of y behind it are left
  * as they were, and gradients behind it are zero.
- * Arithmetic is float32. */
+ * Arithmetic is float32.  On bfloat16 layers with dstate 128 and headdim a
+ * multiple of 64 the prefill runs chunked on the tensor cores; its chain of
+ * states keeps float32 values as sums of bfloat16 parts (16 bits and more), and
+ * only products that end in y round an operand to bfloat16. */
 
 /* Bytes of device workspace m3_delta_fwd needs (host-only; at least 256: the
  * status word that m3_device_status reads). */
@@ -429,7 +433,7 @@ m3_status m3_selftest_bounded_wait(void* workspace, size_t workspace_bytes, void
  * (site = file * 1000 + check: 1 tile prefill, 2 SIMT prefill and segment
  * combine, 3 decode step, 4 rope, 5 transition variants, 6 backward,
  * 7 phase prologues, 8 persistent prefill, 9 this self-test, 10 delta rule,
- * 11 norm; for a span the
+ * 11 norm, 12 chunked delta rule; for a span the
  * index is its last element).  `clear` != 0 resets the records after reading.
  * M3_ERR_INVALID_ARG for a NULL `out`, M3_ERR_CUDA if the device cannot be
  * read.  Host call; the release build touches no device. */

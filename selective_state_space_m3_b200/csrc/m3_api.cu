@@ -26,6 +26,7 @@ cudaError_t bounds_take_bwd(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_phase(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_scan_ws(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_delta(BoundsRecord* out, bool clear);
+cudaError_t bounds_take_delta_tc(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_norm(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_api(BoundsRecord* out, bool clear);
 
@@ -644,6 +645,9 @@ static m3_status check_delta(const m3_dims* d, bool need_seq) {
     return M3_OK;
 }
 
+// whether the chunked tensor-core kernels take these dims
+static bool delta_chunked(const m3_dims& d) { return delta_tc_eligible(d) && !env_is("M3_DELTA_PATH", "token"); }
+
 static DeltaParams delta_params(const m3_dims& d, const void* q, const void* k, const void* v, const float* g,
                                 const float* beta, float scale, const int* lengths) {
     DeltaParams p;
@@ -687,7 +691,9 @@ m3_status m3_delta_fwd(const m3_dims* d, const void* q, const void* k, const voi
     p.init_h = init_h;
     p.y = y;
     p.final_h = final_h;
-    return launch_delta_seq(*d, p, st) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+    const cudaError_t e = delta_chunked(*d) ? launch_delta_tc(*d, p, static_cast<int*>(workspace), st)
+                                            : launch_delta_seq(*d, p, st);
+    return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }
 
 m3_status m3_delta_step(const m3_dims* d, const float* h_in, float* h_out, const void* q, const void* k,
@@ -829,7 +835,7 @@ m3_status m3_debug_bounds_report(m3_bounds_report* out, int clear) {
     const Take takes[] = {bounds_take_scan_tc, bounds_take_scan_simt, bounds_take_step,
                           bounds_take_rope,    bounds_take_seq,       bounds_take_bwd,
                           bounds_take_phase,   bounds_take_scan_ws,   bounds_take_delta,
-                          bounds_take_norm,    bounds_take_api};
+                          bounds_take_delta_tc, bounds_take_norm,    bounds_take_api};
     out->enabled = 1;
     if (cudaDeviceSynchronize() != cudaSuccess) return M3_ERR_CUDA;
     for (Take take : takes) {

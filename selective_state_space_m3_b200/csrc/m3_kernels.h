@@ -159,6 +159,10 @@ int delta_block_tokens(const m3_dims& d);
 int delta_tiles(const m3_dims& d);
 cudaError_t launch_delta_seq(const m3_dims& d, const DeltaParams& q, cudaStream_t st);
 cudaError_t launch_delta_seq_bwd(const m3_dims& d, const DeltaParams& q, cudaStream_t st);
+// chunked prefill on the tensor cores (bf16, N = 128, P a multiple of 64);
+// `status` is the workspace status word its bounded waits report to
+bool delta_tc_eligible(const m3_dims& d);
+cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st);
 cudaError_t launch_delta_step(const m3_dims& d, const DeltaParams& q, cudaStream_t st);
 
 // root-mean-square norm (k_norm.cu)
