@@ -14,12 +14,16 @@
 //   warp 0       one lane issues the chain's tcgen05.mma
 //   warps 1-8    the chain's arithmetic: S lives in registers in float32 (a
 //                thread has one state row and 32 columns)
-//   warps 9-12   up to two chunks ahead: gates, K K^T and Q K^T (one product of
-//                the stacked rows [K; Q] with K), T and the masked Q K^T
-//   warp 13      one lane issues the TMA loads (three chunks of K, Q, two of V)
+//   warps 9-16   two groups, every other chunk each, up to two chunks ahead:
+//                gates, K K^T and Q K^T (one product of the stacked rows
+//                [K; Q] with K), T and the masked Q K^T
+//   warp 17      one lane issues the TMA loads (three chunks of K, Q, two of V)
 // Every product has M = 128 rows: [K; Q] against S gives K S and Q S at once,
 // and the tile [T - I; P] (P = scale Gam o Q K^T) serves both T R (upper half
 // of the accumulator) and P U (lower half); the unused half is never read.
+// The parts of a split operand stand side by side as columns of one product
+// (a 128 x 128 x 16 product takes 64 cycles, a 128 x 64 x 16 one 47) and the
+// epilogue adds the columns.
 //
 // Precision.  K, Q, V are bfloat16 and enter the products as they are.  The
 // chain keeps float32: S, R, U and T are split into bfloat16 parts (hi + lo, 16
@@ -31,13 +35,15 @@
 //
 // Shared memory (KB): K, Q 3 x 32, V 2 x 8, S hi/lo 32 (R and U take its place
 // between the first product's end and the new state), [T - I; P] 2 x 16, T lo
-// 2 x 8, scratch 16.5, gates 4: one CTA an SM.
+// 2 x 8, scratch 2 x 12, gates 6: one CTA an SM.
 //
 // Every wait on an mbarrier is bounded (1 s); on expiry the kernel records
 // M3_ERR_DEVICE_TIMEOUT in the workspace status word and runs out without
 // further waiting.
 #define M3_BOUNDS_FILE 12
 #include "m3_bounds.cuh"
+#include <stdlib.h>
+
 #include "m3_kernels.h"
 #include "tc_ptx.cuh"
 
@@ -51,40 +57,42 @@ using namespace ptx;
 
 constexpr int kC = 64;             // tokens a chunk
 constexpr int kN = 128;
-constexpr int kP = 64;             // columns a CTA
+constexpr int kP = 64;             // columns of a V tile; a CTA takes PC = 64, 32 or 16 of them
 constexpr int kState = 256;        // threads of the chain
-constexpr int kPrep = 128;
-constexpr int kThreads = 32 + kState + kPrep + 32;
-constexpr int kCols = 32;          // state columns a thread
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kPrep = 128;         // threads of one of the two groups that make T
+constexpr int kThreads = 32 + kState + 2 * kPrep + 32;
 constexpr unsigned kFull = 0xffffffffu;
 
 constexpr int OFF_KQ = 0;                       // 3 x 32 KB: two 64-column atoms, rows 0..63 K, 64..127 Q
 constexpr int OFF_V = OFF_KQ + 3 * 32768;       // 2 x 8 KB
 constexpr int OFF_S = OFF_V + 2 * 8192;         // S hi, S lo (16 KB each: rows n, 64 p)
-constexpr int OFF_UH = OFF_S;                   // R hi, then e^{G_C-G} U hi (8 KB: rows t, 64 p)
-constexpr int OFF_UL = OFF_S + 8192;            // R lo, then its lo part
-constexpr int OFF_UB = OFF_S + 16384;           // U rounded, for P U
-constexpr int OFF_UM = OFF_S + 24576;           // third part of e^{G_C-G} U
+constexpr int OFF_U = OFF_S;                    // R hi, lo; then e^{G_C-G} U in three parts (8 KB each: rows t, 64 p)
+constexpr int OFF_UB = OFF_S + 24576;           // U rounded, for P U
 constexpr int OFF_X = OFF_S + 32768;            // 2 x 16 KB: [T - I hi; P]
 constexpr int OFF_TL = OFF_X + 2 * 16384;       // 2 x 8 KB: T - I lo (its operand reads 64 more rows, unused)
-constexpr int OFF_SCR = OFF_TL + 2 * 8192;      // A11 / T11, A22 / A21 T11, A21 (4 KB each), T22 (4.5 KB)
-constexpr int SCR_BYTES = 3 * 4096 + 32 * 36 * 4;
-constexpr int OFF_MISC = OFF_SCR + SCR_BYTES;
+constexpr int OFF_SCR = OFF_TL + 2 * 8192;      // of each group: A11 / T11, A22 / T22, A21 / A21 T11 (4 KB each)
+constexpr int SCR_BYTES = 3 * 4096;
+constexpr int OFF_MISC = OFF_SCR + 2 * SCR_BYTES;
+
+// TMEM columns: K S, Q S against [S hi | S lo] and, once they are read, the
+// state's update in three parts; T R against [R hi | R lo] and, once read, P U;
+// one Gram product a group
+constexpr uint32_t D_KS = 0, D_S = 0, D_TR = 192, D_G = 320;
 
 struct Gates {
-    float hi[kC], lo[kC];          // G in log2 units, as a sum of two floats
+    float2 G[kC];                  // sum of g in log2 units, as a sum of two floats
     float a[kC], at[kC], beta[kC]; // e^G, e^{G_C - G}, beta (0 behind the end)
+    float mid[kC];                 // j < 32: e^{G_31 - G_j}; i >= 32: e^{G_i - G_31}
     float whole;                   // e^{G_C}
     float pad[3];
 };
 
 struct Misc {
-    uint64_t kq_full[3], kq_free[3], v_full[2], v_free[2], t_full[2], x_free[2];
-    uint64_t s_ready, ks, r, tr, u, s, o, g, drain_a, drain_b;
+    uint64_t kq_full[3], kq_free[3], v_full[2], v_free[2], t_full[2], x_free[2], g[2];
+    uint64_t s_ready, ks, r, tr, u, s, o, drain[3];
     uint32_t tmem_base;
     int abort_flag, drain_flag, pad;
-    Gates gates[3];
+    Gates gates[4];
 };
 constexpr int SMEM_BYTES = OFF_MISC + (int)sizeof(Misc) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory of the delta kernel");
@@ -92,37 +100,62 @@ static_assert(SMEM_BYTES <= 232448, "shared memory of the delta kernel");
 __device__ __forceinline__ bool wait(uint64_t* b, int phase, Misc* m, int* status, int where) {
     return mbar_wait_flag(b, (uint32_t)(phase & 1), &m->abort_flag, status, where);
 }
-__device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kPrep) : "memory"); }
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, %1;" ::"r"(2 + group), "n"(kPrep) : "memory"); }
 __device__ __forceinline__ float clamp_g(float g) { return g < -1.0e4f ? -1.0e4f : g; }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
-// 8 floats -> 8 bfloat16 (returned), f becomes what the rounding left
-__device__ __forceinline__ uint4 take_bf16(float* f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        w[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
-        f[2 * j] -= __uint_as_float(w[j] << 16);
-        f[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+// Products and commits by one elected lane of a converged warp: the warp runs
+// the loop as one, so that descriptors stay in uniform registers (measured:
+// 47 cycles a 128 x 64 x 16 product instead of 97 from a divergent lane).
+__device__ __forceinline__ void umma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
 }
-__device__ __forceinline__ void put16(uint8_t* smem, int off, int row, int chunk, int limit, uint4 v) {
-    if (M3_SPAN(1, sw128(row, chunk), 16, limit)) *reinterpret_cast<uint4*>(smem + off + sw128(row, chunk)) = v;
+__device__ __forceinline__ void commit_one(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(su32(bar))
+        : "memory");
 }
-__device__ __forceinline__ void put2(uint8_t* smem, int off, int row, int col, float v) {
-    if (M3_IN(2, row * 64 + col, 4096))
-        *reinterpret_cast<__nv_bfloat16*>(smem + off + sw128(row, col >> 3) + (col & 7) * 2) = __float2bfloat16_rn(v);
+
+// two floats -> two bfloat16 (returned), f becomes what the rounding left
+__device__ __forceinline__ uint32_t take2(float2& f) {
+    const uint32_t w = pack_bf16x2(f.x, f.y);
+    f = __ffma2_rn(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), make_float2(-1.f, -1.f), f);
+    return w;
+}
+__device__ __forceinline__ uint4 take8(float2* f) {
+    return make_uint4(take2(f[0]), take2(f[1]), take2(f[2]), take2(f[3]));
+}
+__device__ __forceinline__ uint4 round8(const float2* f) {
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                      pack_bf16x2(f[3].x, f[3].y));
+}
+// 16 bytes at `off` of the tile that starts at `tile` and has `limit` bytes
+__device__ __forceinline__ void put16(uint8_t* smem, int tile, uint32_t off, int limit, uint4 v) {
+    if (M3_SPAN(1, off, 16, limit)) *reinterpret_cast<uint4*>(smem + tile + off) = v;
 }
 
 struct Where {
-    int b, h, g, p0, len, nch;
+    int b, h, g, p0, len, nch;     // p0: first column of the CTA
 };
 
+template <int PC>
 __device__ __forceinline__ Where where_am_i(const DeltaParams& q) {
     Where w;
-    const int slices = q.headdim / kP;
+    const int slices = q.headdim / PC;
     const int bh = blockIdx.x / slices;
-    w.p0 = (blockIdx.x % slices) * kP;
+    w.p0 = (blockIdx.x % slices) * PC;
     w.b = bh / q.nheads;
     w.h = bh % q.nheads;
     w.g = w.h / (q.nheads / q.ngroups);
@@ -133,65 +166,213 @@ __device__ __forceinline__ Where where_am_i(const DeltaParams& q) {
     return w;
 }
 
-// Gates of chunk c: lane l of every prep warp holds tokens 2 l and 2 l + 1; the
-// sum runs in double, so that differences of G keep float32 accuracy after
-// strong decay.  Warp `pw` 0 writes.
-__device__ __forceinline__ void make_gates(const DeltaParams& q, const Where& w, int c, Gates* out, bool write) {
+// a + b of sums of two floats (each a pair with a small second part)
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+    const float s = a.x + b.x, t = s - a.x;
+    const float e = (a.x - (s - t)) + (b.x - t) + (a.y + b.y);
+    const float r = s + e;
+    return make_float2(r, e - (r - s));
+}
+__device__ __forceinline__ float diff_pair(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); }
+
+// g and beta of a chunk: lane l holds tokens 2 l and 2 l + 1
+struct Raw {
+    float g[2], beta[2];
+};
+__device__ __forceinline__ Raw load_raw(const DeltaParams& q, const Where& w, int c) {
     const int lane = threadIdx.x & 31;
-    float gv[2], bv[2];
+    Raw r;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int t = c * kC + 2 * lane + j;
         const size_t o = ((size_t)w.b * q.seqlen + t) * q.nheads + w.h;
         const bool ok = t < w.len && M3_IN(4, o, (long long)q.batch * q.seqlen * q.nheads);
-        gv[j] = (ok && q.g) ? clamp_g(__ldg(q.g + o)) : 0.f;
-        bv[j] = ok ? __ldg(q.beta + o) : 0.f;
+        r.g[j] = (ok && q.g) ? __ldg(q.g + o) : 0.f;
+        r.beta[j] = ok ? __ldg(q.beta + o) : 0.f;
     }
-    const double l2e = 1.4426950408889634074;
-    double d0 = gv[0] * l2e, d1 = d0 + gv[1] * l2e, sum = d1;
+    return r;
+}
+// Sums of g in log2 units.  They run as pairs of floats, so that differences
+// keep float32 accuracy after strong decay.
+__device__ __forceinline__ void make_gates(const Raw& raw, Gates* out) {
+    const int lane = threadIdx.x & 31;
+    constexpr float kHi = 1.44269502162933349609f, kLo = 1.92596299112661746887e-8f;    // log2 e
+    float2 d[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const float g = clamp_g(raw.g[j]);
+        const float p = g * kHi;
+        d[j] = make_float2(p, fmaf(g, kHi, -p) + g * kLo);
+    }
+    float2 sum = add_pair(d[0], d[1]);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double u = __shfl_up_sync(kFull, sum, o);
-        if (lane >= o) sum += u;
+        const float2 u = make_float2(__shfl_up_sync(kFull, sum.x, o), __shfl_up_sync(kFull, sum.y, o));
+        if (lane >= o) sum = add_pair(sum, u);
     }
-    const double total = __shfl_sync(kFull, sum, 31);
-    const double G[2] = {sum - d1 + d0, sum};
-    if (write) {
+    const float2 total = make_float2(__shfl_sync(kFull, sum.x, 31), __shfl_sync(kFull, sum.y, 31));
+    const float2 mid = make_float2(__shfl_sync(kFull, sum.x, 15), __shfl_sync(kFull, sum.y, 15));
+    const float2 G[2] = {add_pair(sum, make_float2(-d[1].x, -d[1].y)), sum};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int i = 2 * lane + j;
-            const float hi = (float)G[j];
-            out->hi[i] = hi;
-            out->lo[i] = (float)(G[j] - (double)hi);
-            out->a[i] = exp2f(hi);
-            out->at[i] = exp2f((float)(total - G[j]));
-            out->beta[i] = bv[j];
-        }
-        if (lane == 0) out->whole = exp2f((float)total);
+    for (int j = 0; j < 2; ++j) {
+        const int i = 2 * lane + j;
+        out->G[i] = G[j];
+        out->a[i] = ex2(G[j].x + G[j].y);
+        out->at[i] = ex2(diff_pair(total, G[j]));
+        out->beta[i] = raw.beta[j];
+        out->mid[i] = ex2(i < 32 ? diff_pair(mid, G[j]) : diff_pair(G[j], mid));
     }
+    if (lane == 0) out->whole = ex2(total.x + total.y);
 }
 
 // column `lane` of the inverse of a unit lower triangular 32 x 32 matrix whose
 // strict lower part is at[col * 32 + row]: x starts as the unit vector, and a
 // finished x_i takes A_ri x_i off every later x_r
-__device__ __forceinline__ void invert32(const float* at, float* x) {
+__device__ __forceinline__ void invert32(const float* at, float2* x) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = i == lane ? 1.f : 0.f;
+    for (int i = 0; i < 16; ++i) x[i] = make_float2(2 * i == lane ? 1.f : 0.f, 2 * i + 1 == lane ? 1.f : 0.f);
 #pragma unroll
     for (int i = 0; i < 31; ++i) {
-        const float xi = -x[i];
+        const float xi = (i & 1) ? -x[i >> 1].y : -x[i >> 1].x;
+        const float2 x2 = make_float2(xi, xi);
 #pragma unroll
         for (int r4 = (i + 1) / 4; r4 < 8; ++r4) {
             const float4 v = *reinterpret_cast<const float4*>(at + i * 32 + 4 * r4);
-            const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (4 * r4 + j > i) x[4 * r4 + j] = fmaf(e[j], xi, x[4 * r4 + j]);
+            // rows up to i are finished: the strict upper part and the diagonal
+            // of `at` hold zeros, so they stay
+            if (4 * r4 + 1 > i) x[2 * r4] = __ffma2_rn(make_float2(v.x, v.y), x2, x[2 * r4]);
+            x[2 * r4 + 1] = __ffma2_rn(make_float2(v.z, v.w), x2, x[2 * r4 + 1]);
         }
     }
 }
 
+// 8 rows r0.. of (left, columns contiguous) x (right, rows contiguous) at column
+// `lane`; SW: the left matrix is stored with its 16-byte blocks exchanged
+template <bool SW>
+__device__ __forceinline__ void product32(const float* left, const float* right, int r0, float2* acc) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < 32; ++k) {
+        const float t = right[k * 32 + lane];
+        const float2 t2 = make_float2(t, t);
+        const int b0 = r0 >> 2, sw = SW ? (k & 7) : 0;
+        const float4 u = *reinterpret_cast<const float4*>(left + k * 32 + ((b0 ^ sw) << 2));
+        const float4 v = *reinterpret_cast<const float4*>(left + k * 32 + (((b0 + 1) ^ sw) << 2));
+        acc[0] = __ffma2_rn(make_float2(u.x, u.y), t2, acc[0]);
+        acc[1] = __ffma2_rn(make_float2(u.z, u.w), t2, acc[1]);
+        acc[2] = __ffma2_rn(make_float2(v.x, v.y), t2, acc[2]);
+        acc[3] = __ffma2_rn(make_float2(v.z, v.w), t2, acc[3]);
+    }
+}
+
+// NP loads of W consecutive columns (32 lanes, thread = lane), `step` columns
+// apart, issued back to back with one wait; their sum
+template <int W, int NP> __device__ __forceinline__ void tmem_sum(uint32_t t, uint32_t step, float2* f);
+template <> __device__ __forceinline__ void tmem_sum<8, 1>(uint32_t t, uint32_t step, float2* f) {
+    uint32_t r[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(t + 0)
+        : "memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+    }
+}
+template <> __device__ __forceinline__ void tmem_sum<8, 2>(uint32_t t, uint32_t step, float2* f) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t + 0), "r"(t + 1 * step)
+        : "memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        f[j] = __fadd2_rn(f[j], make_float2(__uint_as_float(r[8 + 2 * j]), __uint_as_float(r[9 + 2 * j])));
+    }
+}
+template <> __device__ __forceinline__ void tmem_sum<8, 3>(uint32_t t, uint32_t step, float2* f) {
+    uint32_t r[24];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%24];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%25];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%26];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23])
+        : "r"(t + 0), "r"(t + 1 * step), "r"(t + 2 * step)
+        : "memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        f[j] = __fadd2_rn(f[j], __fadd2_rn(make_float2(__uint_as_float(r[8 + 2 * j]), __uint_as_float(r[9 + 2 * j])),
+                                           make_float2(__uint_as_float(r[16 + 2 * j]), __uint_as_float(r[17 + 2 * j]))));
+    }
+}
+template <> __device__ __forceinline__ void tmem_sum<16, 1>(uint32_t t, uint32_t step, float2* f) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t + 0)
+        : "memory");
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        f[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+    }
+}
+template <> __device__ __forceinline__ void tmem_sum<16, 2>(uint32_t t, uint32_t step, float2* f) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(t + 0), "r"(t + 1 * step)
+        : "memory");
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        f[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        f[j] = __fadd2_rn(f[j], make_float2(__uint_as_float(r[16 + 2 * j]), __uint_as_float(r[17 + 2 * j])));
+    }
+}
+template <> __device__ __forceinline__ void tmem_sum<16, 3>(uint32_t t, uint32_t step, float2* f) {
+    uint32_t r[48];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%48];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%49];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%50];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47])
+        : "r"(t + 0), "r"(t + 1 * step), "r"(t + 2 * step)
+        : "memory");
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        f[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        f[j] = __fadd2_rn(f[j], __fadd2_rn(make_float2(__uint_as_float(r[16 + 2 * j]), __uint_as_float(r[17 + 2 * j])),
+                                           make_float2(__uint_as_float(r[32 + 2 * j]), __uint_as_float(r[33 + 2 * j]))));
+    }
+}
+
+// Split operands.  A row of a tile has 128 bytes, 64 bfloat16 columns; the parts
+// of an operand stand side by side, PC columns each, and go on in further tiles
+// (16 KB for 128 rows, 8 KB for 64).  Byte offset of part `part`, 16-byte
+// column group `ch` (PC / 8 a part) of row `row`:
+template <int PC>
+__device__ __forceinline__ uint32_t part_at(int row, int part, int ch, int tile_bytes) {
+    const int col = part * (PC / 8) + ch;
+    return (uint32_t)((col >> 3) * tile_bytes) + sw128(row, col & 7);
+}
+
+template <int PC>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmV, DeltaParams q, int* status) {
@@ -200,29 +381,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     Misc* m = reinterpret_cast<Misc*>(smem + OFF_MISC);
     const uint32_t sbase = su32(smem);
     if (!M3_SPAN(5, smem - smem_raw, OFF_MISC + (int)sizeof(Misc), dyn_smem_bytes())) return;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Where w = where_am_i(q);
+    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
+    const Where w = where_am_i<PC>(q);
+    constexpr int kCols = PC / 2;                  // state columns a thread
+    constexpr int W = kCols < 16 ? kCols : 16;     // columns of a TMEM load
+    constexpr int NH = kCols / W, NG = kCols / 8;  // loads; 16-byte groups
     const int P = q.headdim;
     const size_t bh = (size_t)w.b * q.nheads + w.h;
 
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i) { mbar_init(&m->kq_full[i], 1); mbar_init(&m->kq_free[i], 1); }
+        for (int i = 0; i < 3; ++i) { mbar_init(&m->kq_full[i], 1); mbar_init(&m->kq_free[i], 1); mbar_init(&m->drain[i], 1); }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m->v_full[i], 1);
             mbar_init(&m->v_free[i], kState / 2);
             mbar_init(&m->t_full[i], kPrep);
             mbar_init(&m->x_free[i], 1);
+            mbar_init(&m->g[i], 1);
         }
         mbar_init(&m->s_ready, kState);
         mbar_init(&m->ks, 1);
-        mbar_init(&m->r, kState / 2);
+        mbar_init(&m->r, kState);
         mbar_init(&m->tr, 1);
         mbar_init(&m->u, kState);
         mbar_init(&m->s, 1);
         mbar_init(&m->o, 1);
-        mbar_init(&m->g, 1);
-        mbar_init(&m->drain_a, 1);
-        mbar_init(&m->drain_b, 1);
         m->abort_flag = 0;
         m->drain_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -235,121 +417,127 @@ __global__ void __launch_bounds__(kThreads, 1)
     // T - I is lower triangular: its upper right blocks stay zero
     for (int e = tid; e < 2 * 32 * 4; e += kThreads) {
         const int buf = e >> 7, row = (e >> 2) & 31, ch = 4 + (e & 3);
-        put16(smem, OFF_X + buf * 16384, row, ch, 16384, make_uint4(0u, 0u, 0u, 0u));
-        put16(smem, OFF_TL + buf * 8192, row, ch, 8192, make_uint4(0u, 0u, 0u, 0u));
+        put16(smem, OFF_X + buf * 16384, sw128(row, ch), 16384, make_uint4(0u, 0u, 0u, 0u));
+        put16(smem, OFF_TL + buf * 8192, sw128(row, ch), 8192, make_uint4(0u, 0u, 0u, 0u));
     }
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem_base;
-    const uint32_t d_ks = tmem, d_tr = tmem + 64, d_s = tmem + 128, d_o = tmem + 192, d_g = tmem + 256;
 
     if (warp == 0) {
         // ------------------------------------------------ the chain's products
-        if (lane == 0) {
-            constexpr uint32_t idKS = idesc_bf16(128, 64, 0, 1);     // A K-major, B MN-major
-            constexpr uint32_t idT = idesc_bf16(128, 64, 1, 1);      // A MN-major (K^T), B MN-major
-            for (int c = 0; c < w.nch; ++c) {
-                const uint32_t kq = sbase + OFF_KQ + (c % 3) * 32768, x = sbase + OFF_X + (c & 1) * 16384;
-                const uint32_t tl = sbase + OFF_TL + (c & 1) * 8192;
-                wait(&m->kq_full[c % 3], c / 3, m, status, 1);
-                // a chunk that ends behind the sequence: its K rows are cleaned by
-                // the prep warps before they hand over T
-                if ((c + 1) * kC > w.len) wait(&m->t_full[c & 1], c >> 1, m, status, 2);
-                wait(&m->s_ready, c, m, status, 3);
-                tc_fence_after();
-                for (int part = 0; part < 2; ++part)
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma(d_ks, sdesc(kq + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
-                             sdesc(sbase + OFF_S + part * 16384 + kk * 2048, 8192, 1024), idKS, part + kk > 0);
-                umma_commit(&m->ks);
-                wait(&m->t_full[c & 1], c >> 1, m, status, 4);
-                wait(&m->r, c, m, status, 5);
-                tc_fence_after();
-                for (int part = 0; part < 3; ++part)
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma(d_tr, sdesc((part < 2 ? x : tl) + kk * 32, 16, 1024),
-                             sdesc(sbase + (part == 1 ? OFF_UL : OFF_UH) + kk * 2048, 8192, 1024), idKS, part + kk > 0);
-                umma_commit(&m->tr);
-                wait(&m->u, c, m, status, 6);
-                tc_fence_after();
-                for (int part = 0; part < 3; ++part)
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma(d_s, sdesc(kq + kk * 2048, 16384, 1024),
-                             sdesc(sbase + (part == 0 ? OFF_UH : part == 1 ? OFF_UL : OFF_UM) + kk * 2048, 8192, 1024),
-                             idT, part + kk > 0);
-                umma_commit(&m->s);
-                for (int kk = 0; kk < 4; ++kk)
-                    umma(d_o, sdesc(x + kk * 32, 16, 1024), sdesc(sbase + OFF_UB + kk * 2048, 8192, 1024), idKS, kk > 0);
-                umma_commit(&m->o);
-                umma_commit(&m->kq_free[c % 3]);
-                umma_commit(&m->x_free[c & 1]);
-            }
-            umma_commit(&m->drain_a);
-            mbar_wait_flag(&m->drain_a, 0, &m->drain_flag, nullptr, 0);
+        // (descriptor starts count 16 bytes)
+        constexpr uint32_t idKS = idesc_bf16(128, 2 * PC, 0, 1);   // A K-major, B MN-major
+        constexpr uint32_t idTl = idesc_bf16(128, PC, 0, 1);
+        constexpr uint32_t idS = idesc_bf16(128, 3 * PC, 1, 1);    // A MN-major (K^T)
+        const uint64_t bS = sdesc(sbase + OFF_S, 16384, 1024), bU = sdesc(sbase + OFF_U, 8192, 1024);
+        const uint64_t bUB = sdesc(sbase + OFF_UB, 8192, 1024);
+        for (int c = 0; c < w.nch; ++c) {
+            const uint32_t kq = sbase + OFF_KQ + (c % 3) * 32768;
+            const uint64_t aKQ = sdesc(kq, 16, 1024), aKT = sdesc(kq, 16384, 1024);
+            const uint64_t aX = sdesc(sbase + OFF_X + (c & 1) * 16384, 16, 1024);
+            const uint64_t aTL = sdesc(sbase + OFF_TL + (c & 1) * 8192, 16, 1024);
+            wait(&m->kq_full[c % 3], c / 3, m, status, 1);
+            // a chunk that ends behind the sequence: its K rows are cleaned by
+            // the group that hands over T
+            if ((c + 1) * kC > w.len) wait(&m->t_full[c & 1], c >> 1, m, status, 2);
+            wait(&m->s_ready, c, m, status, 3);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                umma_one(tmem + D_KS, aKQ + (kk >> 2) * 1024 + (kk & 3) * 2, bS + kk * 128, idKS, kk > 0);
+            commit_one(&m->ks);
+            wait(&m->t_full[c & 1], c >> 1, m, status, 4);
+            wait(&m->r, c, m, status, 5);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_TR, aX + kk * 2, bU + kk * 128, idKS, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_TR, aTL + kk * 2, bU + kk * 128, idTl, 1);
+            commit_one(&m->tr);
+            wait(&m->u, c, m, status, 6);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_S, aKT + kk * 128, bU + kk * 128, idS, kk > 0);
+            commit_one(&m->s);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_TR + PC, aX + kk * 2, bUB + kk * 128, idTl, kk > 0);
+            commit_one(&m->o);
+            commit_one(&m->kq_free[c % 3]);
+            commit_one(&m->x_free[c & 1]);
         }
+        commit_one(&m->drain[2]);
+        mbar_wait_flag(&m->drain[2], 0, &m->drain_flag, nullptr, 0);
         __syncwarp();
     } else if (warp <= 8) {
         // ---------------------------------------------- the chain's arithmetic
         const int wk = tid - 32, wg = wk >> 7, quarter = warp & 3, row = quarter * 32 + lane, c0 = wg * kCols;
-        const uint32_t tl = (uint32_t)(quarter * 32) << 16;
-        const bool top = row < 64;                 // holds a token's K S and U; else its Q S and y
-        const int tok = row & 63;
-        const long long ext_h = (long long)q.batch * q.nheads * kN * P;
+        const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
+        const bool top = quarter < 2;              // holds a token's K S and U; else its Q S and y
+        const int tok = row & 63, ch0 = c0 / 8, vch = (w.p0 & 63) / 8 + ch0;
+        [[maybe_unused]] const long long ext_h = (long long)q.batch * q.nheads * kN * P;
         const size_t ho = (bh * kN + row) * P + w.p0 + c0;
-        float S[kCols];
+        float2 S[kCols / 2];
 #pragma unroll
         for (int c4 = 0; c4 < kCols / 4; ++c4) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (q.init_h && M3_SPAN(6, ho + 4 * c4, 4, ext_h)) v = *reinterpret_cast<const float4*>(q.init_h + ho + 4 * c4);
-            S[4 * c4] = v.x; S[4 * c4 + 1] = v.y; S[4 * c4 + 2] = v.z; S[4 * c4 + 3] = v.w;
+            S[2 * c4] = make_float2(v.x, v.y);
+            S[2 * c4 + 1] = make_float2(v.z, v.w);
         }
         auto store_state = [&]() {                 // S hi, S lo
 #pragma unroll
-            for (int ch = 0; ch < kCols / 8; ++ch) {
-                float f[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = S[8 * ch + j];
-                put16(smem, OFF_S, row, c0 / 8 + ch, 16384, take_bf16(f));
-                put16(smem, OFF_S + 16384, row, c0 / 8 + ch, 16384, take_bf16(f));
+            for (int ch = 0; ch < NG; ++ch) {
+                float2 f[4] = {S[4 * ch], S[4 * ch + 1], S[4 * ch + 2], S[4 * ch + 3]};
+                put16(smem, OFF_S, part_at<PC>(row, 0, ch0 + ch, 16384), 32768, take8(f));
+                put16(smem, OFF_S, part_at<PC>(row, 1, ch0 + ch, 16384), 32768, round8(f));
             }
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(&m->s_ready);
         };
         if (w.nch > 0) store_state();
+#pragma unroll 1
         for (int c = 0; c < w.nch; ++c) {
-            const Gates* gt = &m->gates[c % 3];
-            float buf[kCols];                      // top: R, then U; else Q S
+            const Gates* gt = &m->gates[c & 3];
+            float2 buf[kCols / 2];                 // top: beta V, R, then U; else Q S
             if (top) {
-                // this token's V, ahead of K S
-                uint4 vv[kCols / 8];
                 wait(&m->v_full[c & 1], c >> 1, m, status, 10);
-#pragma unroll
-                for (int ch = 0; ch < kCols / 8; ++ch) {
-                    const uint32_t o = sw128(tok, c0 / 8 + ch);
-                    vv[ch] = M3_SPAN(7, o, 16, 8192) ? *reinterpret_cast<const uint4*>(smem + OFF_V + (c & 1) * 8192 + o)
-                                                     : make_uint4(0u, 0u, 0u, 0u);
-                }
                 wait(&m->t_full[c & 1], c >> 1, m, status, 11);
-                const float be = gt->beta[tok], ba = -be * gt->a[tok];
+                const float be = gt->beta[tok], ba = -be * gt->a[tok], at = gt->at[tok];
                 const bool in = c * kC + tok < w.len;
+                const float2 be2 = make_float2(be, be), ba2 = make_float2(ba, ba), at2 = make_float2(at, at);
+                // beta V; rows behind the end (other data, possibly not numbers) count as zero
+#pragma unroll
+                for (int ch = 0; ch < NG; ++ch) {
+                    const uint32_t o = sw128(tok, vch + ch);
+                    uint4 vv = make_uint4(0u, 0u, 0u, 0u);
+                    if (in && M3_SPAN(7, o, 16, 8192)) vv = *reinterpret_cast<const uint4*>(smem + OFF_V + (c & 1) * 8192 + o);
+                    const uint32_t u[4] = {vv.x, vv.y, vv.z, vv.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        buf[4 * ch + j] = __fmul2_rn(be2, make_float2(__uint_as_float(u[j] << 16),
+                                                                      __uint_as_float(u[j] & 0xffff0000u)));
+                }
                 wait(&m->ks, c, m, status, 12);
+                __syncwarp();
                 tc_fence_after();
-                tmem_ld32(d_ks + tl + c0, buf);
 #pragma unroll
-                for (int ch = 0; ch < kCols / 8; ++ch) {
-                    const uint32_t u[4] = {vv[ch].x, vv[ch].y, vv[ch].z, vv[ch].w};
-                    float f[8];
+                for (int hh = 0; hh < NH; ++hh) {
+                    float2 d[W / 2];
+                    tmem_sum<W, 2>(tl + D_KS + W * hh, PC, d);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float v = __uint_as_float((j & 1) ? (u[j >> 1] & 0xffff0000u) : (u[j >> 1] << 16));
-                        buf[8 * ch + j] = in ? fmaf(ba, buf[8 * ch + j], be * v) : 0.f;
-                        f[j] = buf[8 * ch + j];
+                    for (int j = 0; j < W / 2; ++j) d[j] = buf[W / 2 * hh + j] = __ffma2_rn(ba2, d[j], buf[W / 2 * hh + j]);
+#pragma unroll
+                    for (int ch = 0; ch < W / 8; ++ch) {
+                        put16(smem, OFF_U, part_at<PC>(tok, 0, ch0 + W / 8 * hh + ch, 8192), 24576, take8(d + 4 * ch));
+                        put16(smem, OFF_U, part_at<PC>(tok, 1, ch0 + W / 8 * hh + ch, 8192), 24576, round8(d + 4 * ch));
                     }
-                    put16(smem, OFF_UH, tok, c0 / 8 + ch, 8192, take_bf16(f));
-                    put16(smem, OFF_UL, tok, c0 / 8 + ch, 8192, take_bf16(f));
                 }
                 fence_async_smem();
                 tc_fence_before();
@@ -357,61 +545,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // V is free only now: R, which is stored, shows that it has been read
                 // (an arrival right behind the loads let the next V overtake them)
                 mbar_arrive(&m->v_free[c & 1]);
-                const float at = gt->at[tok];
                 wait(&m->tr, c, m, status, 13);
+                __syncwarp();
                 tc_fence_after();
-                float d[kCols];
-                tmem_ld32(d_tr + tl + c0, d);
 #pragma unroll
-                for (int ch = 0; ch < kCols / 8; ++ch) {
-                    float f[8], e[8];
+                for (int hh = 0; hh < NH; ++hh) {
+                    float2 f[W / 2];
+                    tmem_sum<W, 2>(tl + D_TR + W * hh, PC, f);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        f[j] = buf[8 * ch + j] + d[8 * ch + j];
-                        e[j] = at * f[j];
+                    for (int j = 0; j < W / 2; ++j) f[j] = __fadd2_rn(f[j], buf[W / 2 * hh + j]);
+#pragma unroll
+                    for (int ch = 0; ch < W / 8; ++ch) {
+                        const int cc = ch0 + W / 8 * hh + ch;
+                        put16(smem, OFF_UB, sw128(tok, cc), 8192, round8(f + 4 * ch));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) f[4 * ch + j] = __fmul2_rn(at2, f[4 * ch + j]);
+                        put16(smem, OFF_U, part_at<PC>(tok, 0, cc, 8192), 24576, take8(f + 4 * ch));
+                        put16(smem, OFF_U, part_at<PC>(tok, 1, cc, 8192), 24576, take8(f + 4 * ch));
+                        put16(smem, OFF_U, part_at<PC>(tok, 2, cc, 8192), 24576, round8(f + 4 * ch));
                     }
-                    put16(smem, OFF_UH, tok, c0 / 8 + ch, 8192, take_bf16(e));
-                    put16(smem, OFF_UL, tok, c0 / 8 + ch, 8192, take_bf16(e));
-                    put16(smem, OFF_UM, tok, c0 / 8 + ch, 8192, take_bf16(e));
-                    put16(smem, OFF_UB, tok, c0 / 8 + ch, 8192, take_bf16(f));
                 }
                 fence_async_smem();
                 tc_fence_before();
                 mbar_arrive(&m->u);
             } else {
-                wait(&m->t_full[c & 1], c >> 1, m, status, 14);
-                wait(&m->ks, c, m, status, 15);
-                tc_fence_after();
-                tmem_ld32(d_ks + tl + c0, buf);
-                const float sa = q.scale * gt->a[tok];
-#pragma unroll
-                for (int j = 0; j < kCols; ++j) buf[j] *= sa;
                 tc_fence_before();
-                mbar_arrive(&m->u);                // the previous chunk's y has been read out
+                mbar_arrive(&m->r);                // the previous chunk's P U has been read
+                wait(&m->t_full[c & 1], c >> 1, m, status, 14);
+                const float sa = q.scale * gt->a[tok];
+                const float2 sa2 = make_float2(sa, sa);
+                wait(&m->ks, c, m, status, 15);
+                __syncwarp();
+                tc_fence_after();
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) {
+                    tmem_sum<W, 2>(tl + D_KS + W * hh, PC, buf + W / 2 * hh);
+#pragma unroll
+                    for (int j = 0; j < W / 2; ++j) buf[W / 2 * hh + j] = __fmul2_rn(sa2, buf[W / 2 * hh + j]);
+                }
+                tc_fence_before();
+                mbar_arrive(&m->u);
             }
             const float whole = gt->whole;
+            const float2 w2 = make_float2(whole, whole);
             wait(&m->s, c, m, status, 16);
+            __syncwarp();
             tc_fence_after();
-            {
-                float d[kCols];
-                tmem_ld32(d_s + tl + c0, d);
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) S[j] = fmaf(whole, S[j], d[j]);
+            for (int hh = 0; hh < NH; ++hh) {
+                float2 d[W / 2];
+                tmem_sum<W, 3>(tl + D_S + W * hh, PC, d);
+#pragma unroll
+                for (int j = 0; j < W / 2; ++j) S[W / 2 * hh + j] = __ffma2_rn(w2, S[W / 2 * hh + j], d[j]);
             }
-            // S lo takes the place of the U that P U reads
+            // S takes the place of the U that P U reads
             wait(&m->o, c, m, status, 17);
+            __syncwarp();
             if (c + 1 < w.nch) store_state();
             if (!top) {
                 tc_fence_after();
                 const size_t o = (((size_t)w.b * q.seqlen + c * kC + tok) * q.nheads + w.h) * P + w.p0 + c0;
-                float d[kCols];
-                tmem_ld32(d_o + tl + c0, d);
+                const bool in = c * kC + tok < w.len && M3_SPAN(8, o, kCols, (long long)q.batch * q.seqlen * q.nheads * P);
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(q.y) + o);
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) buf[j] += d[j];
-                if (c * kC + tok < w.len && M3_SPAN(8, o, kCols, (long long)q.batch * q.seqlen * q.nheads * P)) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(q.y) + o);
+                for (int hh = 0; hh < NH; ++hh) {
+                    float2 f[W / 2];
+                    tmem_sum<W, 1>(tl + D_TR + PC + W * hh, PC, f);
 #pragma unroll
-                    for (int ch = 0; ch < kCols / 8; ++ch) dst[ch] = pack_chunk(buf + 8 * ch);
+                    for (int j = 0; j < W / 2; ++j) f[j] = __fadd2_rn(buf[W / 2 * hh + j], f[j]);
+                    if (in) {
+#pragma unroll
+                        for (int ch = 0; ch < W / 8; ++ch) dst[W / 8 * hh + ch] = round8(f + 4 * ch);
+                    }
                 }
             }
         }
@@ -419,142 +624,184 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c4 = 0; c4 < kCols / 4; ++c4)
                 *reinterpret_cast<float4*>(q.final_h + ho + 4 * c4) =
-                    make_float4(S[4 * c4], S[4 * c4 + 1], S[4 * c4 + 2], S[4 * c4 + 3]);
+                    make_float4(S[2 * c4].x, S[2 * c4].y, S[2 * c4 + 1].x, S[2 * c4 + 1].y);
         }
-    } else if (warp <= 12) {
-        // ------------------------------- T and the masked Q K^T of every chunk
-        const int quarter = warp & 3, row = quarter * 32 + lane, pt = tid - 32 - kState;
-        const uint32_t tl = (uint32_t)(quarter * 32) << 16;
-        float* a11 = reinterpret_cast<float*>(smem + OFF_SCR);
+    } else if (warp <= 16) {
+        // ------------------- T and the masked Q K^T of every other chunk
+        const int group = (warp - 9) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const int pt = tid - 32 - kState - group * kPrep;
+        const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + D_G + 64 * group;
+        float* a11 = reinterpret_cast<float*>(smem + OFF_SCR + group * SCR_BYTES);
         float* a22 = a11 + 1024;
         float* a21 = a22 + 1024;
-        float* t22 = a21 + 1024;
+        const int xo = OFF_X + group * 16384, lo = OFF_TL + group * 8192;
+        const int tok = row & 63, blk = quarter & 1;       // the row's token; its 32-token block
         constexpr uint32_t idG = idesc_bf16(128, 64, 0, 0);
-        for (int c = 0; c < w.nch; ++c) {
-            const uint32_t kqo = OFF_KQ + (c % 3) * 32768;
-            const int xo = OFF_X + (c & 1) * 16384, lo = OFF_TL + (c & 1) * 8192;
+        Raw raw = {};
+        if (quarter == 2) raw = load_raw(q, w, group);
+        for (int c = group; c < w.nch; c += 2) {
+            const int kqo = OFF_KQ + (c % 3) * 32768;
             const int nt = min(kC, w.len - c * kC);
-            Gates* gt = &m->gates[c % 3];
+            Gates* gt = &m->gates[c & 3];
             wait(&m->kq_full[c % 3], c / 3, m, status, 20);
             // K rows behind the sequence's end (other data, possibly not numbers)
             // must be zeros: K^T U sums over all rows of the tile
-            for (int e = pt; e < (kC - nt) * 16; e += kPrep) {
-                const int r = nt + (e >> 4), ch = e & 15;
-                put16(smem, kqo + (ch >> 3) * 16384, r, ch & 7, 16384, make_uint4(0u, 0u, 0u, 0u));
+            if (nt < kC) {
+                for (int e = pt; e < (kC - nt) * 16; e += kPrep) {
+                    const int r = nt + (e >> 4), ch = e & 15;
+                    put16(smem, kqo + (ch >> 3) * 16384, sw128(r, ch & 7), 16384, make_uint4(0u, 0u, 0u, 0u));
+                }
+                fence_async_smem();
             }
-            if (nt < kC) fence_async_smem();
-            // this chunk's tiles and gates take the places of chunk c - 2's and c - 3's
-            if (c >= 2) wait(&m->x_free[c & 1], (c >> 1) - 1, m, status, 21);
-            make_gates(q, w, c, gt, warp == 9);
             tc_fence_before();
-            prep_sync();
-            if (pt == 0) {
+            group_sync(group);
+            if (quarter == 1) {
                 tc_fence_after();
+                const uint64_t aKQ = sdesc(sbase + kqo, 16, 1024);
+#pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t o = sbase + kqo + (kk >> 2) * 16384 + (kk & 3) * 32;
-                    umma(d_g, sdesc(o, 16, 1024), sdesc(o, 16, 1024), idG, kk > 0);
+                    const uint64_t o = aKQ + (kk >> 2) * 1024 + (kk & 3) * 2;
+                    umma_one(tmem + D_G + 64 * group, o, o, idG, kk > 0);
                 }
-                umma_commit(&m->g);
+                commit_one(&m->g[group]);
             }
-            __syncwarp();
-            wait(&m->g, c, m, status, 22);
+            // the gates take the place of chunk c - 4's, which every chain thread
+            // left before the products of chunk c - 3 freed this chunk's K and Q
+            if (quarter == 2) {
+                make_gates(raw, gt);
+                raw = load_raw(q, w, c + 2);       // the group's next
+            }
+            group_sync(group);
+            wait(&m->g[group], c >> 1, m, status, 22);
             tc_fence_after();
-            const int tok = row & 63;
-            const float gh = gt->hi[tok], gl = gt->lo[tok];
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                if (half * 32 > (tok | 31)) {      // columns behind every row of this warp
-                    if (row >= 64)
-#pragma unroll
-                        for (int ch = 0; ch < 4; ++ch) put16(smem, xo, row, 4 + ch, 16384, make_uint4(0u, 0u, 0u, 0u));
-                    continue;
-                }
+            const float2 G = gt->G[tok];
+            const float f = row < 64 ? gt->beta[tok] : q.scale;
+            const float fm = f * gt->mid[tok];             // (only rows of the second block use it)
+            // P takes the place of chunk c - 2's
+            if (row >= 64 && c >= 2) wait(&m->x_free[group], (c >> 1) - 1, m, status, 21);
+            __syncwarp();
+            if (blk == 1) {                                // the block left of the diagonal
                 float d[32];
-                tmem_ld32(d_g + tl + half * 32, d);
-                const float f = row < 64 ? gt->beta[tok] : q.scale;
-                const int last = row < 64 ? tok - 1 : tok;
+                tmem_ld32(tl, d);
+                const float2 f2 = make_float2(fm, fm);
+                float2 e[16];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int col = half * 32 + j;
-                    const float e = exp2f((gh - gt->hi[col]) + (gl - gt->lo[col]));
-                    d[j] = col <= last ? f * e * d[j] : 0.f;
+                for (int j = 0; j < 8; ++j) {
+                    const float4 u = *reinterpret_cast<const float4*>(&gt->mid[4 * j]);
+                    e[2 * j] = __fmul2_rn(__fmul2_rn(make_float2(u.x, u.y), f2), make_float2(d[4 * j], d[4 * j + 1]));
+                    e[2 * j + 1] = __fmul2_rn(__fmul2_rn(make_float2(u.z, u.w), f2), make_float2(d[4 * j + 2], d[4 * j + 3]));
                 }
                 if (row < 64) {
-                    float* dst = half ? a22 : (quarter == 0 ? a11 : a21);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) dst[j * 32 + lane] = d[j];
+                    for (int j = 0; j < 16; ++j) {
+                        a21[2 * j * 32 + lane] = e[j].x;
+                        a21[(2 * j + 1) * 32 + lane] = e[j].y;
+                    }
                 } else {
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) put16(smem, xo, row, half * 4 + ch, 16384, pack_chunk(d + 8 * ch));
+                    for (int ch = 0; ch < 4; ++ch) put16(smem, xo, sw128(row, ch), 16384, round8(e + 4 * ch));
+                }
+            } else if (row >= 64) {
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) put16(smem, xo, sw128(row, 4 + ch), 16384, make_uint4(0u, 0u, 0u, 0u));
+            }
+            {                                              // the diagonal block
+                float d[32];
+                tmem_ld32(tl + 32 * blk, d);
+                const int last = row < 64 ? lane - 1 : lane;
+                float2 e[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float4 u = *reinterpret_cast<const float4*>(&gt->G[32 * blk + 2 * j]);
+                    const float x0 = ex2((G.x - u.x) + (G.y - u.y)), x1 = ex2((G.x - u.z) + (G.y - u.w));
+                    e[j] = make_float2(2 * j <= last ? f * x0 * d[2 * j] : 0.f, 2 * j + 1 <= last ? f * x1 * d[2 * j + 1] : 0.f);
+                }
+                if (row < 64) {
+                    float* dst = blk ? a22 : a11;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        dst[2 * j * 32 + lane] = e[j].x;
+                        dst[(2 * j + 1) * 32 + lane] = e[j].y;
+                    }
+                } else {
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) put16(smem, xo, sw128(row, 4 * blk + ch), 16384, round8(e + 4 * ch));
                 }
             }
             tc_fence_before();
-            prep_sync();
-            if (row < 64) {
-                float x[32];
-                invert32(quarter == 0 ? a11 : a22, x);
+            group_sync(group);
+            // warps 2 and 3 of the quarters, whose side of the chain has less to do
+            if (quarter >= 2) {
+                float* at = blk ? a22 : a11;
+                float2 x[16];
+                invert32(at, x);
                 __syncwarp();
-                // T11 by rows for A21 T11; T22 by columns, padded, for T22 (A21 T11)
-                if (quarter == 0) {
+                if (blk == 0) {                            // T11 by rows
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) a11[i * 32 + lane] = x[i];
-                } else {
+                    for (int i = 0; i < 16; ++i) {
+                        a11[2 * i * 32 + lane] = x[i].x;
+                        a11[(2 * i + 1) * 32 + lane] = x[i].y;
+                    }
+                } else {                                   // T22 by columns, 16-byte blocks exchanged
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<float4*>(t22 + lane * 36 + 4 * i) =
-                            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                }
-                const int r0 = quarter * 32;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float v = i > lane ? x[i] : 0.f;
-                    put2(smem, xo, r0 + i, r0 + lane, v);
-                    put2(smem, lo, r0 + i, r0 + lane, v - __bfloat162float(__float2bfloat16_rn(v)));
+                        *reinterpret_cast<float4*>(a22 + lane * 32 + ((i ^ (lane & 7)) << 2)) =
+                            make_float4(x[2 * i].x, x[2 * i].y, x[2 * i + 1].x, x[2 * i + 1].y);
                 }
             }
-            prep_sync();
+            if (c >= 2) wait(&m->x_free[group], (c >> 1) - 1, m, status, 23);
+            group_sync(group);
             {
                 const int r0 = quarter * 8;
-                float acc[8];
+                float2 acc[4];
+                product32<false>(a21, a11, r0, acc);       // A21 T11
+                // T11 - I and T22 - I as bfloat16 parts: a thread has 8 columns of a row of each
+                const int r = pt >> 2, ch = pt & 3;
+                float2 t[4];
+                const float4 u = *reinterpret_cast<const float4*>(a11 + r * 32 + 8 * ch);
+                const float4 v = *reinterpret_cast<const float4*>(a11 + r * 32 + 8 * ch + 4);
+                const float tv[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-#pragma unroll 8
-                for (int k = 0; k < 32; ++k) {
-                    const float t = a11[k * 32 + lane];
-                    const float4 u = *reinterpret_cast<const float4*>(a21 + k * 32 + r0);
-                    const float4 v = *reinterpret_cast<const float4*>(a21 + k * 32 + r0 + 4);
-                    acc[0] = fmaf(u.x, t, acc[0]); acc[1] = fmaf(u.y, t, acc[1]);
-                    acc[2] = fmaf(u.z, t, acc[2]); acc[3] = fmaf(u.w, t, acc[3]);
-                    acc[4] = fmaf(v.x, t, acc[4]); acc[5] = fmaf(v.y, t, acc[5]);
-                    acc[6] = fmaf(v.z, t, acc[6]); acc[7] = fmaf(v.w, t, acc[7]);
+                for (int j = 0; j < 4; ++j)
+                    t[j] = make_float2(8 * ch + 2 * j == r ? 0.f : tv[2 * j], 8 * ch + 2 * j + 1 == r ? 0.f : tv[2 * j + 1]);
+                put16(smem, xo, sw128(r, ch), 16384, take8(t));
+                put16(smem, lo, sw128(r, ch), 8192, round8(t));
+                float s8[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int k = 8 * ch + j;
+                    s8[j] = k == r ? 0.f : a22[k * 32 + (((r >> 2) ^ j) << 2) + (r & 3)];      // k & 7 = j
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) a22[(r0 + i) * 32 + lane] = acc[i];
-                prep_sync();
+                for (int j = 0; j < 4; ++j) t[j] = make_float2(s8[2 * j], s8[2 * j + 1]);
+                put16(smem, xo, sw128(32 + r, 4 + ch), 16384, take8(t));
+                put16(smem, lo, sw128(32 + r, 4 + ch), 8192, round8(t));
+                group_sync(group);                         // A21 has been read
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-#pragma unroll 8
-                for (int k = 0; k < 32; ++k) {
-                    const float t = -a22[k * 32 + lane];
-                    const float4 u = *reinterpret_cast<const float4*>(t22 + k * 36 + r0);
-                    const float4 v = *reinterpret_cast<const float4*>(t22 + k * 36 + r0 + 4);
-                    acc[0] = fmaf(u.x, t, acc[0]); acc[1] = fmaf(u.y, t, acc[1]);
-                    acc[2] = fmaf(u.z, t, acc[2]); acc[3] = fmaf(u.w, t, acc[3]);
-                    acc[4] = fmaf(v.x, t, acc[4]); acc[5] = fmaf(v.y, t, acc[5]);
-                    acc[6] = fmaf(v.z, t, acc[6]); acc[7] = fmaf(v.w, t, acc[7]);
+                for (int i = 0; i < 4; ++i) {
+                    a21[(r0 + 2 * i) * 32 + lane] = -acc[i].x;
+                    a21[(r0 + 2 * i + 1) * 32 + lane] = -acc[i].y;
                 }
+                group_sync(group);
+                product32<true>(a22, a21, r0, acc);        // - T22 (A21 T11)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    put2(smem, xo, 32 + r0 + i, lane, acc[i]);
-                    put2(smem, lo, 32 + r0 + i, lane, acc[i] - __bfloat162float(__float2bfloat16_rn(acc[i])));
+                    const float n = (i & 1) ? acc[i >> 1].y : acc[i >> 1].x;
+                    const uint32_t o = (uint32_t)((32 + r0 + i) * 128 + (((lane >> 3) ^ i) << 4) + (lane & 7) * 2);   // (row & 7 = i)
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(n);
+                    if (M3_SPAN(2, o, 2, 8192)) {
+                        *reinterpret_cast<__nv_bfloat16*>(smem + xo + o) = hi;
+                        *reinterpret_cast<__nv_bfloat16*>(smem + lo + o) = __float2bfloat16_rn(n - __bfloat162float(hi));
+                    }
                 }
             }
             fence_async_smem();
-            mbar_arrive(&m->t_full[c & 1]);
+            mbar_arrive(&m->t_full[group]);
         }
-        if (pt == 0) {
-            umma_commit(&m->drain_b);
-            mbar_wait_flag(&m->drain_b, 0, &m->drain_flag, nullptr, 0);
+        if (quarter == 1) {
+            __syncwarp();
+            commit_one(&m->drain[group]);
+            mbar_wait_flag(&m->drain[group], 0, &m->drain_flag, nullptr, 0);
         }
         __syncwarp();
     } else {
@@ -572,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c >= 2) wait(&m->v_free[c & 1], (c >> 1) - 1, m, status, 31);
                 bar = &m->v_full[c & 1];
                 mbar_expect_tx(bar, 8192);
-                tma_load_5d(sbase + OFF_V + (c & 1) * 8192, &tmV, bar, w.p0, 0, w.h, c * kC, w.b);
+                tma_load_5d(sbase + OFF_V + (c & 1) * 8192, &tmV, bar, w.p0 & ~63, 0, w.h, c * kC, w.b);
             }
             // nothing may still be on its way into shared memory when the CTA ends
             for (int c = max(0, w.nch - 3); c < w.nch; ++c) {
@@ -594,6 +841,17 @@ bool delta_tc_eligible(const m3_dims& d) {
     return d.io_dtype == M3_BF16 && d.dstate == dtc::kN && d.headdim % dtc::kP == 0;
 }
 
+template <int PC>
+static cudaError_t launch_pc(const CUtensorMap& mK, const CUtensorMap& mQ, const CUtensorMap& mV, const m3_dims& d,
+                             const DeltaParams& q, int* status, cudaStream_t st) {
+    using namespace dtc;
+    const cudaError_t e = cudaFuncSetAttribute(delta_tc_kernel<PC>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)((long long)d.batch * d.nheads * (d.headdim / PC));
+    delta_tc_kernel<PC><<<grid, kThreads, SMEM_BYTES, st>>>(mK, mQ, mV, q, status);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st) {
     using namespace dtc;
     CUtensorMap mK, mQ, mV;
@@ -601,11 +859,12 @@ cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, int* status,
         !make_tile_map(&mQ, q.q, kN, 1, d.ngroups, d.seqlen, d.batch, kC) ||
         !make_tile_map(&mV, q.v, d.headdim, 1, d.nheads, d.seqlen, d.batch, kC))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(delta_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((long long)d.batch * d.nheads * (d.headdim / kP));
-    delta_tc_kernel<<<grid, kThreads, SMEM_BYTES, st>>>(mK, mQ, mV, q, status);
-    return cudaGetLastError();
+    // columns a CTA
+    const char* env = getenv("M3_DTC_PC");
+    const int pc = env ? atoi(env) : 64;
+    if (pc == 64) return launch_pc<64>(mK, mQ, mV, d, q, status, st);
+    if (pc == 32) return launch_pc<32>(mK, mQ, mV, d, q, status, st);
+    return launch_pc<16>(mK, mQ, mV, d, q, status, st);
 }
 
 }  // namespace m3
