@@ -1,0 +1,118 @@
+// delta_tc.cuh -- what the chunked kernels of the gated delta rule share: the
+// gates of a chunk, splitting of float32 values into bfloat16 parts, and the
+// records that the gradient's passes hand on.
+#pragma once
+
+#include "m3_kernels.h"
+#include "tc_ptx.cuh"
+
+namespace m3 {
+namespace dtc {
+
+using namespace ptx;
+
+constexpr int kC = 64;             // tokens a chunk
+constexpr int kN = 128;
+constexpr unsigned kFull = 0xffffffffu;
+
+struct Gates {
+    float2 G[kC];                  // sum of g in log2 units, as a sum of two floats
+    float a[kC], at[kC], beta[kC]; // e^G, e^{G_C - G}, beta (0 behind the end)
+    float mid[kC];                 // j < 32: e^{G_31 - G_j}; i >= 32: e^{G_i - G_31}
+    float whole;                   // e^{G_C}
+    float pad[3];
+};
+
+__device__ __forceinline__ float clamp_g(float g) { return g < -1.0e4f ? -1.0e4f : g; }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// two floats -> two bfloat16 (returned), f becomes what the rounding left
+__device__ __forceinline__ uint32_t take2(float2& f) {
+    const uint32_t w = pack_bf16x2(f.x, f.y);
+    f = __ffma2_rn(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), make_float2(-1.f, -1.f), f);
+    return w;
+}
+__device__ __forceinline__ uint4 take8(float2* f) {
+    return make_uint4(take2(f[0]), take2(f[1]), take2(f[2]), take2(f[3]));
+}
+__device__ __forceinline__ uint4 round8(const float2* f) {
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                      pack_bf16x2(f[3].x, f[3].y));
+}
+// a + b of sums of two floats (each a pair with a small second part)
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+    const float s = a.x + b.x, t = s - a.x;
+    const float e = (a.x - (s - t)) + (b.x - t) + (a.y + b.y);
+    const float r = s + e;
+    return make_float2(r, e - (r - s));
+}
+__device__ __forceinline__ float diff_pair(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); }
+
+// g and beta of a chunk: lane l holds tokens 2 l and 2 l + 1
+struct Raw {
+    float g[2], beta[2];
+};
+__device__ __forceinline__ Raw load_raw(const DeltaParams& q, int b, int h, int len, int c) {
+    const int lane = threadIdx.x & 31;
+    Raw r;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int t = c * kC + 2 * lane + j;
+        const size_t o = ((size_t)b * q.seqlen + t) * q.nheads + h;
+        const bool ok = t < len && M3_IN(40, o, (long long)q.batch * q.seqlen * q.nheads);
+        r.g[j] = (ok && q.g) ? __ldg(q.g + o) : 0.f;
+        r.beta[j] = ok ? __ldg(q.beta + o) : 0.f;
+    }
+    return r;
+}
+// Sums of g in log2 units.  They run as pairs of floats, so that differences
+// keep float32 accuracy after strong decay.
+__device__ __forceinline__ void make_gates(const Raw& raw, Gates* out) {
+    const int lane = threadIdx.x & 31;
+    constexpr float kHi = 1.44269502162933349609f, kLo = 1.92596299112661746887e-8f;    // log2 e
+    float2 d[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const float g = clamp_g(raw.g[j]);
+        const float p = g * kHi;
+        d[j] = make_float2(p, fmaf(g, kHi, -p) + g * kLo);
+    }
+    float2 sum = add_pair(d[0], d[1]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float2 u = make_float2(__shfl_up_sync(kFull, sum.x, o), __shfl_up_sync(kFull, sum.y, o));
+        if (lane >= o) sum = add_pair(sum, u);
+    }
+    const float2 total = make_float2(__shfl_sync(kFull, sum.x, 31), __shfl_sync(kFull, sum.y, 31));
+    const float2 mid = make_float2(__shfl_sync(kFull, sum.x, 15), __shfl_sync(kFull, sum.y, 15));
+    const float2 G[2] = {add_pair(sum, make_float2(-d[1].x, -d[1].y)), sum};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = 2 * lane + j;
+        out->G[i] = G[j];
+        out->a[i] = ex2(G[j].x + G[j].y);
+        out->at[i] = ex2(diff_pair(total, G[j]));
+        out->beta[i] = raw.beta[j];
+        out->mid[i] = ex2(i < 32 ? diff_pair(mid, G[j]) : diff_pair(G[j], mid));
+    }
+    if (lane == 0) out->whole = ex2(total.x + total.y);
+}
+
+// Records of the gradient's passes, one a chunk of a (batch, head): bfloat16
+// matrices, rows of 64 columns, each as hi and lo part (elements):
+//   T - I, P = scale Gam o Q K^T       [2][64][64] each
+//   then for every 64 columns of the head
+//   S before the chunk, its gradient behind the chunk   [2][128][64] each
+//   U, dR                                               [2][64][64] each
+constexpr size_t kTok = 64 * 64, kSt = 128 * 64;
+constexpr size_t kRecT = 0, kRecP = 2 * kTok, kRecSlice = 4 * kTok;
+constexpr size_t kSliceS = 0, kSliceDS = 2 * kSt, kSliceU = 4 * kSt, kSliceDR = 4 * kSt + 2 * kTok;
+constexpr size_t kSliceElems = 4 * kSt + 4 * kTok;
+__host__ __device__ constexpr size_t rec_elems(int P) { return kRecSlice + (size_t)(P / 64) * kSliceElems; }
+
+}  // namespace dtc
+}  // namespace m3

@@ -520,6 +520,13 @@ cudaError_t launch_delta_seq(const m3_dims& d, const DeltaParams& q, cudaStream_
     return d.io_dtype == M3_BF16 ? delta::seq<__nv_bfloat16>(q, grid, st) : delta::seq<float>(q, grid, st);
 }
 
+cudaError_t launch_delta_reduce(const m3_dims& d, const DeltaParams& q, int tiles, cudaStream_t st) {
+    const unsigned rows = (unsigned)((long long)d.batch * d.seqlen * d.ngroups);
+    if (d.io_dtype == M3_BF16) delta::delta_reduce_kernel<__nv_bfloat16><<<rows, delta::kThreads, 0, st>>>(q, tiles);
+    else delta::delta_reduce_kernel<float><<<rows, delta::kThreads, 0, st>>>(q, tiles);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_delta_seq_bwd(const m3_dims& d, const DeltaParams& q, cudaStream_t st) {
     DeltaParams f = q;                       // checkpoints first
     f.y = nullptr;
@@ -528,13 +535,7 @@ cudaError_t launch_delta_seq_bwd(const m3_dims& d, const DeltaParams& q, cudaStr
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((long long)d.batch * d.nheads * delta_tiles(d));
     e = d.io_dtype == M3_BF16 ? delta::seq_bwd<__nv_bfloat16>(q, grid, st) : delta::seq_bwd<float>(q, grid, st);
-    if (e != cudaSuccess) return e;
-    const unsigned rows = (unsigned)((long long)d.batch * d.seqlen * d.ngroups);
-    if (d.io_dtype == M3_BF16)
-        delta::delta_reduce_kernel<__nv_bfloat16><<<rows, delta::kThreads, 0, st>>>(q, delta_tiles(d));
-    else
-        delta::delta_reduce_kernel<float><<<rows, delta::kThreads, 0, st>>>(q, delta_tiles(d));
-    return cudaGetLastError();
+    return e == cudaSuccess ? launch_delta_reduce(d, q, delta_tiles(d), st) : e;
 }
 
 // The streaming kernel needs whole float4 columns that divide its 256 threads

@@ -1,0 +1,611 @@
+// k_delta_bwd_tc.cu -- chunked gradient of the gated delta rule (sm_100a):
+// bfloat16 io, N = 128, P a multiple of 64.  The formulas of a chunk (notation
+// of k_delta_tc.cu; ' marks the gradient of the state behind the chunk):
+//   dU  = P^T dY + e^{G_C-G} o (K dS')              P = scale Gam o Q K^T
+//   dR  = T^T dU                                     dV = beta o dR
+//   dS  = e^{G_C} dS' + Q^T (scale e^G o dY) - K^T (beta e^G o dR)
+//   dP  = dY U^T (j <= i)        dA = - dR U^T (j < i)
+//   Z = dY S^T,  X = dR S^T,  Y = U dS'^T
+//   dQ  = scale e^G o Z + (scale Gam o dP) K
+//   dK  = (scale Gam o dP)^T Q + D K + D^T K + e^{G_C-G} o Y - beta e^G o X,   D = beta Gam o dA
+//   dbeta_i = dR_i . v_i - e^{G_i} k_i . X_i + sum_j dA_ij Gam_ij k_i.k_j
+//   dG_i = (rows - columns of E)_i + scale e^{G_i} q_i.Z_i - beta_i e^{G_i} k_i.X_i - e^{G_C-G_i} k_i.Y_i,
+//          E = dP o P + dA o A
+//   dG_C += e^{G_C} <S, dS'> + sum_j e^{G_C-G_j} k_j.Y_j;    dg_t = sum_{i >= t} dG_i
+//
+// Three passes.  The prefill kernel runs once more and records T, P, the state
+// before every chunk and U.  delta_rev_kernel carries dS from the last chunk to
+// the first (one CTA a head and 32 columns; dU and T^T dU are the only
+// dependent products of a chunk) and records dS' and dR.  delta_grad_kernel
+// then takes all chunks at once, one CTA each.  dq and dk of a group's heads
+// are added by a further kernel in a fixed order.
+//
+// The chain and all that feeds sums keep float32 values as two bfloat16 parts
+// (hi + lo); a product with two split operands drops lo x lo (2^-17 of the
+// product).  Products are 16 x 8 x 16 warp-level mma with register
+// accumulators: the matrices of a chunk (64 x 64 to 64 x 128) are masked,
+// scaled and split between one product and the next, and register fragments
+// take these steps without a way through tensor memory.
+//
+// Times on one B200 stand with the launcher.
+#define M3_BOUNDS_FILE 13
+#include "m3_bounds.cuh"
+#include "delta_tc.cuh"
+
+namespace m3 {
+namespace dbw {
+
+using namespace dtc;
+
+constexpr int kThreads = 256;
+
+// a matrix in shared memory: rows of 128 bytes (64 columns), 16-byte groups
+// exchanged by row (sw128); columns 64.. go on `atom` bytes further
+__device__ __forceinline__ uint32_t at(uint32_t base, int atom, int row, int col8) {
+    return base + (col8 >> 3) * atom + row * 128 + (((col8 & 7) ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+struct Mat {
+    uint32_t base;
+    int atom;
+};
+
+// acc (16 rows from m0, 8 NT columns from n0) += A (B + B2), K steps of 16.
+// AT: A is stored transposed ([k][m]); BT: B is stored as [n][k], else [k][n].
+// B2 (same layout) is left out where its base is 0; n2 is its first column.
+template <int NT, int K, bool AT, bool BT, bool TWO>
+__device__ __forceinline__ void mm(float (*acc)[4], Mat A, int m0, Mat B, int n0, uint32_t base2, int n2) {
+    const int lane = threadIdx.x & 31, mi = lane >> 3, l7 = lane & 7;
+#pragma unroll 2
+    for (int k0 = 0; k0 < K; k0 += 16) {
+        uint32_t a[4];
+        if (AT) ldsm4t(a, at(A.base, A.atom, k0 + (mi >> 1) * 8 + l7, (m0 >> 3) + (mi & 1)));
+        else ldsm4(a, at(A.base, A.atom, m0 + (mi & 1) * 8 + l7, (k0 >> 3) + (mi >> 1)));
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+            uint32_t b[4];
+            if (BT) ldsm4(b, at(B.base, B.atom, n0 + 8 * n + (mi >> 1) * 8 + l7, (k0 >> 3) + (mi & 1)));
+            else ldsm4t(b, at(B.base, B.atom, k0 + (mi & 1) * 8 + l7, (n0 >> 3) + n + (mi >> 1)));
+            mma16816(acc[n], a, b[0], b[1]);
+            mma16816(acc[n + 1], a, b[2], b[3]);
+            if (TWO) {
+                if (BT) ldsm4(b, at(base2, B.atom, n2 + 8 * n + (mi >> 1) * 8 + l7, (k0 >> 3) + (mi & 1)));
+                else ldsm4t(b, at(base2, B.atom, k0 + (mi & 1) * 8 + l7, (n2 >> 3) + n + (mi >> 1)));
+                mma16816(acc[n], a, b[0], b[1]);
+                mma16816(acc[n + 1], a, b[2], b[3]);
+            }
+        }
+    }
+}
+
+template <int NT> __device__ __forceinline__ void zero(float (*acc)[4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+    const int n = ok ? 16 : 0;               // 0: the destination gets zeros, the source is not read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ float2 unpack(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
+__device__ __forceinline__ uint32_t elem(uint32_t base, int row, int col) { return at(base, 0, row, col >> 3) + (col & 7) * 2; }
+
+__device__ __forceinline__ int length_of(const DeltaParams& q, int b) {
+    if (!q.lengths) return q.seqlen;
+    return M3_IN(1, b, q.batch) ? min(max(q.lengths[b], 0), q.seqlen) : 0;
+}
+__device__ __forceinline__ long long ext_rec(const DeltaParams& q) {
+    return (long long)q.batch * q.nheads * q.nck * (long long)rec_elems(q.headdim);
+}
+
+// 64 token rows (chunk c) of q, k or one 64-column tile of v, dy into shared
+// memory: `groups` 16-byte groups a row; rows behind the end are zeros
+__device__ __forceinline__ void load_tokens(uint32_t dst, int atom, const void* src, size_t row0, size_t pitch, size_t col,
+                                            int groups, int nt, long long ext) {
+    for (int e = threadIdx.x; e < 64 * groups; e += kThreads) {
+        const int r = e / groups, g = e - r * groups;
+        const size_t o = (row0 + r) * pitch + col + 8 * g;
+        const bool ok = r < nt && M3_SPAN(2, o, 8, ext);
+        cp16(at(dst, atom, r, g), static_cast<const __nv_bfloat16*>(src) + (ok ? o : 0), ok);
+    }
+}
+// `rows` rows of 64 recorded columns
+__device__ __forceinline__ void load_rec(const DeltaParams& q, uint32_t dst, size_t o, int rows) {
+    for (int e = threadIdx.x; e < rows * 8; e += kThreads) {
+        const bool ok = M3_SPAN(3, o + e * 8, 8, ext_rec(q));
+        cp16(at(dst, 0, e >> 3, e & 7), q.rec + (ok ? o + e * 8 : 0), ok);
+    }
+}
+
+// ------------------------------------------------------- the reverse chain --
+constexpr int kPS = 32;                      // columns a CTA
+constexpr uint32_t RV_K = 0, RV_Q = 16384, RV_T = 32768, RV_P = 49152, RV_DY = 65536, RV_STAGE = 73728;
+constexpr uint32_t RV_DS = 2 * RV_STAGE;     // dS hi (columns 0..31), lo (32..63): 128 rows
+constexpr uint32_t RV_DU = RV_DS + 16384;    // 64 rows each, hi and lo side by side: dU,
+constexpr uint32_t RV_DR = RV_DU + 8192;     //   - beta e^G dR,
+constexpr uint32_t RV_DYS = RV_DR + 8192;    //   scale e^G dY
+constexpr uint32_t RV_GATES = RV_DYS + 8192;
+constexpr int RV_BYTES = RV_GATES + 2 * sizeof(Gates) + 128;
+
+__global__ void __launch_bounds__(kThreads, 1) delta_rev_kernel(DeltaParams q) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    const uint32_t sb = (su32(smem_raw) + 127u) & ~127u;
+    uint8_t* smem = smem_raw + (sb - su32(smem_raw));
+    Gates* gates = reinterpret_cast<Gates*>(smem + RV_GATES);
+    if (!M3_SPAN(4, sb - su32(smem_raw), RV_GATES + 2 * sizeof(Gates), dyn_smem_bytes())) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, P = q.headdim, H = q.nheads;
+    const int slices = P / kPS, bh = blockIdx.x / slices, p0 = (blockIdx.x % slices) * kPS;
+    const int b = bh / H, h = bh % H, g = h / (H / q.ngroups);
+    const int len = length_of(q, b), nch = (len + kC - 1) / kC;
+    const int mt = warp & 3, nh = warp >> 2, qr = lane >> 2, qc = (lane & 3) * 2;
+    const long long ext_k = (long long)q.batch * q.seqlen * q.ngroups * kN, ext_v = (long long)q.batch * q.seqlen * H * P;
+    [[maybe_unused]] const long long ext_h = (long long)q.batch * H * kN * P;
+    const size_t rec = rec_elems(P);
+    auto slice_at = [&](int c) { return ((size_t)bh * q.nck + c) * rec + kRecSlice + (size_t)(p0 >> 6) * kSliceElems + (p0 & 63); };
+
+    auto load = [&](int c) {
+        const uint32_t st = sb + (c & 1) * RV_STAGE;
+        const int nt = min(kC, len - c * kC);
+        const size_t row0 = (size_t)b * q.seqlen + c * kC;
+        load_tokens(st + RV_K, 8192, q.k, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
+        load_tokens(st + RV_Q, 8192, q.q, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
+        load_tokens(st + RV_DY, 0, q.dy, row0, (size_t)H * P, (size_t)h * P + p0, 4, nt, ext_v);
+        const size_t o = ((size_t)bh * q.nck + c) * rec;
+        load_rec(q, st + RV_T, o + kRecT, 128);
+        load_rec(q, st + RV_P, o + kRecP, 128);
+        cp_commit();
+    };
+    // dS: warp w has rows 16 w .., all 32 columns
+    float dS[4][4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const size_t o = ((size_t)bh * kN + 16 * warp + qr + 8 * (i >> 1)) * P + p0 + 8 * n + qc + (i & 1);
+            dS[n][i] = (q.d_final_h && M3_IN(5, o, ext_h)) ? q.d_final_h[o] : 0.f;
+        }
+    // dS into shared memory and, as the gradient of the state behind chunk c, into the record
+    auto keep_ds = [&](int c) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = 16 * warp + qr + 8 * r, col = 8 * n + qc;
+                float2 f = make_float2(dS[n][2 * r], dS[n][2 * r + 1]);
+                const uint32_t hi = take2(f), lo = pack_bf16x2(f.x, f.y);
+                sts32(elem(sb + RV_DS, row, col), hi);
+                sts32(elem(sb + RV_DS, row, 32 + col), lo);
+                const size_t o = slice_at(c) + kSliceDS + row * 64 + col;
+                if (M3_SPAN(6, o + kSt, 2, ext_rec(q))) {
+                    *reinterpret_cast<uint32_t*>(q.rec + o) = hi;
+                    *reinterpret_cast<uint32_t*>(q.rec + o + kSt) = lo;
+                }
+            }
+    };
+    Raw raw = {};
+    if (nch > 0) {
+        load(nch - 1);
+        keep_ds(nch - 1);
+        if (warp == 0) {
+            raw = load_raw(q, b, h, len, nch - 1);
+            make_gates(raw, &gates[(nch - 1) & 1]);
+            if (nch > 1) raw = load_raw(q, b, h, len, nch - 2);
+        }
+    }
+    __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(q.dv);
+    for (int c = nch - 1; c >= 0; --c) {
+        const uint32_t st = sb + (c & 1) * RV_STAGE;
+        const Gates* gt = &gates[c & 1];
+        const int nt = min(kC, len - c * kC);
+        cp_wait();
+        __syncthreads();
+        if (c > 0) load(c - 1);
+        {                                    // scale e^G dY
+            const int r = tid >> 2, ch = tid & 3;
+            const uint4 v = lds128(at(st + RV_DY, 0, r, ch));
+            const float s = q.scale * gt->a[r];
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            float2 f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = __fmul2_rn(make_float2(s, s), unpack(u[j]));
+            sts128(at(sb + RV_DYS, 0, r, ch), take8(f));
+            sts128(at(sb + RV_DYS, 0, r, 4 + ch), round8(f));
+        }
+        float dU[2][4], t[2][4];
+        zero<2>(dU);
+        zero<2>(t);
+        const Mat K = {st + RV_K, 8192}, Q = {st + RV_Q, 8192}, T = {st + RV_T, 0}, Tl = {st + RV_T + 8192, 0};
+        const Mat Ph = {st + RV_P, 0}, Pl = {st + RV_P + 8192, 0}, dY = {st + RV_DY, 0};
+        mm<2, 64, true, false, false>(dU, Ph, 16 * mt, dY, 16 * nh, 0, 0);
+        mm<2, 64, true, false, false>(dU, Pl, 16 * mt, dY, 16 * nh, 0, 0);
+        mm<2, 128, false, false, true>(t, K, 16 * mt, {sb + RV_DS, 0}, 16 * nh, sb + RV_DS, 32 + 16 * nh);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = 16 * mt + qr + 8 * r;
+            const float e = gt->at[row];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int col = 16 * nh + 8 * n + qc;
+                float2 f = make_float2(fmaf(e, t[n][2 * r], dU[n][2 * r]), fmaf(e, t[n][2 * r + 1], dU[n][2 * r + 1]));
+                dU[n][2 * r] = f.x;
+                dU[n][2 * r + 1] = f.y;
+                sts32(elem(sb + RV_DU, row, col), take2(f));
+                sts32(elem(sb + RV_DU, row, 32 + col), pack_bf16x2(f.x, f.y));
+            }
+        }
+        __syncthreads();
+        // dR = dU + (T - I)^T dU
+        mm<2, 64, true, false, true>(dU, T, 16 * mt, {sb + RV_DU, 0}, 16 * nh, sb + RV_DU, 32 + 16 * nh);
+        mm<2, 64, true, false, false>(dU, Tl, 16 * mt, {sb + RV_DU, 0}, 16 * nh, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = 16 * mt + qr + 8 * r;
+            const float be = gt->beta[row], s = -be * gt->a[row];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int col = 16 * nh + 8 * n + qc;
+                const float2 d = make_float2(dU[n][2 * r], dU[n][2 * r + 1]);
+                float2 f = d;
+                const size_t o = slice_at(c) + kSliceDR + row * 64 + col;
+                const uint32_t hi = take2(f), lo = pack_bf16x2(f.x, f.y);
+                if (M3_SPAN(7, o + kTok, 2, ext_rec(q))) {
+                    *reinterpret_cast<uint32_t*>(q.rec + o) = hi;
+                    *reinterpret_cast<uint32_t*>(q.rec + o + kTok) = lo;
+                }
+                const size_t vo = (((size_t)b * q.seqlen + c * kC + row) * H + h) * P + p0 + col;
+                if (row < nt && M3_SPAN(8, vo, 2, ext_v))
+                    *reinterpret_cast<uint32_t*>(dv + vo) = pack_bf16x2(be * d.x, be * d.y);
+                f = make_float2(s * d.x, s * d.y);
+                sts32(elem(sb + RV_DR, row, col), take2(f));
+                sts32(elem(sb + RV_DR, row, 32 + col), pack_bf16x2(f.x, f.y));
+            }
+        }
+        const float whole = gt->whole;
+        if (warp == 0 && c > 0) {
+            make_gates(raw, &gates[(c - 1) & 1]);
+            if (c > 1) raw = load_raw(q, b, h, len, c - 2);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dS[n][i] *= whole;
+        mm<4, 64, true, false, true>(dS, Q, 16 * warp, {sb + RV_DYS, 0}, 0, sb + RV_DYS, 32);
+        mm<4, 64, true, false, true>(dS, K, 16 * warp, {sb + RV_DR, 0}, 0, sb + RV_DR, 32);
+        if (c > 0) keep_ds(c - 1);
+    }
+    if (q.d_init_h) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const size_t o = ((size_t)bh * kN + 16 * warp + qr + 8 * r) * P + p0 + 8 * n + qc;
+                if (M3_SPAN(9, o, 2, ext_h)) *reinterpret_cast<float2*>(q.d_init_h + o) = make_float2(dS[n][2 * r], dS[n][2 * r + 1]);
+            }
+    }
+    // tokens behind the end of the sequence have no gradient
+    for (size_t e = (size_t)len * (kPS / 8) + tid; e < (size_t)q.seqlen * (kPS / 8); e += kThreads) {
+        const size_t vo = (((size_t)b * q.seqlen + e / (kPS / 8)) * H + h) * P + p0 + 8 * (e % (kPS / 8));
+        if (M3_SPAN(10, vo, 8, ext_v)) *reinterpret_cast<uint4*>(dv + vo) = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// ------------------------------------------------ the gradients of a chunk --
+constexpr uint32_t GR_K = 0, GR_Q = 16384, GR_DY = 32768, GR_V = 40960, GR_U = 49152, GR_DR = 65536, GR_S = 81920,
+                   GR_DS = 114688, GR_GATES = 147456;
+constexpr uint32_t GR_DQK = GR_S, GR_DKK = GR_S + 16384;       // hi, lo each, where S was
+struct GradSums {
+    float row[2][kC], beta[2][kC], tail[2][kC];      // by column half
+    float col[4][kC];                                // by row tile
+    float drv[kC], dot[8];
+};
+constexpr int GR_BYTES = GR_GATES + sizeof(Gates) + sizeof(GradSums) + 128;
+
+__global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, int nchunks) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    const uint32_t sb = (su32(smem_raw) + 127u) & ~127u;
+    uint8_t* smem = smem_raw + (sb - su32(smem_raw));
+    Gates* gt = reinterpret_cast<Gates*>(smem + GR_GATES);
+    GradSums* gs = reinterpret_cast<GradSums*>(smem + GR_GATES + sizeof(Gates));
+    if (!M3_SPAN(11, sb - su32(smem_raw), GR_GATES + sizeof(Gates) + sizeof(GradSums), dyn_smem_bytes())) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, P = q.headdim, H = q.nheads;
+    const int bh = blockIdx.x / nchunks, c = blockIdx.x % nchunks;
+    const int b = bh / H, h = bh % H, hpg = H / q.ngroups, g = h / hpg;
+    const int len = length_of(q, b), nt = min(kC, len - c * kC);
+    const int mt = warp & 3, nh = warp >> 2, qr = lane >> 2, qc = (lane & 3) * 2;
+    const long long ext_k = (long long)q.batch * q.seqlen * q.ngroups * kN, ext_v = (long long)q.batch * q.seqlen * H * P;
+    [[maybe_unused]] const long long toks = (long long)q.batch * q.seqlen * H;
+    const size_t row0 = (size_t)b * q.seqlen + c * kC;
+    const int rows = min(kC, q.seqlen - c * kC);               // rows of the outputs in this chunk
+    __nv_bfloat16* out_q = static_cast<__nv_bfloat16*>(q.dq);
+    __nv_bfloat16* out_k = static_cast<__nv_bfloat16*>(q.dk);
+    __nv_bfloat16* out_g = static_cast<__nv_bfloat16*>(q.dg);
+    __nv_bfloat16* out_b = static_cast<__nv_bfloat16*>(q.dbeta);
+    if (nt <= 0) {                                             // behind the end (a group's heads: the sum kernel's zeros)
+        if (hpg == 1) {
+            for (int e = tid; e < rows * 16; e += kThreads) {
+                const size_t o = ((row0 + (e >> 4)) * q.ngroups + g) * kN + 8 * (e & 15);
+                if (M3_SPAN(12, o, 8, ext_k)) {
+                    *reinterpret_cast<uint4*>(out_q + o) = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(out_k + o) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            if (tid < rows && M3_IN(13, (row0 + tid) * H + h, toks)) {
+                if (out_g) out_g[(row0 + tid) * H + h] = __float2bfloat16_rn(0.f);
+                out_b[(row0 + tid) * H + h] = __float2bfloat16_rn(0.f);
+            }
+        }
+        return;
+    }
+    const size_t rec0 = ((size_t)bh * q.nck + c) * rec_elems(P);
+    load_tokens(sb + GR_K, 8192, q.k, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
+    load_tokens(sb + GR_Q, 8192, q.q, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
+    if (warp == 0) make_gates(load_raw(q, b, h, len, c), gt);
+    const Mat K = {sb + GR_K, 8192}, Q = {sb + GR_Q, 8192}, dY = {sb + GR_DY, 0};
+    const Mat Uh = {sb + GR_U, 0}, Ul = {sb + GR_U + 8192, 0}, dRh = {sb + GR_DR, 0}, dRl = {sb + GR_DR + 8192, 0};
+    const Mat Sh = {sb + GR_S, 0}, Dh = {sb + GR_DS, 0};
+
+    float dP[4][4], dA[4][4], Z[8][4], X[8][4], Y[8][4];
+    zero<4>(dP); zero<4>(dA); zero<8>(Z); zero<8>(X); zero<8>(Y);
+    float dot = 0.f, drv = 0.f;                                // <S, dS'>, dR . v of row tid / 4
+    for (int sl = 0; sl < P / 64; ++sl) {
+        if (sl > 0) __syncthreads();
+        const size_t o = rec0 + kRecSlice + sl * kSliceElems;
+        load_tokens(sb + GR_DY, 0, q.dy, row0, (size_t)H * P, (size_t)h * P + 64 * sl, 8, nt, ext_v);
+        load_tokens(sb + GR_V, 0, q.v, row0, (size_t)H * P, (size_t)h * P + 64 * sl, 8, nt, ext_v);
+        load_rec(q, sb + GR_U, o + kSliceU, 128);
+        load_rec(q, sb + GR_DR, o + kSliceDR, 128);
+        load_rec(q, sb + GR_S, o + kSliceS, 256);
+        load_rec(q, sb + GR_DS, o + kSliceDS, 256);
+        cp_commit();
+        cp_wait();
+        __syncthreads();
+        mm<4, 64, false, true, true>(dP, dY, 16 * mt, Uh, 32 * nh, Ul.base, 32 * nh);
+        mm<4, 64, false, true, true>(dA, dRh, 16 * mt, Uh, 32 * nh, Ul.base, 32 * nh);
+        mm<4, 64, false, true, false>(dA, dRl, 16 * mt, Uh, 32 * nh, 0, 0);
+        mm<8, 64, false, true, true>(Z, dY, 16 * mt, Sh, 64 * nh, Sh.base + 16384, 64 * nh);
+        mm<8, 64, false, true, true>(X, dRh, 16 * mt, Sh, 64 * nh, Sh.base + 16384, 64 * nh);
+        mm<8, 64, false, true, false>(X, dRl, 16 * mt, Sh, 64 * nh, 0, 0);
+        mm<8, 64, false, true, true>(Y, Uh, 16 * mt, Dh, 64 * nh, Dh.base + 16384, 64 * nh);
+        mm<8, 64, false, true, false>(Y, Ul, 16 * mt, Dh, 64 * nh, 0, 0);
+        for (int e = tid; e < 128 * 8; e += kThreads) {
+            const uint32_t p = at(0, 0, e >> 3, e & 7);
+            const uint4 s0 = lds128(sb + GR_S + p), s1 = lds128(sb + GR_S + 16384 + p);
+            const uint4 d0 = lds128(sb + GR_DS + p), d1 = lds128(sb + GR_DS + 16384 + p);
+            const uint32_t sh[4] = {s0.x, s0.y, s0.z, s0.w}, s2[4] = {s1.x, s1.y, s1.z, s1.w};
+            const uint32_t dh[4] = {d0.x, d0.y, d0.z, d0.w}, d2[4] = {d1.x, d1.y, d1.z, d1.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 a = __fadd2_rn(unpack(sh[j]), unpack(s2[j])), d = __fadd2_rn(unpack(dh[j]), unpack(d2[j]));
+                dot = fmaf(a.x, d.x, fmaf(a.y, d.y, dot));
+            }
+        }
+#pragma unroll
+        for (int j2 = 0; j2 < 2; ++j2) {
+            const uint32_t p = at(0, 0, tid >> 2, 2 * (tid & 3) + j2);
+            const uint4 r0 = lds128(dRh.base + p), r1 = lds128(dRl.base + p), v0 = lds128(sb + GR_V + p);
+            const uint32_t rh[4] = {r0.x, r0.y, r0.z, r0.w}, rl[4] = {r1.x, r1.y, r1.z, r1.w}, vv[4] = {v0.x, v0.y, v0.z, v0.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 d = __fadd2_rn(unpack(rh[j]), unpack(rl[j])), v = unpack(vv[j]);
+                drv = fmaf(d.x, v.x, fmaf(d.y, v.y, drv));
+            }
+        }
+    }
+    float kk[4][4];
+    zero<4>(kk);
+    mm<4, 128, false, true, false>(kk, K, 16 * mt, K, 32 * nh, 0, 0);
+    __syncthreads();                                           // S has been read: its place takes dP and D
+    drv += __shfl_xor_sync(kFull, drv, 1);
+    drv += __shfl_xor_sync(kFull, drv, 2);
+    if ((tid & 3) == 0) gs->drv[tid >> 2] = drv;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+    if (lane == 0) gs->dot[warp] = dot;
+
+    float rowG[2] = {0.f, 0.f}, rowB[2] = {0.f, 0.f}, tail[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const int j = 32 * nh + 8 * n + qc;
+        float cs[2] = {0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int i = 16 * mt + qr + 8 * r;
+            const float2 Gi = gt->G[i];
+            const float be = gt->beta[i];
+            float2 fq, fk;
+            const size_t o = rec0 + kRecP + i * 64 + j;
+            float2 pv = make_float2(0.f, 0.f);
+            if (M3_SPAN(14, o + kTok, 2, ext_rec(q)))
+                pv = __fadd2_rn(unpack(*reinterpret_cast<const uint32_t*>(q.rec + o)),
+                                unpack(*reinterpret_cast<const uint32_t*>(q.rec + o + kTok)));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float gam = i >= j + e ? ex2(diff_pair(Gi, gt->G[j + e])) : 0.f;
+                const float dp = i >= j + e ? dP[n][2 * r + e] : 0.f;
+                const float da = i > j + e ? -dA[n][2 * r + e] * gam : 0.f;
+                const float t = da * kk[n][2 * r + e];
+                const float E = fmaf(dp, e ? pv.y : pv.x, be * t);
+                rowG[r] += E;
+                cs[e] += E;
+                rowB[r] += t;
+                (e ? fq.y : fq.x) = q.scale * gam * dp;
+                (e ? fk.y : fk.x) = be * da;
+            }
+            sts32(elem(sb + GR_DQK, i, j), take2(fq));
+            sts32(elem(sb + GR_DQK + 8192, i, j), pack_bf16x2(fq.x, fq.y));
+            sts32(elem(sb + GR_DKK, i, j), take2(fk));
+            sts32(elem(sb + GR_DKK + 8192, i, j), pack_bf16x2(fk.x, fk.y));
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) cs[e] += __shfl_xor_sync(kFull, cs[e], o);
+            if (qr == 0) gs->col[mt][j + e] = cs[e];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int i = 16 * mt + qr + 8 * r;
+        const float a = gt->a[i], tl = gt->at[i], be = gt->beta[i], sa = q.scale * a, ba = be * a;
+        float zq = 0.f, xk = 0.f, yk = 0.f;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const int col = 64 * nh + 8 * n + qc;
+            const uint32_t p = at(0, 8192, i, col >> 3) + (col & 7) * 2;
+            const float2 qv = unpack(lds32(sb + GR_Q + p)), kv = unpack(lds32(sb + GR_K + p));
+            zq = fmaf(Z[n][2 * r], qv.x, fmaf(Z[n][2 * r + 1], qv.y, zq));
+            xk = fmaf(X[n][2 * r], kv.x, fmaf(X[n][2 * r + 1], kv.y, xk));
+            yk = fmaf(Y[n][2 * r], kv.x, fmaf(Y[n][2 * r + 1], kv.y, yk));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                Z[n][2 * r + e] *= sa;
+                Y[n][2 * r + e] = fmaf(tl, Y[n][2 * r + e], -ba * X[n][2 * r + e]);
+            }
+        }
+        rowG[r] += sa * zq - ba * xk - tl * yk;
+        rowB[r] -= a * xk;
+        tail[r] = tl * yk;
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            rowG[r] += __shfl_xor_sync(kFull, rowG[r], o);
+            rowB[r] += __shfl_xor_sync(kFull, rowB[r], o);
+            tail[r] += __shfl_xor_sync(kFull, tail[r], o);
+        }
+        if ((lane & 3) == 0) {
+            gs->row[nh][i] = rowG[r];
+            gs->beta[nh][i] = rowB[r];
+            gs->tail[nh][i] = tail[r];
+        }
+    }
+    __syncthreads();
+    const Mat Pq = {sb + GR_DQK, 0}, Pq2 = {sb + GR_DQK + 8192, 0}, Dk = {sb + GR_DKK, 0}, Dk2 = {sb + GR_DKK + 8192, 0};
+    mm<8, 64, false, false, false>(Z, Pq, 16 * mt, K, 64 * nh, 0, 0);
+    mm<8, 64, false, false, false>(Z, Pq2, 16 * mt, K, 64 * nh, 0, 0);
+    mm<8, 64, true, false, false>(Y, Pq, 16 * mt, Q, 64 * nh, 0, 0);
+    mm<8, 64, true, false, false>(Y, Pq2, 16 * mt, Q, 64 * nh, 0, 0);
+    mm<8, 64, false, false, false>(Y, Dk, 16 * mt, K, 64 * nh, 0, 0);
+    mm<8, 64, false, false, false>(Y, Dk2, 16 * mt, K, 64 * nh, 0, 0);
+    mm<8, 64, true, false, false>(Y, Dk, 16 * mt, K, 64 * nh, 0, 0);
+    mm<8, 64, true, false, false>(Y, Dk2, 16 * mt, K, 64 * nh, 0, 0);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int i = 16 * mt + qr + 8 * r;
+        const float m = i < nt ? 1.f : 0.f;
+        if (i >= rows) continue;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const int col = 64 * nh + 8 * n + qc;
+            const float2 vq = make_float2(m * Z[n][2 * r], m * Z[n][2 * r + 1]), vk = make_float2(m * Y[n][2 * r], m * Y[n][2 * r + 1]);
+            if (hpg == 1) {
+                const size_t o = ((row0 + i) * q.ngroups + g) * kN + col;
+                if (M3_SPAN(15, o, 2, ext_k)) {
+                    *reinterpret_cast<uint32_t*>(out_q + o) = pack_bf16x2(vq.x, vq.y);
+                    *reinterpret_cast<uint32_t*>(out_k + o) = pack_bf16x2(vk.x, vk.y);
+                }
+            } else {
+                const size_t o = ((row0 + i) * H + h) * 2 * kN + col;
+                if (M3_SPAN(16, o + kN, 2, toks * 2 * kN)) {
+                    *reinterpret_cast<float2*>(q.part_qk + o) = vq;
+                    *reinterpret_cast<float2*>(q.part_qk + o + kN) = vk;
+                }
+            }
+        }
+    }
+    if (warp == 0) {
+        // lane l has tokens 2 l, 2 l + 1; dg is the sum from a token to the chunk's end
+        float d[2], tl = 0.f, total = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 2 * lane + e;
+            d[e] = gs->row[0][i] + gs->row[1][i] - (gs->col[0][i] + gs->col[1][i] + gs->col[2][i] + gs->col[3][i]);
+            tl += gs->tail[0][i] + gs->tail[1][i];
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) tl += __shfl_xor_sync(kFull, tl, o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) total += gs->dot[j];
+        tl += gt->whole * total;
+        float sum = d[0] + d[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float u = __shfl_down_sync(kFull, sum, o);
+            if (lane + o < 32) sum += u;
+        }
+        const float dg[2] = {sum + tl, sum - d[0] + tl};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 2 * lane + e;
+            const size_t o = (row0 + i) * H + h;
+            if (i >= rows || !M3_IN(17, o, toks)) continue;
+            const float vg = i < nt ? dg[e] : 0.f;
+            const float vb = i < nt ? gs->drv[i] + gs->beta[0][i] + gs->beta[1][i] : 0.f;
+            if (hpg == 1) {
+                if (out_g) out_g[o] = __float2bfloat16_rn(vg);
+                out_b[o] = __float2bfloat16_rn(vb);
+            } else {
+                q.part_g[2 * o] = vg;
+                q.part_g[2 * o + 1] = vb;
+            }
+        }
+    }
+}
+
+}  // namespace dbw
+
+size_t delta_record_bytes(const m3_dims& d) { return dtc::rec_elems(d.headdim) * 2; }
+
+cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st) {
+    using namespace dbw;
+    DeltaParams f = q;                       // records of the prefill
+    f.y = nullptr;
+    f.final_h = nullptr;
+    cudaError_t e = launch_delta_tc(d, f, status, st);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(delta_rev_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RV_BYTES);
+    if (e != cudaSuccess) return e;
+    const long long bh = (long long)d.batch * d.nheads;
+    delta_rev_kernel<<<(unsigned)(bh * (d.headdim / kPS)), dbw::kThreads, RV_BYTES, st>>>(q);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_BYTES);
+    if (e != cudaSuccess) return e;
+    delta_grad_kernel<<<(unsigned)(bh * q.nck), dbw::kThreads, GR_BYTES, st>>>(q, q.nck);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || d.nheads == d.ngroups) return e;
+    return launch_delta_reduce(d, q, 1, st);
+}
+
+}  // namespace m3
+
+M3_BOUNDS_EXPORT(delta_bwd_tc)

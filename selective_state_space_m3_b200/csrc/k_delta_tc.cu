@@ -44,8 +44,7 @@
 #include "m3_bounds.cuh"
 #include <stdlib.h>
 
-#include "m3_kernels.h"
-#include "tc_ptx.cuh"
+#include "delta_tc.cuh"
 
 namespace m3 {
 
@@ -53,15 +52,10 @@ bool make_tile_map(CUtensorMap* map, const void* base, int inner, int R, int grp
 
 namespace dtc {
 
-using namespace ptx;
-
-constexpr int kC = 64;             // tokens a chunk
-constexpr int kN = 128;
 constexpr int kP = 64;             // columns of a V tile; a CTA takes PC = 64, 32 or 16 of them
 constexpr int kState = 256;        // threads of the chain
 constexpr int kPrep = 128;         // threads of one of the two groups that make T
 constexpr int kThreads = 32 + kState + 2 * kPrep + 32;
-constexpr unsigned kFull = 0xffffffffu;
 
 constexpr int OFF_KQ = 0;                       // 3 x 32 KB: two 64-column atoms, rows 0..63 K, 64..127 Q
 constexpr int OFF_V = OFF_KQ + 3 * 32768;       // 2 x 8 KB
@@ -79,14 +73,6 @@ constexpr int OFF_MISC = OFF_SCR + 2 * SCR_BYTES;
 // one Gram product a group
 constexpr uint32_t D_KS = 0, D_S = 0, D_TR = 192, D_G = 320;
 
-struct Gates {
-    float2 G[kC];                  // sum of g in log2 units, as a sum of two floats
-    float a[kC], at[kC], beta[kC]; // e^G, e^{G_C - G}, beta (0 behind the end)
-    float mid[kC];                 // j < 32: e^{G_31 - G_j}; i >= 32: e^{G_i - G_31}
-    float whole;                   // e^{G_C}
-    float pad[3];
-};
-
 struct Misc {
     uint64_t kq_full[3], kq_free[3], v_full[2], v_free[2], t_full[2], x_free[2], g[2];
     uint64_t s_ready, ks, r, tr, u, s, o, drain[3];
@@ -101,13 +87,6 @@ __device__ __forceinline__ bool wait(uint64_t* b, int phase, Misc* m, int* statu
     return mbar_wait_flag(b, (uint32_t)(phase & 1), &m->abort_flag, status, where);
 }
 __device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, %1;" ::"r"(2 + group), "n"(kPrep) : "memory"); }
-__device__ __forceinline__ float clamp_g(float g) { return g < -1.0e4f ? -1.0e4f : g; }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Products and commits by one elected lane of a converged warp: the warp runs
 // the loop as one, so that descriptors stay in uniform registers (measured:
 // 47 cycles a 128 x 64 x 16 product instead of 97 from a divergent lane).
@@ -128,19 +107,6 @@ __device__ __forceinline__ void commit_one(uint64_t* bar) {
         : "memory");
 }
 
-// two floats -> two bfloat16 (returned), f becomes what the rounding left
-__device__ __forceinline__ uint32_t take2(float2& f) {
-    const uint32_t w = pack_bf16x2(f.x, f.y);
-    f = __ffma2_rn(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), make_float2(-1.f, -1.f), f);
-    return w;
-}
-__device__ __forceinline__ uint4 take8(float2* f) {
-    return make_uint4(take2(f[0]), take2(f[1]), take2(f[2]), take2(f[3]));
-}
-__device__ __forceinline__ uint4 round8(const float2* f) {
-    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
-                      pack_bf16x2(f[3].x, f[3].y));
-}
 // 16 bytes at `off` of the tile that starts at `tile` and has `limit` bytes
 __device__ __forceinline__ void put16(uint8_t* smem, int tile, uint32_t off, int limit, uint4 v) {
     if (M3_SPAN(1, off, 16, limit)) *reinterpret_cast<uint4*>(smem + tile + off) = v;
@@ -164,65 +130,6 @@ __device__ __forceinline__ Where where_am_i(const DeltaParams& q) {
     w.len = len;
     w.nch = (len + kC - 1) / kC;
     return w;
-}
-
-// a + b of sums of two floats (each a pair with a small second part)
-__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
-    const float s = a.x + b.x, t = s - a.x;
-    const float e = (a.x - (s - t)) + (b.x - t) + (a.y + b.y);
-    const float r = s + e;
-    return make_float2(r, e - (r - s));
-}
-__device__ __forceinline__ float diff_pair(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); }
-
-// g and beta of a chunk: lane l holds tokens 2 l and 2 l + 1
-struct Raw {
-    float g[2], beta[2];
-};
-__device__ __forceinline__ Raw load_raw(const DeltaParams& q, const Where& w, int c) {
-    const int lane = threadIdx.x & 31;
-    Raw r;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int t = c * kC + 2 * lane + j;
-        const size_t o = ((size_t)w.b * q.seqlen + t) * q.nheads + w.h;
-        const bool ok = t < w.len && M3_IN(4, o, (long long)q.batch * q.seqlen * q.nheads);
-        r.g[j] = (ok && q.g) ? __ldg(q.g + o) : 0.f;
-        r.beta[j] = ok ? __ldg(q.beta + o) : 0.f;
-    }
-    return r;
-}
-// Sums of g in log2 units.  They run as pairs of floats, so that differences
-// keep float32 accuracy after strong decay.
-__device__ __forceinline__ void make_gates(const Raw& raw, Gates* out) {
-    const int lane = threadIdx.x & 31;
-    constexpr float kHi = 1.44269502162933349609f, kLo = 1.92596299112661746887e-8f;    // log2 e
-    float2 d[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const float g = clamp_g(raw.g[j]);
-        const float p = g * kHi;
-        d[j] = make_float2(p, fmaf(g, kHi, -p) + g * kLo);
-    }
-    float2 sum = add_pair(d[0], d[1]);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const float2 u = make_float2(__shfl_up_sync(kFull, sum.x, o), __shfl_up_sync(kFull, sum.y, o));
-        if (lane >= o) sum = add_pair(sum, u);
-    }
-    const float2 total = make_float2(__shfl_sync(kFull, sum.x, 31), __shfl_sync(kFull, sum.y, 31));
-    const float2 mid = make_float2(__shfl_sync(kFull, sum.x, 15), __shfl_sync(kFull, sum.y, 15));
-    const float2 G[2] = {add_pair(sum, make_float2(-d[1].x, -d[1].y)), sum};
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int i = 2 * lane + j;
-        out->G[i] = G[j];
-        out->a[i] = ex2(G[j].x + G[j].y);
-        out->at[i] = ex2(diff_pair(total, G[j]));
-        out->beta[i] = raw.beta[j];
-        out->mid[i] = ex2(i < 32 ? diff_pair(mid, G[j]) : diff_pair(G[j], mid));
-    }
-    if (lane == 0) out->whole = ex2(total.x + total.y);
 }
 
 // column `lane` of the inverse of a unit lower triangular 32 x 32 matrix whose
@@ -372,7 +279,8 @@ __device__ __forceinline__ uint32_t part_at(int row, int part, int ch, int tile_
     return (uint32_t)((col >> 3) * tile_bytes) + sw128(row, col & 7);
 }
 
-template <int PC>
+// DUMP: also write the records that the gradient's passes read
+template <int PC, bool DUMP>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmV, DeltaParams q, int* status) {
@@ -490,18 +398,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             S[2 * c4] = make_float2(v.x, v.y);
             S[2 * c4 + 1] = make_float2(v.z, v.w);
         }
-        auto store_state = [&]() {                 // S hi, S lo
+        // this CTA's columns in a record, and this thread's first one
+        auto slice_of = [&](int c) {
+            return q.rec + (bh * q.nck + c) * rec_elems(P) + kRecSlice + (size_t)(w.p0 >> 6) * kSliceElems + (w.p0 & 63) + c0;
+        };
+        auto keep = [&](__nv_bfloat16* dst, int ch, uint4 v) {
+            if (M3_SPAN(10, dst + 8 * ch - q.rec, 8, (long long)q.batch * q.nheads * q.nck * rec_elems(P)))
+                *reinterpret_cast<uint4*>(dst + 8 * ch) = v;
+        };
+        auto store_state = [&](int c) {            // S hi, S lo before chunk c
 #pragma unroll
             for (int ch = 0; ch < NG; ++ch) {
                 float2 f[4] = {S[4 * ch], S[4 * ch + 1], S[4 * ch + 2], S[4 * ch + 3]};
-                put16(smem, OFF_S, part_at<PC>(row, 0, ch0 + ch, 16384), 32768, take8(f));
-                put16(smem, OFF_S, part_at<PC>(row, 1, ch0 + ch, 16384), 32768, round8(f));
+                const uint4 hi = take8(f), lo = round8(f);
+                put16(smem, OFF_S, part_at<PC>(row, 0, ch0 + ch, 16384), 32768, hi);
+                put16(smem, OFF_S, part_at<PC>(row, 1, ch0 + ch, 16384), 32768, lo);
+                if (DUMP) {
+                    keep(slice_of(c) + kSliceS + row * 64, ch, hi);
+                    keep(slice_of(c) + kSliceS + kSt + row * 64, ch, lo);
+                }
             }
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(&m->s_ready);
         };
-        if (w.nch > 0) store_state();
+        if (w.nch > 0) store_state(0);
 #pragma unroll 1
         for (int c = 0; c < w.nch; ++c) {
             const Gates* gt = &m->gates[c & 3];
@@ -558,6 +479,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int ch = 0; ch < W / 8; ++ch) {
                         const int cc = ch0 + W / 8 * hh + ch;
                         put16(smem, OFF_UB, sw128(tok, cc), 8192, round8(f + 4 * ch));
+                        if (DUMP) {
+                            float2 e[4] = {f[4 * ch], f[4 * ch + 1], f[4 * ch + 2], f[4 * ch + 3]};
+                            keep(slice_of(c) + kSliceU + tok * 64, W / 8 * hh + ch, take8(e));
+                            keep(slice_of(c) + kSliceU + kTok + tok * 64, W / 8 * hh + ch, round8(e));
+                        }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) f[4 * ch + j] = __fmul2_rn(at2, f[4 * ch + j]);
                         put16(smem, OFF_U, part_at<PC>(tok, 0, cc, 8192), 24576, take8(f + 4 * ch));
@@ -601,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // S takes the place of the U that P U reads
             wait(&m->o, c, m, status, 17);
             __syncwarp();
-            if (c + 1 < w.nch) store_state();
+            if (c + 1 < w.nch) store_state(c + 1);
             if (!top) {
                 tc_fence_after();
                 const size_t o = (((size_t)w.b * q.seqlen + c * kC + tok) * q.nheads + w.h) * P + w.p0 + c0;
@@ -613,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_sum<W, 1>(tl + D_TR + PC + W * hh, PC, f);
 #pragma unroll
                     for (int j = 0; j < W / 2; ++j) f[j] = __fadd2_rn(buf[W / 2 * hh + j], f[j]);
-                    if (in) {
+                    if (!DUMP && in) {
 #pragma unroll
                         for (int ch = 0; ch < W / 8; ++ch) dst[W / 8 * hh + ch] = round8(f + 4 * ch);
                     }
@@ -637,8 +563,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int xo = OFF_X + group * 16384, lo = OFF_TL + group * 8192;
         const int tok = row & 63, blk = quarter & 1;       // the row's token; its 32-token block
         constexpr uint32_t idG = idesc_bf16(128, 64, 0, 0);
+        // T and P of the records (one CTA of a head writes them)
+        auto keep = [&](size_t at, int c, int r, int ch, uint4 v) {
+            const size_t o = (bh * q.nck + c) * rec_elems(P) + at + r * 64 + ch * 8;
+            if (w.p0 == 0 && M3_SPAN(11, o, 8, (long long)q.batch * q.nheads * q.nck * rec_elems(P)))
+                *reinterpret_cast<uint4*>(q.rec + o) = v;
+        };
+        // P rows of tokens behind the end (other data, possibly not numbers) are recorded as zeros
+        auto keep_p = [&](int c, int tok, int ch, float2* f, bool live) {
+            if (!live) f[0] = f[1] = f[2] = f[3] = make_float2(0.f, 0.f);
+            keep(kRecP, c, tok, ch, take8(f));
+            keep(kRecP + kTok, c, tok, ch, round8(f));
+        };
         Raw raw = {};
-        if (quarter == 2) raw = load_raw(q, w, group);
+        if (quarter == 2) raw = load_raw(q, w.b, w.h, w.len, group);
         for (int c = group; c < w.nch; c += 2) {
             const int kqo = OFF_KQ + (c % 3) * 32768;
             const int nt = min(kC, w.len - c * kC);
@@ -669,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // left before the products of chunk c - 3 freed this chunk's K and Q
             if (quarter == 2) {
                 make_gates(raw, gt);
-                raw = load_raw(q, w, c + 2);       // the group's next
+                raw = load_raw(q, w.b, w.h, w.len, c + 2);       // the group's next
             }
             group_sync(group);
             wait(&m->g[group], c >> 1, m, status, 22);
@@ -699,11 +637,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 } else {
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) put16(smem, xo, sw128(row, ch), 16384, round8(e + 4 * ch));
+                    for (int ch = 0; ch < 4; ++ch) {
+                        put16(smem, xo, sw128(row, ch), 16384, round8(e + 4 * ch));
+                        if (DUMP) keep_p(c, tok, ch, e + 4 * ch, tok < nt);
+                    }
                 }
             } else if (row >= 64) {
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) put16(smem, xo, sw128(row, 4 + ch), 16384, make_uint4(0u, 0u, 0u, 0u));
+                for (int ch = 0; ch < 4; ++ch) {
+                    put16(smem, xo, sw128(row, 4 + ch), 16384, make_uint4(0u, 0u, 0u, 0u));
+                    if (DUMP) {
+                        keep(kRecP, c, tok, 4 + ch, make_uint4(0u, 0u, 0u, 0u));
+                        keep(kRecP + kTok, c, tok, 4 + ch, make_uint4(0u, 0u, 0u, 0u));
+                    }
+                }
             }
             {                                              // the diagonal block
                 float d[32];
@@ -725,7 +672,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 } else {
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) put16(smem, xo, sw128(row, 4 * blk + ch), 16384, round8(e + 4 * ch));
+                    for (int ch = 0; ch < 4; ++ch) {
+                        put16(smem, xo, sw128(row, 4 * blk + ch), 16384, round8(e + 4 * ch));
+                        if (DUMP) keep_p(c, tok, 4 * blk + ch, e + 4 * ch, tok < nt);
+                    }
                 }
             }
             tc_fence_before();
@@ -764,8 +714,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     t[j] = make_float2(8 * ch + 2 * j == r ? 0.f : tv[2 * j], 8 * ch + 2 * j + 1 == r ? 0.f : tv[2 * j + 1]);
-                put16(smem, xo, sw128(r, ch), 16384, take8(t));
-                put16(smem, lo, sw128(r, ch), 8192, round8(t));
+                auto put_t = [&](int row_, int ch_, float2* f) {
+                    const uint4 h8 = take8(f), l8 = round8(f);
+                    put16(smem, xo, sw128(row_, ch_), 16384, h8);
+                    put16(smem, lo, sw128(row_, ch_), 8192, l8);
+                    if (DUMP) {
+                        keep(kRecT, c, row_, ch_, h8);
+                        keep(kRecT + kTok, c, row_, ch_, l8);
+                    }
+                };
+                put_t(r, ch, t);
+                if (DUMP) {
+                    keep(kRecT, c, r, 4 + ch, make_uint4(0u, 0u, 0u, 0u));
+                    keep(kRecT + kTok, c, r, 4 + ch, make_uint4(0u, 0u, 0u, 0u));
+                }
                 float s8[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -774,8 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) t[j] = make_float2(s8[2 * j], s8[2 * j + 1]);
-                put16(smem, xo, sw128(32 + r, 4 + ch), 16384, take8(t));
-                put16(smem, lo, sw128(32 + r, 4 + ch), 8192, round8(t));
+                put_t(32 + r, 4 + ch, t);
                 group_sync(group);                         // A21 has been read
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -789,6 +750,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float n = (i & 1) ? acc[i >> 1].y : acc[i >> 1].x;
                     const uint32_t o = (uint32_t)((32 + r0 + i) * 128 + (((lane >> 3) ^ i) << 4) + (lane & 7) * 2);   // (row & 7 = i)
                     const __nv_bfloat16 hi = __float2bfloat16_rn(n);
+                    if (DUMP && w.p0 == 0) {
+                        const size_t at = (bh * q.nck + c) * rec_elems(P) + (32 + r0 + i) * 64 + lane;
+                        if (M3_IN(12, at + kTok, (long long)q.batch * q.nheads * q.nck * rec_elems(P))) {
+                            q.rec[at] = hi;
+                            q.rec[at + kTok] = __float2bfloat16_rn(n - __bfloat162float(hi));
+                        }
+                    }
                     if (M3_SPAN(2, o, 2, 8192)) {
                         *reinterpret_cast<__nv_bfloat16*>(smem + xo + o) = hi;
                         *reinterpret_cast<__nv_bfloat16*>(smem + lo + o) = __float2bfloat16_rn(n - __bfloat162float(hi));
@@ -841,14 +809,14 @@ bool delta_tc_eligible(const m3_dims& d) {
     return d.io_dtype == M3_BF16 && d.dstate == dtc::kN && d.headdim % dtc::kP == 0;
 }
 
-template <int PC>
+template <int PC, bool DUMP>
 static cudaError_t launch_pc(const CUtensorMap& mK, const CUtensorMap& mQ, const CUtensorMap& mV, const m3_dims& d,
                              const DeltaParams& q, int* status, cudaStream_t st) {
     using namespace dtc;
-    const cudaError_t e = cudaFuncSetAttribute(delta_tc_kernel<PC>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    const cudaError_t e = cudaFuncSetAttribute(delta_tc_kernel<PC, DUMP>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((long long)d.batch * d.nheads * (d.headdim / PC));
-    delta_tc_kernel<PC><<<grid, kThreads, SMEM_BYTES, st>>>(mK, mQ, mV, q, status);
+    delta_tc_kernel<PC, DUMP><<<grid, kThreads, SMEM_BYTES, st>>>(mK, mQ, mV, q, status);
     return cudaGetLastError();
 }
 
@@ -859,12 +827,17 @@ cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, int* status,
         !make_tile_map(&mQ, q.q, kN, 1, d.ngroups, d.seqlen, d.batch, kC) ||
         !make_tile_map(&mV, q.v, d.headdim, 1, d.nheads, d.seqlen, d.batch, kC))
         return cudaErrorInvalidValue;
-    // columns a CTA
+    // columns a CTA: all 64 of a tile where the sequences fill the SMs, else
+    // fewer, so that the heads are spread over more of them
     const char* env = getenv("M3_DTC_PC");
-    const int pc = env ? atoi(env) : 64;
-    if (pc == 64) return launch_pc<64>(mK, mQ, mV, d, q, status, st);
-    if (pc == 32) return launch_pc<32>(mK, mQ, mV, d, q, status, st);
-    return launch_pc<16>(mK, mQ, mV, d, q, status, st);
+    const int pc = env ? atoi(env) : q.rec ? 32 : 64;
+    if (q.rec) {
+        if (pc == 64) return launch_pc<64, true>(mK, mQ, mV, d, q, status, st);
+        return launch_pc<32, true>(mK, mQ, mV, d, q, status, st);
+    }
+    if (pc == 64) return launch_pc<64, false>(mK, mQ, mV, d, q, status, st);
+    if (pc == 32) return launch_pc<32, false>(mK, mQ, mV, d, q, status, st);
+    return launch_pc<16, false>(mK, mQ, mV, d, q, status, st);
 }
 
 }  // namespace m3

@@ -27,6 +27,7 @@ cudaError_t bounds_take_phase(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_scan_ws(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_delta(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_delta_tc(BoundsRecord* out, bool clear);
+cudaError_t bounds_take_delta_bwd_tc(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_norm(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_api(BoundsRecord* out, bool clear);
 
@@ -641,7 +642,8 @@ static m3_status check_delta(const m3_dims* d, bool need_seq) {
     // launch grids are one-dimensional
     const long long kMax = 0x7fffffffLL, bh = (long long)d->batch * d->nheads;
     if (bh > kMax || bh * delta_tiles(*d) > kMax) return M3_ERR_UNSUPPORTED;
-    if (need_seq && (long long)d->batch * d->seqlen * d->ngroups > kMax) return M3_ERR_UNSUPPORTED;
+    if (need_seq && ((long long)d->batch * d->seqlen * d->ngroups > kMax || bh * ((d->seqlen + 63LL) / 64) > kMax))
+        return M3_ERR_UNSUPPORTED;
     return M3_OK;
 }
 
@@ -713,18 +715,25 @@ m3_status m3_delta_step(const m3_dims* d, const float* h_in, float* h_out, const
 }
 
 struct DeltaBwdLayout {
+    bool chunked;
     int KB, nck;
-    size_t ckpt, part_qk, part_g, total;
+    size_t ckpt, rec, part_qk, part_g, total;
 };
 
+// Token path: a state a checkpoint, and every column tile's parts of dq, dk,
+// dg, dbeta.  Chunked path: a record a chunk, and, where heads share keys,
+// every head's parts.
 static DeltaBwdLayout delta_bwd_layout(const m3_dims& d) {
     DeltaBwdLayout l;
-    l.KB = delta_block_tokens(d);
+    l.chunked = delta_chunked(d);
+    l.KB = l.chunked ? 64 : delta_block_tokens(d);
     l.nck = d.seqlen > 0 ? (int)(((long long)d.seqlen + l.KB - 1) / l.KB) : 0;
     const size_t units = (size_t)d.batch * d.nheads, NP = (size_t)d.dstate * d.headdim;
-    const size_t toks = units * d.seqlen * delta_tiles(d);
+    const size_t tiles = !l.chunked ? delta_tiles(d) : d.nheads == d.ngroups ? 0 : 1;
+    const size_t toks = units * d.seqlen * tiles;
     size_t off = kWorkspaceHeaderBytes;
-    l.ckpt = off;    off = round256(off + units * l.nck * NP * sizeof(float));
+    l.ckpt = off;    off = round256(off + (l.chunked ? 0 : units * l.nck * NP * sizeof(float)));
+    l.rec = off;     off = round256(off + (l.chunked ? units * l.nck * delta_record_bytes(d) : 0));
     l.part_qk = off; off = round256(off + toks * 2 * d.dstate * sizeof(float));
     l.part_g = off;  off = round256(off + toks * 2 * sizeof(float));
     l.total = off;
@@ -765,7 +774,10 @@ m3_status m3_delta_bwd(const m3_dims* d, const void* q, const void* k, const voi
     p.ckpt = reinterpret_cast<float*>(ws + l.ckpt);
     p.part_qk = reinterpret_cast<float*>(ws + l.part_qk);
     p.part_g = reinterpret_cast<float*>(ws + l.part_g);
-    return launch_delta_seq_bwd(*d, p, st) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+    p.rec = reinterpret_cast<__nv_bfloat16*>(ws + l.rec);
+    const cudaError_t e = l.chunked ? launch_delta_bwd_tc(*d, p, static_cast<int*>(workspace), st)
+                                    : launch_delta_seq_bwd(*d, p, st);
+    return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }
 
 // -------------------------------------------------- root-mean-square norm --
@@ -835,7 +847,7 @@ m3_status m3_debug_bounds_report(m3_bounds_report* out, int clear) {
     const Take takes[] = {bounds_take_scan_tc, bounds_take_scan_simt, bounds_take_step,
                           bounds_take_rope,    bounds_take_seq,       bounds_take_bwd,
                           bounds_take_phase,   bounds_take_scan_ws,   bounds_take_delta,
-                          bounds_take_delta_tc, bounds_take_norm,    bounds_take_api};
+                          bounds_take_delta_tc, bounds_take_delta_bwd_tc, bounds_take_norm,    bounds_take_api};
     out->enabled = 1;
     if (cudaDeviceSynchronize() != cudaSuccess) return M3_ERR_CUDA;
     for (Take take : takes) {
