@@ -64,8 +64,11 @@ constexpr int OFF_U = OFF_S;                    // R hi, lo; then e^{G_C-G} U in
 constexpr int OFF_UB = OFF_S + 24576;           // U rounded, for P U
 constexpr int OFF_X = OFF_S + 32768;            // 2 x 16 KB: [T - I hi; P]
 constexpr int OFF_TL = OFF_X + 2 * 16384;       // 2 x 8 KB: T - I lo (its operand reads 64 more rows, unused)
-constexpr int OFF_SCR = OFF_TL + 2 * 8192;      // of each group: A11 / T11, A22 / T22, A21 / A21 T11 (4 KB each)
-constexpr int SCR_BYTES = 3 * 4096;
+constexpr int OFF_SCR = OFF_TL + 2 * 8192;      // of each group:
+constexpr int SCR_D = 0;                        //   4 KB: A's 16 x 16 diagonal blocks, float32, by columns
+constexpr int SCR_21 = 4096;                    //   4 KB: A's lower left 32 x 32 block, hi and lo side by side
+constexpr int SCR_10 = 8192;                    //   2 KB: its two 16 x 16 blocks under the diagonal, hi, lo, hi, lo
+constexpr int SCR_BYTES = 10240;
 constexpr int OFF_MISC = OFF_SCR + 2 * SCR_BYTES;
 
 // TMEM columns: K S, Q S against [S hi | S lo] and, once they are read, the
@@ -78,7 +81,7 @@ struct Misc {
     uint64_t s_ready, ks, r, tr, u, s, o, drain[3];
     uint32_t tmem_base;
     int abort_flag, drain_flag, pad;
-    Gates gates[4];
+    Gates gates[5];
 };
 constexpr int SMEM_BYTES = OFF_MISC + (int)sizeof(Misc) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory of the delta kernel");
@@ -132,47 +135,146 @@ __device__ __forceinline__ Where where_am_i(const DeltaParams& q) {
     return w;
 }
 
-// column `lane` of the inverse of a unit lower triangular 32 x 32 matrix whose
-// strict lower part is at[col * 32 + row]: x starts as the unit vector, and a
-// finished x_i takes A_ri x_i off every later x_r
-__device__ __forceinline__ void invert32(const float* at, float2* x) {
+// column `lane` (< 16) of the inverse of a unit lower triangular 16 x 16 matrix
+// whose strict lower part is at[col * 16 + row] (zeros elsewhere): x starts as
+// the unit vector, and a finished x_i takes A_ri x_i off every later x_r
+__device__ __forceinline__ void invert16(const float* at, float2* x) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = make_float2(2 * i == lane ? 1.f : 0.f, 2 * i + 1 == lane ? 1.f : 0.f);
+    for (int i = 0; i < 8; ++i) x[i] = make_float2(2 * i == lane ? 1.f : 0.f, 2 * i + 1 == lane ? 1.f : 0.f);
 #pragma unroll
-    for (int i = 0; i < 31; ++i) {
+    for (int i = 0; i < 15; ++i) {
         const float xi = (i & 1) ? -x[i >> 1].y : -x[i >> 1].x;
         const float2 x2 = make_float2(xi, xi);
 #pragma unroll
-        for (int r4 = (i + 1) / 4; r4 < 8; ++r4) {
-            const float4 v = *reinterpret_cast<const float4*>(at + i * 32 + 4 * r4);
-            // rows up to i are finished: the strict upper part and the diagonal
-            // of `at` hold zeros, so they stay
+        for (int r4 = (i + 1) / 4; r4 < 4; ++r4) {
+            const float4 v = *reinterpret_cast<const float4*>(at + i * 16 + 4 * r4);
             if (4 * r4 + 1 > i) x[2 * r4] = __ffma2_rn(make_float2(v.x, v.y), x2, x[2 * r4]);
             x[2 * r4 + 1] = __ffma2_rn(make_float2(v.z, v.w), x2, x[2 * r4 + 1]);
         }
     }
 }
 
-// 8 rows r0.. of (left, columns contiguous) x (right, rows contiguous) at column
-// `lane`; SW: the left matrix is stored with its 16-byte blocks exchanged
-template <bool SW>
-__device__ __forceinline__ void product32(const float* left, const float* right, int r0, float2* acc) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t* r) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// accumulators of two 8-column tiles as the left operand of the next product, hi and lo
+__device__ __forceinline__ void split_acc(const float (*c)[4], uint32_t* hi, uint32_t* lo) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.f, 0.f);
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k) {
-        const float t = right[k * 32 + lane];
-        const float2 t2 = make_float2(t, t);
-        const int b0 = r0 >> 2, sw = SW ? (k & 7) : 0;
-        const float4 u = *reinterpret_cast<const float4*>(left + k * 32 + ((b0 ^ sw) << 2));
-        const float4 v = *reinterpret_cast<const float4*>(left + k * 32 + (((b0 + 1) ^ sw) << 2));
-        acc[0] = __ffma2_rn(make_float2(u.x, u.y), t2, acc[0]);
-        acc[1] = __ffma2_rn(make_float2(u.z, u.w), t2, acc[1]);
-        acc[2] = __ffma2_rn(make_float2(v.x, v.y), t2, acc[2]);
-        acc[3] = __ffma2_rn(make_float2(v.z, v.w), t2, acc[3]);
+    for (int i = 0; i < 4; ++i) {
+        float2 f = make_float2(c[i >> 1][2 * (i & 1)], c[i >> 1][2 * (i & 1) + 1]);
+        hi[i] = take2(f);
+        lo[i] = pack_bf16x2(f.x, f.y);
     }
+}
+
+// The inverse of a chunk's unit lower triangular matrix from its 16 x 16
+// diagonal blocks' inverses, as T^T (upper triangular, hi at `hi`, lo at `lo`,
+// rows of 128 bytes).  With M^T = T_a^T A_ba^T the block below T_a, left of
+// T_b, is T_ba^T = - M^T T_b^T: the accumulators of the first product are the
+// left operand of the second as they stand.  Level 1: 16 x 16 blocks (A_ba in
+// `a10`), warps 2 p and 2 p + 1 do the 32 x 32 block p.
+__device__ __forceinline__ void join16(uint32_t hi, uint32_t lo, uint32_t a10, int wq) {
+    const int lane = threadIdx.x & 31, mi = lane >> 3, l7 = lane & 7, p = wq >> 1, nh = wq & 1;
+    uint32_t ah[4], al[4], bh[4], bl[4];
+    const uint32_t oa = sw128(32 * p + (mi & 1) * 8 + l7, 4 * p + (mi >> 1));
+    ldsm4(ah, hi + oa);
+    ldsm4(al, lo + oa);
+    const int rb = (mi >> 1) * 8 + l7;
+    ldsm4(bh, a10 + sw128(rb, 4 * p + (mi & 1)));
+    ldsm4(bl, a10 + sw128(rb, 4 * p + 2 + (mi & 1)));
+    float c[2][4] = {};
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        mma16816(c[n], al, bh[2 * n], bh[2 * n + 1]);
+        mma16816(c[n], ah, bl[2 * n], bl[2 * n + 1]);
+        mma16816(c[n], ah, bh[2 * n], bh[2 * n + 1]);
+    }
+    split_acc(c, ah, al);
+    // T_b^T: k rows 32 p + 16 .., 8 columns; hi and lo in one load
+    ldsm4t(bh, ((mi >> 1) ? lo : hi) + sw128(32 * p + 16 + (mi & 1) * 8 + l7, 4 * p + 2 + nh));
+    float d[4] = {};
+    mma16816(d, al, bh[0], bh[1]);
+    mma16816(d, ah, bh[2], bh[3]);
+    mma16816(d, ah, bh[0], bh[1]);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float2 f = make_float2(-d[2 * r], -d[2 * r + 1]);
+        const uint32_t o = sw128(32 * p + (lane >> 2) + 8 * r, 4 * p + 2 + nh) + (lane & 3) * 4;
+        sts32(hi + o, take2(f));
+        sts32(lo + o, pack_bf16x2(f.x, f.y));
+    }
+    if (lane < 16) {               // below T_a^T stands zero
+        const uint32_t o = sw128(32 * p + 16 + lane, 4 * p + nh);
+        sts128(hi + o, make_uint4(0u, 0u, 0u, 0u));
+        sts128(lo + o, make_uint4(0u, 0u, 0u, 0u));
+    }
+}
+// Level 2: the 32 x 32 block (A_ba in `a21`); a warp has 16 of its columns and rows
+__device__ __forceinline__ void join32(uint32_t hi, uint32_t lo, uint32_t a21, int wq) {
+    const int lane = threadIdx.x & 31, mi = lane >> 3, l7 = lane & 7, mt = wq & 1, nh = wq >> 1;
+    float c[4][4] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t ah[4], al[4];
+        const uint32_t oa = sw128(16 * mt + (mi & 1) * 8 + l7, 2 * k + (mi >> 1));
+        ldsm4(ah, hi + oa);
+        ldsm4(al, lo + oa);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            uint32_t bh[4], bl[4];
+            const int rb = 16 * n + (mi >> 1) * 8 + l7;
+            ldsm4(bh, a21 + sw128(rb, 2 * k + (mi & 1)));
+            ldsm4(bl, a21 + sw128(rb, 4 + 2 * k + (mi & 1)));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mma16816(c[2 * n + e], al, bh[2 * e], bh[2 * e + 1]);
+                mma16816(c[2 * n + e], ah, bl[2 * e], bl[2 * e + 1]);
+                mma16816(c[2 * n + e], ah, bh[2 * e], bh[2 * e + 1]);
+            }
+        }
+    }
+    float d[2][4] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t ah[4], al[4], bh[4], bl[4];
+        split_acc(c + 2 * k, ah, al);
+        const uint32_t ob = sw128(32 + 16 * k + (mi & 1) * 8 + l7, 4 + 2 * nh + (mi >> 1));
+        ldsm4t(bh, hi + ob);
+        ldsm4t(bl, lo + ob);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            mma16816(d[e], al, bh[2 * e], bh[2 * e + 1]);
+            mma16816(d[e], ah, bl[2 * e], bl[2 * e + 1]);
+            mma16816(d[e], ah, bh[2 * e], bh[2 * e + 1]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float2 f = make_float2(-d[e][2 * r], -d[e][2 * r + 1]);
+            const uint32_t o = sw128(16 * mt + (lane >> 2) + 8 * r, 4 + 2 * nh + e) + (lane & 3) * 4;
+            sts32(hi + o, take2(f));
+            sts32(lo + o, pack_bf16x2(f.x, f.y));
+        }
 }
 
 // NP loads of W consecutive columns (32 lanes, thread = lane), `step` columns
@@ -322,12 +424,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&m->tmem_base, 512);
         tmem_relinquish();
     }
-    // T - I is lower triangular: its upper right blocks stay zero
-    for (int e = tid; e < 2 * 32 * 4; e += kThreads) {
-        const int buf = e >> 7, row = (e >> 2) & 31, ch = 4 + (e & 3);
-        put16(smem, OFF_X + buf * 16384, sw128(row, ch), 16384, make_uint4(0u, 0u, 0u, 0u));
-        put16(smem, OFF_TL + buf * 8192, sw128(row, ch), 8192, make_uint4(0u, 0u, 0u, 0u));
-    }
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -425,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w.nch > 0) store_state(0);
 #pragma unroll 1
         for (int c = 0; c < w.nch; ++c) {
-            const Gates* gt = &m->gates[c & 3];
+            const Gates* gt = &m->gates[c % 5];
             float2 buf[kCols / 2];                 // top: beta V, R, then U; else Q S
             if (top) {
                 wait(&m->v_full[c & 1], c >> 1, m, status, 10);
@@ -557,9 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int group = (warp - 9) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const int pt = tid - 32 - kState - group * kPrep;
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + D_G + 64 * group;
-        float* a11 = reinterpret_cast<float*>(smem + OFF_SCR + group * SCR_BYTES);
-        float* a22 = a11 + 1024;
-        float* a21 = a22 + 1024;
+        const int scr = OFF_SCR + group * SCR_BYTES;
+        float* diag = reinterpret_cast<float*>(smem + scr + SCR_D);
         const int xo = OFF_X + group * 16384, lo = OFF_TL + group * 8192;
         const int tok = row & 63, blk = quarter & 1;       // the row's token; its 32-token block
         constexpr uint32_t idG = idesc_bf16(128, 64, 0, 0);
@@ -570,17 +665,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(q.rec + o) = v;
         };
         // P rows of tokens behind the end (other data, possibly not numbers) are recorded as zeros
-        auto keep_p = [&](int c, int tok, int ch, float2* f, bool live) {
-            if (!live) f[0] = f[1] = f[2] = f[3] = make_float2(0.f, 0.f);
+        auto keep_p = [&](int c, int ch, const float2* e, bool live) {
+            float2 f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = live ? e[j] : make_float2(0.f, 0.f);
             keep(kRecP, c, tok, ch, take8(f));
             keep(kRecP + kTok, c, tok, ch, round8(f));
         };
         Raw raw = {};
         if (quarter == 2) raw = load_raw(q, w.b, w.h, w.len, group);
+#pragma unroll 1
         for (int c = group; c < w.nch; c += 2) {
             const int kqo = OFF_KQ + (c % 3) * 32768;
             const int nt = min(kC, w.len - c * kC);
-            Gates* gt = &m->gates[c & 3];
+            Gates* gt = &m->gates[c % 5];
+            // The gates take the place of chunk c - 5's.  This group has seen the
+            // products of chunk c - 4 end (x_free below), so every chain thread
+            // has begun that chunk and left the one before.
+            if (quarter == 2) {
+                make_gates(raw, gt);
+                raw = load_raw(q, w.b, w.h, w.len, c + 2);       // the group's next
+            }
             wait(&m->kq_full[c % 3], c / 3, m, status, 20);
             // K rows behind the sequence's end (other data, possibly not numbers)
             // must be zeros: K^T U sums over all rows of the tile
@@ -603,163 +708,141 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 commit_one(&m->g[group]);
             }
-            // the gates take the place of chunk c - 4's, which every chain thread
-            // left before the products of chunk c - 3 freed this chunk's K and Q
-            if (quarter == 2) {
-                make_gates(raw, gt);
-                raw = load_raw(q, w.b, w.h, w.len, c + 2);       // the group's next
-            }
-            group_sync(group);
-            wait(&m->g[group], c >> 1, m, status, 22);
-            tc_fence_after();
             const float2 G = gt->G[tok];
             const float f = row < 64 ? gt->beta[tok] : q.scale;
             const float fm = f * gt->mid[tok];             // (only rows of the second block use it)
-            // P takes the place of chunk c - 2's
-            if (row >= 64 && c >= 2) wait(&m->x_free[group], (c >> 1) - 1, m, status, 21);
+            wait(&m->g[group], c >> 1, m, status, 22);
             __syncwarp();
+            tc_fence_after();
+            uint4 pk[8];                                   // P's row, rounded (rows 64..)
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) pk[ch] = make_uint4(0u, 0u, 0u, 0u);
             if (blk == 1) {                                // the block left of the diagonal
                 float d[32];
                 tmem_ld32(tl, d);
                 const float2 f2 = make_float2(fm, fm);
-                float2 e[16];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 u = *reinterpret_cast<const float4*>(&gt->mid[4 * j]);
-                    e[2 * j] = __fmul2_rn(__fmul2_rn(make_float2(u.x, u.y), f2), make_float2(d[4 * j], d[4 * j + 1]));
-                    e[2 * j + 1] = __fmul2_rn(__fmul2_rn(make_float2(u.z, u.w), f2), make_float2(d[4 * j + 2], d[4 * j + 3]));
-                }
-                if (row < 64) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        a21[2 * j * 32 + lane] = e[j].x;
-                        a21[(2 * j + 1) * 32 + lane] = e[j].y;
-                    }
-                } else {
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        put16(smem, xo, sw128(row, ch), 16384, round8(e + 4 * ch));
-                        if (DUMP) keep_p(c, tok, ch, e + 4 * ch, tok < nt);
-                    }
-                }
-            } else if (row >= 64) {
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
-                    put16(smem, xo, sw128(row, 4 + ch), 16384, make_uint4(0u, 0u, 0u, 0u));
-                    if (DUMP) {
-                        keep(kRecP, c, tok, 4 + ch, make_uint4(0u, 0u, 0u, 0u));
-                        keep(kRecP + kTok, c, tok, 4 + ch, make_uint4(0u, 0u, 0u, 0u));
+                    float2 e[4];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float4 u = *reinterpret_cast<const float4*>(&gt->mid[8 * ch + 4 * j]);
+                        e[2 * j] = __fmul2_rn(__fmul2_rn(make_float2(u.x, u.y), f2), make_float2(d[8 * ch + 4 * j], d[8 * ch + 4 * j + 1]));
+                        e[2 * j + 1] = __fmul2_rn(__fmul2_rn(make_float2(u.z, u.w), f2), make_float2(d[8 * ch + 4 * j + 2], d[8 * ch + 4 * j + 3]));
                     }
+                    if (row < 64) {
+                        put16(smem, scr + SCR_21, sw128(lane, ch), 4096, take8(e));
+                        put16(smem, scr + SCR_21, sw128(lane, 4 + ch), 4096, round8(e));
+                    } else {
+                        pk[ch] = round8(e);
+                        if (DUMP) keep_p(c, ch, e, tok < nt);
+                    }
+                }
+            } else if (DUMP && row >= 64) {
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    keep(kRecP, c, tok, 4 + ch, make_uint4(0u, 0u, 0u, 0u));
+                    keep(kRecP + kTok, c, tok, 4 + ch, make_uint4(0u, 0u, 0u, 0u));
                 }
             }
             {                                              // the diagonal block
                 float d[32];
                 tmem_ld32(tl + 32 * blk, d);
                 const int last = row < 64 ? lane - 1 : lane;
-                float2 e[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float4 u = *reinterpret_cast<const float4*>(&gt->G[32 * blk + 2 * j]);
-                    const float x0 = ex2((G.x - u.x) + (G.y - u.y)), x1 = ex2((G.x - u.z) + (G.y - u.w));
-                    e[j] = make_float2(2 * j <= last ? f * x0 * d[2 * j] : 0.f, 2 * j + 1 <= last ? f * x1 * d[2 * j + 1] : 0.f);
-                }
-                if (row < 64) {
-                    float* dst = blk ? a22 : a11;
+                for (int ch = 0; ch < 4; ++ch) {
+                    float2 e[4];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        dst[2 * j * 32 + lane] = e[j].x;
-                        dst[(2 * j + 1) * 32 + lane] = e[j].y;
+                    for (int j = 0; j < 4; ++j) {
+                        const int k = 8 * ch + 2 * j;
+                        const float4 u = *reinterpret_cast<const float4*>(&gt->G[32 * blk + k]);
+                        const float x0 = ex2((G.x - u.x) + (G.y - u.y)), x1 = ex2((G.x - u.z) + (G.y - u.w));
+                        e[j] = make_float2(k <= last ? f * x0 * d[k] : 0.f, k + 1 <= last ? f * x1 * d[k + 1] : 0.f);
                     }
-                } else {
+                    if (row < 64) {
+                        // rows 0..15: diagonal block 2 blk, columns 0..15; rows 16..31: block
+                        // 2 blk + 1, columns 16..31, and the block left of it
+                        const bool low = lane >= 16;
+                        if (low == (ch >= 2)) {
+                            float* dst = diag + (2 * blk + (ch >> 1)) * 256 + (8 * (ch & 1)) * 16 + (lane & 15);
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        put16(smem, xo, sw128(row, 4 * blk + ch), 16384, round8(e + 4 * ch));
-                        if (DUMP) keep_p(c, tok, 4 * blk + ch, e + 4 * ch, tok < nt);
+                            for (int j = 0; j < 4; ++j) {
+                                dst[2 * j * 16] = e[j].x;
+                                dst[(2 * j + 1) * 16] = e[j].y;
+                            }
+                        } else if (low) {
+                            put16(smem, scr + SCR_10, sw128(lane & 15, 4 * blk + ch), 2048, take8(e));
+                            put16(smem, scr + SCR_10, sw128(lane & 15, 4 * blk + 2 + ch), 2048, round8(e));
+                        }
+                    } else {
+                        if (blk) pk[4 + ch] = round8(e);
+                        else pk[ch] = round8(e);
+                        if (DUMP) keep_p(c, 4 * blk + ch, e, tok < nt);
                     }
                 }
             }
             tc_fence_before();
             group_sync(group);
-            // warps 2 and 3 of the quarters, whose side of the chain has less to do
-            if (quarter >= 2) {
-                float* at = blk ? a22 : a11;
-                float2 x[16];
-                invert32(at, x);
-                __syncwarp();
-                if (blk == 0) {                            // T11 by rows
+            float2 x[8];
+            invert16(diag + 256 * quarter, x);             // (lanes 16.. repeat zeros)
+            // T and P take the places of chunk c - 2's
+            if (c >= 2) wait(&m->x_free[group], (c >> 1) - 1, m, status, 23);
+            __syncwarp();
+            const uint32_t th = sbase + xo, tlo = sbase + lo;
+            if (lane < 16) {                               // row `lane` of the block's T^T
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        a11[2 * i * 32 + lane] = x[i].x;
-                        a11[(2 * i + 1) * 32 + lane] = x[i].y;
-                    }
-                } else {                                   // T22 by columns, 16-byte blocks exchanged
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<float4*>(a22 + lane * 32 + ((i ^ (lane & 7)) << 2)) =
-                            make_float4(x[2 * i].x, x[2 * i].y, x[2 * i + 1].x, x[2 * i + 1].y);
+                for (int ch = 0; ch < 2; ++ch) {
+                    const uint32_t o = sw128(16 * quarter + lane, 2 * quarter + ch);
+                    sts128(th + o, take8(x + 4 * ch));
+                    sts128(tlo + o, round8(x + 4 * ch));
                 }
             }
-            if (c >= 2) wait(&m->x_free[group], (c >> 1) - 1, m, status, 23);
+            if (row >= 64) {
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch) put16(smem, xo, sw128(row, ch), 16384, pk[ch]);
+            }
+            group_sync(group);
+            join16(th, tlo, sbase + scr + SCR_10, quarter);
+            group_sync(group);
+            join32(th, tlo, sbase + scr + SCR_21, quarter);
             group_sync(group);
             {
-                const int r0 = quarter * 8;
-                float2 acc[4];
-                product32<false>(a21, a11, r0, acc);       // A21 T11
-                // T11 - I and T22 - I as bfloat16 parts: a thread has 8 columns of a row of each
-                const int r = pt >> 2, ch = pt & 3;
-                float2 t[4];
-                const float4 u = *reinterpret_cast<const float4*>(a11 + r * 32 + 8 * ch);
-                const float4 v = *reinterpret_cast<const float4*>(a11 + r * 32 + 8 * ch + 4);
-                const float tv[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    t[j] = make_float2(8 * ch + 2 * j == r ? 0.f : tv[2 * j], 8 * ch + 2 * j + 1 == r ? 0.f : tv[2 * j + 1]);
-                auto put_t = [&](int row_, int ch_, float2* f) {
-                    const uint4 h8 = take8(f), l8 = round8(f);
-                    put16(smem, xo, sw128(row_, ch_), 16384, h8);
-                    put16(smem, lo, sw128(row_, ch_), 8192, l8);
-                    if (DUMP) {
-                        keep(kRecT, c, row_, ch_, h8);
-                        keep(kRecT + kTok, c, row_, ch_, l8);
-                    }
-                };
-                put_t(r, ch, t);
-                if (DUMP) {
-                    keep(kRecT, c, r, 4 + ch, make_uint4(0u, 0u, 0u, 0u));
-                    keep(kRecT + kTok, c, r, 4 + ch, make_uint4(0u, 0u, 0u, 0u));
-                }
-                float s8[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int k = 8 * ch + j;
-                    s8[j] = k == r ? 0.f : a22[k * 32 + (((r >> 2) ^ j) << 2) + (r & 3)];      // k & 7 = j
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) t[j] = make_float2(s8[2 * j], s8[2 * j + 1]);
-                put_t(32 + r, 4 + ch, t);
-                group_sync(group);                         // A21 has been read
+                // T - I from T^T, in place: rows 16 quarter .. of T, 8 x 8 blocks
+                // exchanged; blocks right of the diagonal are zeros
+                const int mi = lane >> 3, l7 = lane & 7;
+                uint32_t rh[4][4], rl[4][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    a21[(r0 + 2 * i) * 32 + lane] = -acc[i].x;
-                    a21[(r0 + 2 * i + 1) * 32 + lane] = -acc[i].y;
+                    const int ib = 2 * quarter + (i >> 1), jb = 4 * (i & 1) + mi;
+                    if (4 * (i & 1) <= ib) {
+                        const uint32_t o = sw128(8 * jb + l7, ib);
+                        ldsm4t(rh[i], th + o);
+                        ldsm4t(rl[i], tlo + o);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = 4 * (i & 1) + e;
+                        if (j > ib) rh[i][e] = rl[i][e] = 0u;
+                        if (j == ib && (lane >> 3) == (lane & 3)) rh[i][e] &= (lane & 4) ? 0x0000ffffu : 0xffff0000u;
+                    }
                 }
                 group_sync(group);
-                product32<true>(a22, a21, r0, acc);        // - T22 (A21 T11)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float n = (i & 1) ? acc[i >> 1].y : acc[i >> 1].x;
-                    const uint32_t o = (uint32_t)((32 + r0 + i) * 128 + (((lane >> 3) ^ i) << 4) + (lane & 7) * 2);   // (row & 7 = i)
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(n);
+                for (int i = 0; i < 4; ++i) {
+                    const int ib = 2 * quarter + (i >> 1), jb = 4 * (i & 1) + mi;
+                    const uint32_t o = sw128(8 * ib + l7, jb);
+                    stsm4(th + o, rh[i]);
+                    stsm4(tlo + o, rl[i]);
                     if (DUMP && w.p0 == 0) {
-                        const size_t at = (bh * q.nck + c) * rec_elems(P) + (32 + r0 + i) * 64 + lane;
-                        if (M3_IN(12, at + kTok, (long long)q.batch * q.nheads * q.nck * rec_elems(P))) {
-                            q.rec[at] = hi;
-                            q.rec[at + kTok] = __float2bfloat16_rn(n - __bfloat162float(hi));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const size_t at = (bh * q.nck + c) * rec_elems(P) + kRecT + (8 * ib + (lane >> 2)) * 64 +
+                                              8 * (4 * (i & 1) + e) + 2 * (lane & 3);
+                            if (M3_SPAN(12, at + kTok, 2, (long long)q.batch * q.nheads * q.nck * rec_elems(P))) {
+                                *reinterpret_cast<uint32_t*>(q.rec + at) = rh[i][e];
+                                *reinterpret_cast<uint32_t*>(q.rec + at + kTok) = rl[i][e];
+                            }
                         }
-                    }
-                    if (M3_SPAN(2, o, 2, 8192)) {
-                        *reinterpret_cast<__nv_bfloat16*>(smem + xo + o) = hi;
-                        *reinterpret_cast<__nv_bfloat16*>(smem + lo + o) = __float2bfloat16_rn(n - __bfloat162float(hi));
                     }
                 }
             }
@@ -778,6 +861,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < w.nch; ++c) {
                 const uint32_t kq = sbase + OFF_KQ + (c % 3) * 32768;
                 if (c >= 3) wait(&m->kq_free[c % 3], c / 3 - 1, m, status, 30);
+                // chunk c + 3 into L2: its load waits for a stage, and then finds it there
+                if (c + 3 < w.nch) {
+                    const int t = (c + 3) * kC;
+                    tma_prefetch_5d(&tmK, 0, 0, w.g, t, w.b);
+                    tma_prefetch_5d(&tmK, 64, 0, w.g, t, w.b);
+                    tma_prefetch_5d(&tmQ, 0, 0, w.g, t, w.b);
+                    tma_prefetch_5d(&tmQ, 64, 0, w.g, t, w.b);
+                    tma_prefetch_5d(&tmV, w.p0 & ~63, 0, w.h, t, w.b);
+                }
                 uint64_t* bar = &m->kq_full[c % 3];
                 mbar_expect_tx(bar, 32768);
                 tma_load_5d(kq, &tmK, bar, 0, 0, w.g, c * kC, w.b);
@@ -827,8 +919,6 @@ cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, int* status,
         !make_tile_map(&mQ, q.q, kN, 1, d.ngroups, d.seqlen, d.batch, kC) ||
         !make_tile_map(&mV, q.v, d.headdim, 1, d.nheads, d.seqlen, d.batch, kC))
         return cudaErrorInvalidValue;
-    // columns a CTA: all 64 of a tile where the sequences fill the SMs, else
-    // fewer, so that the heads are spread over more of them
     const char* env = getenv("M3_DTC_PC");
     const int pc = env ? atoi(env) : q.rec ? 32 : 64;
     if (q.rec) {
