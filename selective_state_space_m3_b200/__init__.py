@@ -371,38 +371,36 @@ def m3_scan_fwd_reflect(dims: Dims, u, x, B, C, dt, A, lam, theta, y,
 
 
 # ------------------------------------------------- gated delta rule, norm --
-def _dev(*tensors) -> torch.device:
-    """The one device all given tensors are on."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("m3 takes device tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"m3 takes tensors of one device, got {dev} and {t.device}")
-    return dev
-
-
-def _arg(t: Optional[torch.Tensor], what: str, dtype: torch.dtype, numel: int):
-    """Device pointer of a contiguous tensor of the expected type and size."""
+def _arg(t: Optional[torch.Tensor], what: str, dtype: torch.dtype, numel: int, dev: int):
+    """Device pointer of a contiguous tensor of the expected type, size and device."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.get_device() == dev and dev >= 0 and t.dtype is dtype and t.numel() == numel and t.is_contiguous():
+        return t.data_ptr()
+    if not t.is_cuda:
+        raise ValueError("m3 takes device tensors")
+    if t.get_device() != dev:
+        raise ValueError(f"m3 takes tensors of one device: {what} is on {t.device}, not cuda:{dev}")
+    if t.dtype is not dtype:
         raise TypeError(f"{what} is {dtype}, got {t.dtype}")
     if t.numel() != numel:
         raise ValueError(f"{what} has {numel} elements for these dims, got {t.numel()}")
-    return _ptr(t)
+    raise ValueError("m3 takes contiguous tensors")
 
 
-def _on(dev: torch.device, stream, call):
-    """``call(stream)`` with ``dev`` current (streams and launches are a device's)."""
-    if dev is None or dev.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(dev):
-        return call(_stream(stream))
+def _ws(t: torch.Tensor, dev: int):
+    """Pointer and bytes of a workspace tensor of any type."""
+    n = t.numel()
+    return _arg(t, "workspace", t.dtype, n, dev), n * t.element_size()
+
+
+def _call(fn, what: str, dev: int, stream, *args) -> None:
+    """``fn(*args, stream)`` with device ``dev`` current (streams and launches are a device's)."""
+    if dev == torch._C._cuda_getDevice():
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)), what)
 
 
 def _io_torch(dims: Dims) -> torch.dtype:
@@ -428,48 +426,42 @@ def m3_delta_fwd(dims: Dims, q, k, v, g, beta, y, workspace, scale: float = 1.0,
     """Gated delta rule over whole sequences (see include/m3.h): writes ``y``
     and, if given, ``final_h``.  ``g`` may be None (no decay); ``lengths`` is
     an int32 device tensor [batch] or None."""
-    dev = _dev(q, k, v, g, beta, y, workspace, lengths, init_h, final_h)
-    io, tok = _io_torch(dims), dims.batch * dims.seqlen
+    dev, io, f32, tok = q.get_device(), _io_torch(dims), torch.float32, dims.batch * dims.seqlen
     nk, nv, ng = tok * dims.ngroups * dims.dstate, tok * dims.nheads * dims.headdim, tok * dims.nheads
     nh = dims.batch * dims.nheads * dims.dstate * dims.headdim
-    args = (_arg(q, "q", io, nk), _arg(k, "k", io, nk), _arg(v, "v", io, nv), _arg(g, "g", torch.float32, ng),
-            _arg(beta, "beta", torch.float32, ng), float(scale), _arg(lengths, "lengths", torch.int32, dims.batch),
-            _arg(init_h, "init_h", torch.float32, nh), _arg(y, "y", io, nv),
-            _arg(final_h, "final_h", torch.float32, nh), _ptr(workspace), workspace.numel() * workspace.element_size())
-    _check(_on(dev, stream, lambda st: _lib.m3_delta_fwd(ctypes.byref(dims.c()), *args, st)), "m3_delta_fwd")
+    _call(_lib.m3_delta_fwd, "m3_delta_fwd", dev, stream, dims.c(), _arg(q, "q", io, nk, dev), _arg(k, "k", io, nk, dev),
+          _arg(v, "v", io, nv, dev), _arg(g, "g", f32, ng, dev), _arg(beta, "beta", f32, ng, dev), scale,
+          _arg(lengths, "lengths", torch.int32, dims.batch, dev), _arg(init_h, "init_h", f32, nh, dev),
+          _arg(y, "y", io, nv, dev), _arg(final_h, "final_h", f32, nh, dev), *_ws(workspace, dev))
 
 
 def m3_delta_step(dims: Dims, h, q, k, v, g, beta, y, scale: float = 1.0, h_out=None, stream=None) -> None:
     """One decode token of the gated delta rule; the state ``h`` is updated in
     place, or left alone and the new one written to ``h_out`` if given."""
-    out = h if h_out is None else h_out
-    dev = _dev(h, out, q, k, v, g, beta, y)
-    io = _io_torch(dims)
-    nk, ng = dims.batch * dims.ngroups * dims.dstate, dims.batch * dims.nheads
-    nv, nh = ng * dims.headdim, ng * dims.dstate * dims.headdim
-    args = (_arg(h, "h", torch.float32, nh), _arg(out, "h_out", torch.float32, nh), _arg(q, "q", io, nk),
-            _arg(k, "k", io, nk), _arg(v, "v", io, nv), _arg(g, "g", torch.float32, ng),
-            _arg(beta, "beta", torch.float32, ng), float(scale), _arg(y, "y", io, nv))
-    _check(_on(dev, stream, lambda st: _lib.m3_delta_step(ctypes.byref(dims.c()), *args, st)), "m3_delta_step")
+    dev, io, f32, b = q.get_device(), _io_torch(dims), torch.float32, dims.batch
+    nk, ng = b * dims.ngroups * dims.dstate, b * dims.nheads
+    nv = ng * dims.headdim
+    nh = nv * dims.dstate
+    _call(_lib.m3_delta_step, "m3_delta_step", dev, stream, dims.c(), _arg(h, "h", f32, nh, dev),
+          _arg(h if h_out is None else h_out, "h_out", f32, nh, dev), _arg(q, "q", io, nk, dev), _arg(k, "k", io, nk, dev),
+          _arg(v, "v", io, nv, dev), _arg(g, "g", f32, ng, dev), _arg(beta, "beta", f32, ng, dev), scale,
+          _arg(y, "y", io, nv, dev))
 
 
 def m3_delta_bwd(dims: Dims, q, k, v, g, beta, dy, grads: dict, workspace, scale: float = 1.0, lengths=None,
                  init_h=None, d_final_h=None, d_init_h=None, stream=None) -> None:
     """Gradient of m3_delta_fwd (see include/m3.h).  ``grads`` holds the output
     tensors dq, dk, dv, dg, dbeta in the io dtype (dg may be absent)."""
-    outs = [grads[n] for n in ("dq", "dk", "dv")] + [grads.get("dg"), grads["dbeta"]]
-    dev = _dev(q, k, v, g, beta, dy, *outs, workspace, lengths, init_h, d_final_h, d_init_h)
-    io, tok = _io_torch(dims), dims.batch * dims.seqlen
+    dev, io, f32, tok = q.get_device(), _io_torch(dims), torch.float32, dims.batch * dims.seqlen
     nk, nv, ng = tok * dims.ngroups * dims.dstate, tok * dims.nheads * dims.headdim, tok * dims.nheads
     nh = dims.batch * dims.nheads * dims.dstate * dims.headdim
-    args = (_arg(q, "q", io, nk), _arg(k, "k", io, nk), _arg(v, "v", io, nv), _arg(g, "g", torch.float32, ng),
-            _arg(beta, "beta", torch.float32, ng), float(scale), _arg(lengths, "lengths", torch.int32, dims.batch),
-            _arg(init_h, "init_h", torch.float32, nh), _arg(dy, "dy", io, nv),
-            _arg(d_final_h, "d_final_h", torch.float32, nh), _arg(outs[0], "dq", io, nk), _arg(outs[1], "dk", io, nk),
-            _arg(outs[2], "dv", io, nv), _arg(outs[3], "dg", io, ng), _arg(outs[4], "dbeta", io, ng),
-            _arg(d_init_h, "d_init_h", torch.float32, nh), _ptr(workspace),
-            workspace.numel() * workspace.element_size())
-    _check(_on(dev, stream, lambda st: _lib.m3_delta_bwd(ctypes.byref(dims.c()), *args, st)), "m3_delta_bwd")
+    _call(_lib.m3_delta_bwd, "m3_delta_bwd", dev, stream, dims.c(), _arg(q, "q", io, nk, dev), _arg(k, "k", io, nk, dev),
+          _arg(v, "v", io, nv, dev), _arg(g, "g", f32, ng, dev), _arg(beta, "beta", f32, ng, dev), scale,
+          _arg(lengths, "lengths", torch.int32, dims.batch, dev), _arg(init_h, "init_h", f32, nh, dev),
+          _arg(dy, "dy", io, nv, dev), _arg(d_final_h, "d_final_h", f32, nh, dev),
+          _arg(grads["dq"], "dq", io, nk, dev), _arg(grads["dk"], "dk", io, nk, dev), _arg(grads["dv"], "dv", io, nv, dev),
+          _arg(grads.get("dg"), "dg", io, ng, dev), _arg(grads["dbeta"], "dbeta", io, ng, dev),
+          _arg(d_init_h, "d_init_h", f32, nh, dev), *_ws(workspace, dev))
 
 
 def m3_rms_norm_fwd(x, eps: float, residual=None, weight=None, sum=None, y=None, y8=None, scale=None,
@@ -477,15 +469,13 @@ def m3_rms_norm_fwd(x, eps: float, residual=None, weight=None, sum=None, y=None,
     """Root-mean-square norm of the rows (last axis) of ``x`` plus ``residual``
     (see include/m3.h): writes whichever of ``sum``, ``y`` (io dtype) and ``y8``
     with ``scale`` (float8_e4m3fn, float32) are given."""
-    dev = _dev(x, residual, weight, sum, y, y8, scale)
-    io, width, n = x.dtype, x.shape[-1], x.numel()
+    dev, io, f32, width, n = x.get_device(), x.dtype, torch.float32, x.shape[-1], x.numel()
     rows = n // width if width else 0
     blocks = -(-width // scale_block) if scale_block > 0 else 1
-    args = (_arg(x, "x", io, n), _arg(residual, "residual", io, n), _arg(weight, "weight", torch.float32, width),
-            float(eps), _arg(sum, "sum", io, n), _arg(y, "y", io, n), _arg(y8, "y8", torch.float8_e4m3fn, n),
-            _arg(scale, "scale", torch.float32, rows * blocks), int(scale_block))
-    code = io_dtype_of(x)
-    _check(_on(dev, stream, lambda st: _lib.m3_rms_norm_fwd(rows, width, code, *args, st)), "m3_rms_norm_fwd")
+    _call(_lib.m3_rms_norm_fwd, "m3_rms_norm_fwd", dev, stream, rows, width, io_dtype_of(x), _arg(x, "x", io, n, dev),
+          _arg(residual, "residual", io, n, dev), _arg(weight, "weight", f32, width, dev), eps,
+          _arg(sum, "sum", io, n, dev), _arg(y, "y", io, n, dev), _arg(y8, "y8", torch.float8_e4m3fn, n, dev),
+          _arg(scale, "scale", f32, rows * blocks, dev), scale_block)
 
 
 def m3_rms_norm_bwd_workspace_size(rows: int, width: int, io_dtype: int) -> int:
@@ -496,14 +486,11 @@ def m3_rms_norm_bwd_workspace_size(rows: int, width: int, io_dtype: int) -> int:
 def m3_rms_norm_bwd(s, dy, eps: float, dx, workspace, weight=None, d_sum=None, dweight=None, stream=None) -> None:
     """Gradient of m3_rms_norm_fwd at its input ``s`` (the stored sum): writes
     ``dx`` (io dtype) and, if given, ``dweight`` (float32)."""
-    dev = _dev(s, dy, dx, workspace, weight, d_sum, dweight)
-    io, width, n = s.dtype, s.shape[-1], s.numel()
+    dev, io, f32, width, n = s.get_device(), s.dtype, torch.float32, s.shape[-1], s.numel()
     rows = n // width if width else 0
-    args = (_arg(s, "s", io, n), _arg(weight, "weight", torch.float32, width), float(eps), _arg(dy, "dy", io, n),
-            _arg(d_sum, "d_sum", io, n), _arg(dx, "dx", io, n), _arg(dweight, "dweight", torch.float32, width),
-            _ptr(workspace), workspace.numel() * workspace.element_size())
-    code = io_dtype_of(s)
-    _check(_on(dev, stream, lambda st: _lib.m3_rms_norm_bwd(rows, width, code, *args, st)), "m3_rms_norm_bwd")
+    _call(_lib.m3_rms_norm_bwd, "m3_rms_norm_bwd", dev, stream, rows, width, io_dtype_of(s), _arg(s, "s", io, n, dev),
+          _arg(weight, "weight", f32, width, dev), eps, _arg(dy, "dy", io, n, dev), _arg(d_sum, "d_sum", io, n, dev),
+          _arg(dx, "dx", io, n, dev), _arg(dweight, "dweight", f32, width, dev), *_ws(workspace, dev))
 
 
 def raw_lib():

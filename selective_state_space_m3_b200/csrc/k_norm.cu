@@ -6,16 +6,16 @@
 // Gradient at the norm's input s (rs = (mean s^2 + eps)^(-1/2), s^ = s rs):
 //   dx = d_sum + rs (w dy - s^ mean(w dy s^)),   dw = sum over rows of dy s^
 //
-// Bound by memory: every element is read and written once.  A row lives in the
-// registers of TPR threads (8 consecutive elements a thread and vector, up to
-// NV vectors), all its loads are issued before the reduction, and the
-// reduction is shuffles (TPR <= 32) or shuffles and one exchange through shared
-// memory.  Sums are float32.  A 128-column scale is the maximum over 16 lanes
-// that hold one block, so 8-bit output needs no second pass.  The weight's
-// gradient stays in registers over the rows that a thread group walks; the
-// groups' parts are added by a second kernel in a fixed order.  Rows whose
-// width is not a multiple of 8 (or too wide for registers) take scalar
-// kernels that read the row twice (the second time from cache).
+// Bound by memory: every element is read and written once.  A row belongs to
+// TPR threads (8 consecutive elements a thread and vector, up to NV vectors),
+// whose loads are all issued before any arithmetic.  The reduction is shuffles
+// (TPR <= 32) or shuffles and one exchange through shared memory.  Sums are
+// float32.  A 128-column scale is the maximum over 16 lanes that hold one block,
+// so 8-bit output needs no second pass.  The weight's gradient stays in
+// registers over the rows that a thread group walks; the CTAs' parts are added
+// by a second kernel in a fixed order.  Rows whose width is not a multiple of 8
+// (or too wide for registers) take scalar kernels that read the row again from
+// cache.
 #include <cuda_fp8.h>
 
 #define M3_BOUNDS_FILE 11
@@ -30,11 +30,16 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kE4M3Max = 448.f;
 constexpr float kTiny = 1e-30f;      // floor of a scale's maximum: an all-zero block has a finite scale
 
-template <typename T> struct Vec8;   // 8 elements as float
+// 8 elements as loaded (kept packed until they are used) and as float
+template <typename T> struct Vec8;
 template <> struct Vec8<__nv_bfloat16> {
-    static __device__ __forceinline__ void load(const void* base, size_t o, float* f) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + o));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    struct Raw { uint4 v; };
+    static __device__ __forceinline__ Raw fetch(const void* base, size_t o) {
+        return {__ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + o))};
+    }
+    static __device__ __forceinline__ Raw none() { return {make_uint4(0u, 0u, 0u, 0u)}; }
+    static __device__ __forceinline__ void open(const Raw& r, float* f) {
+        const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f[2 * j] = __uint_as_float(w[j] << 16);
@@ -52,16 +57,37 @@ template <> struct Vec8<__nv_bfloat16> {
     }
 };
 template <> struct Vec8<float> {
-    static __device__ __forceinline__ void load(const void* base, size_t o, float* f) {
+    struct Raw { float4 a, b; };
+    static __device__ __forceinline__ Raw fetch(const void* base, size_t o) {
         const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + o);
-        const float4 a = __ldcs(p), b = __ldcs(p + 1);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        return {__ldcs(p), __ldcs(p + 1)};
+    }
+    static __device__ __forceinline__ Raw none() { return {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)}; }
+    static __device__ __forceinline__ void open(const Raw& r, float* f) {
+        f[0] = r.a.x; f[1] = r.a.y; f[2] = r.a.z; f[3] = r.a.w;
+        f[4] = r.b.x; f[5] = r.b.y; f[6] = r.b.z; f[7] = r.b.w;
     }
     static __device__ __forceinline__ void store(void* base, size_t o, const float* f) {
         float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + o);
         __stcs(p, make_float4(f[0], f[1], f[2], f[3]));
         __stcs(p + 1, make_float4(f[4], f[5], f[6], f[7]));
+    }
+};
+
+// NA arrays' elements of a row that a thread holds, NV vectors of each
+template <typename T, int NV, int NA>
+struct RowRegs {
+    typename Vec8<T>::Raw r[NA][NV];
+    __device__ __forceinline__ void fetch(const void* const (&src)[NA], const NormParams& q, long long row, int lane, int tpr) {
+        const bool live = row < q.rows;
+        const size_t base = live ? (size_t)row * q.width : 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + tpr * i) * 8;
+            const bool in = live && c < q.width && M3_SPAN(1, base + c, 8, q.rows * q.width);
+#pragma unroll
+            for (int a = 0; a < NA; ++a) r[a][i] = in && src[a] ? Vec8<T>::fetch(src[a], base + c) : Vec8<T>::none();
+        }
     }
 };
 
@@ -90,7 +116,11 @@ __device__ __forceinline__ uint2 e4m3x8(const float* f, float inv) {
 }
 
 // NaN-keeping maximum: a row with a NaN gets a NaN scale, not a finite one
-__device__ __forceinline__ float nmax(float a, float b) { return (a > b || a != a) ? a : b; }
+__device__ __forceinline__ float nmax(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
 
 // sum (or maximum) over the TPR threads of a row; `buf` holds one value a warp
 // of the CTA.  Every thread of the CTA calls it.
@@ -111,78 +141,95 @@ __device__ __forceinline__ float row_reduce(float v, int tpr, float* buf) {
     return v;
 }
 
-template <typename T, int NV>
-__global__ void __launch_bounds__(512) norm_kernel(NormParams q, int tpr) {
+// Both sums of a row in one reduction; `buf` has two sets of a pair a warp,
+// taken in turn, so that one barrier a row is enough.
+__device__ __forceinline__ float2 row_reduce2(float2 v, int tpr, float2* buf) {
+    for (int o = min(tpr, 32) >> 1; o; o >>= 1) {
+        v.x += __shfl_xor_sync(kFull, v.x, o);
+        v.y += __shfl_xor_sync(kFull, v.y, o);
+    }
+    if (tpr > 32) {
+        const int warp = threadIdx.x >> 5, per = tpr >> 5, first = warp / per * per;
+        if ((threadIdx.x & 31) == 0) buf[warp] = v;
+        __syncthreads();
+        v = buf[first];
+        for (int i = 1; i < per; ++i) {
+            v.x += buf[first + i].x;
+            v.y += buf[first + i].y;
+        }
+    }
+    return v;
+}
+
+// RES: a residual is added; Q8: an 8-bit output is written.  At most 40 registers
+// a thread (three CTAs of 512 an SM), so that enough loads are in flight:
+// measured 80 instead of 99 us for 32768 x 2048 with residual and 8-bit output
+// (90 % of the copy rate).
+template <typename T, int NV, bool RES, bool Q8>
+__global__ void __launch_bounds__(512, NV <= 2 ? 3 : 1) norm_kernel(NormParams q, int tpr) {
     __shared__ float buf[16];
-    const int lane = threadIdx.x & (tpr - 1), nvec = q.width >> 3;
-    const long long row = (long long)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    const int lane = threadIdx.x & (tpr - 1), per = blockDim.x / tpr;
+    const long long row = (long long)blockIdx.x * per + threadIdx.x / tpr;
+    const long long ext = q.rows * q.width;
+    const void* src[RES ? 2 : 1];
+    src[0] = q.x;
+    if constexpr (RES) src[1] = q.residual;
     const bool live = row < q.rows;
     const size_t base = live ? (size_t)row * q.width : 0;
-    const long long ext = q.rows * q.width;
-    float s[NV][8];
-    float ss = 0.f;
+    RowRegs<T, NV, RES ? 2 : 1> cur;
+    cur.fetch(src, q, row, lane, tpr);
+    {
+        float s[NV][8];
+        float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (lane + tpr * i) * 8;
+        for (int i = 0; i < NV; ++i) {
+            Vec8<T>::open(cur.r[0][i], s[i]);
+            if constexpr (RES) {
+                float r[8];
+                Vec8<T>::open(cur.r[1][i], r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[i][j] = 0.f;
-        if (live && lane + tpr * i < nvec && M3_SPAN(1, base + c, 8, ext)) Vec8<T>::load(q.x, base + c, s[i]);
-    }
-    if (q.residual) {
-        float r[NV][8];
+                for (int j = 0; j < 8; ++j) s[i][j] += r[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(s[i][j], s[i][j], ss);
+        }
+        ss = row_reduce<false>(ss, tpr, buf);
+        const float rs = rsqrtf(ss / (float)q.width + q.eps);
+        float top = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + tpr * i) * 8;
+            const bool in = live && c < q.width && M3_SPAN(3, base + c, 8, ext);
+            if (in && q.sum) Vec8<T>::store(q.sum, base + c, s[i]);
+            float w[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) r[i][j] = 0.f;
-            if (live && lane + tpr * i < nvec && M3_SPAN(2, base + c, 8, ext)) Vec8<T>::load(q.residual, base + c, r[i]);
+            for (int j = 0; j < 8; ++j) w[j] = 0.f;
+            if (in) load_weight8(q.weight, c, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s[i][j] = in ? s[i][j] * rs * w[j] : 0.f;
+                if (Q8) top = nmax(top, fabsf(s[i][j]));
+            }
+            if (in && q.y) Vec8<T>::store(q.y, base + c, s[i]);
+            if (Q8 && q.block) {          // 16 lanes hold the 128 columns of one scale
+                for (int o = 8; o; o >>= 1) top = nmax(top, __shfl_xor_sync(kFull, top, o));
+                top = nmax(top, kTiny);
+                const int nb = (q.width + 127) >> 7;
+                if (in) __stcs(reinterpret_cast<uint2*>(q.y8 + base + c), e4m3x8(s[i], __fdividef(kE4M3Max, top)));
+                if (in && (c & 127) == 0 && M3_IN(7, row * nb + (c >> 7), q.rows * nb)) q.scale[row * nb + (c >> 7)] = top * (1.f / kE4M3Max);
+                top = 0.f;
+            }
         }
+        if (Q8 && !q.block) {
+            top = nmax(row_reduce<true>(top, tpr, buf), kTiny);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s[i][j] += r[i][j];
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(s[i][j], s[i][j], ss);
-    ss = row_reduce<false>(ss, tpr, buf);
-    const float rs = rsqrtf(ss / (float)q.width + q.eps);
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (lane + tpr * i) * 8;
-        const bool in = live && lane + tpr * i < nvec;
-        if (in && q.sum && M3_SPAN(3, base + c, 8, ext)) Vec8<T>::store(q.sum, base + c, s[i]);
-        float w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 0.f;
-        if (in && M3_SPAN(4, c, 8, q.width)) load_weight8(q.weight, c, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            s[i][j] = in ? s[i][j] * rs * w[j] : 0.f;
-            if (q.y8) top = nmax(top, fabsf(s[i][j]));
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + tpr * i) * 8;
+                if (live && c < q.width && M3_SPAN(8, base + c, 8, ext))
+                    __stcs(reinterpret_cast<uint2*>(q.y8 + base + c), e4m3x8(s[i], __fdividef(kE4M3Max, top)));
+            }
+            if (live && lane == 0 && M3_IN(9, row, q.rows)) q.scale[row] = top * (1.f / kE4M3Max);
         }
-        if (in && q.y && M3_SPAN(5, base + c, 8, ext)) Vec8<T>::store(q.y, base + c, s[i]);
-        if (q.y8 && q.block) {          // 16 lanes hold the 128 columns of one scale
-            for (int o = min(tpr, 16) >> 1; o; o >>= 1) top = nmax(top, __shfl_xor_sync(kFull, top, o));
-            top = nmax(top, kTiny);
-            const int nb = (q.width + 127) >> 7;
-            if (in && M3_SPAN(6, base + c, 8, ext))
-                *reinterpret_cast<uint2*>(q.y8 + base + c) = e4m3x8(s[i], kE4M3Max / top);
-            if (in && (c & 127) == 0 && M3_IN(7, row * nb + (c >> 7), q.rows * nb)) q.scale[row * nb + (c >> 7)] = top / kE4M3Max;
-            top = 0.f;
-        }
-    }
-    if (q.y8 && !q.block) {
-        top = nmax(row_reduce<true>(top, tpr, buf), kTiny);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + tpr * i) * 8;
-            if (live && lane + tpr * i < nvec && M3_SPAN(8, base + c, 8, ext))
-                *reinterpret_cast<uint2*>(q.y8 + base + c) = e4m3x8(s[i], kE4M3Max / top);
-        }
-        if (live && lane == 0 && M3_IN(9, row, q.rows)) q.scale[row] = top / kE4M3Max;
     }
 }
 
@@ -229,12 +276,16 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormParams q) {
 }
 
 // ---------------------------------------------------------------- gradient --
+// The weight's gradient of a group's columns stays in registers; at the end the
+// groups of a CTA are added through shared memory (`part` has a row a CTA).
 template <typename T, int NV>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(NormParams q, int tpr) {
-    __shared__ float buf[16];
-    const int lane = threadIdx.x & (tpr - 1), nvec = q.width >> 3, per = blockDim.x / tpr;
-    const int group = blockIdx.x * per + threadIdx.x / tpr, groups = gridDim.x * per;
+    extern __shared__ float sums[];
+    __shared__ float2 buf[2][16];
+    const int lane = threadIdx.x & (tpr - 1), per = blockDim.x / tpr, sub = threadIdx.x / tpr;
+    const long long group = (long long)blockIdx.x * per + sub, groups = (long long)gridDim.x * per;
     const long long ext = q.rows * q.width;
+    const void* const src[3] = {q.x, q.dy, q.d_sum};
     float dw[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -242,67 +293,69 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormParams q, int tpr) {
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
     // all groups of a CTA take the same number of rounds (the reduction may be CTA-wide)
     const long long rounds = (q.rows + groups - 1) / groups;
+    // a row's loads are issued while the row before is reduced
+    RowRegs<T, NV, 3> next;
+    next.fetch(src, q, group, lane, tpr);
     for (long long k = 0; k < rounds; ++k) {
         const long long row = k * groups + group;
         const bool live = row < q.rows;
         const size_t base = live ? (size_t)row * q.width : 0;
-        float s[NV][8], d[NV][8];
-        float ss = 0.f, dot = 0.f;
+        const RowRegs<T, NV, 3> cur = next;
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + tpr * i) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s[i][j] = d[i][j] = 0.f;
-            if (live && lane + tpr * i < nvec && M3_SPAN(14, base + c, 8, ext)) {
-                Vec8<T>::load(q.x, base + c, s[i]);
-                Vec8<T>::load(q.dy, base + c, d[i]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + tpr * i) * 8;
-            float w[8];
+            float s[8], d[8], w[8];
+            Vec8<T>::open(cur.r[0][i], s);
+            Vec8<T>::open(cur.r[1][i], d);
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = 0.f;
-            if (lane + tpr * i < nvec && M3_SPAN(15, c, 8, q.width)) load_weight8(q.weight, c, w);
+            if (c < q.width && M3_SPAN(15, c, 8, q.width)) load_weight8(q.weight, c, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                ss = fmaf(s[i][j], s[i][j], ss);
-                dot = fmaf(s[i][j] * w[j], d[i][j], dot);
+                sum.x = fmaf(s[j], s[j], sum.x);
+                sum.y = fmaf(s[j] * w[j], d[j], sum.y);
             }
         }
-        ss = row_reduce<false>(ss, tpr, buf);
-        dot = row_reduce<false>(dot, tpr, buf);
-        const float rs = rsqrtf(ss / (float)q.width + q.eps);
-        const float m = dot * rs * rs / (float)q.width;          // mean(w dy s^) rs
+        if (k + 1 < rounds) next.fetch(src, q, row + groups, lane, tpr);
+        sum = row_reduce2(sum, tpr, buf[k & 1]);
+        const float rs = rsqrtf(sum.x / (float)q.width + q.eps);
+        const float m = sum.y * rs * rs / (float)q.width;          // mean(w dy s^) rs
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + tpr * i) * 8;
-            if (!(live && lane + tpr * i < nvec && M3_SPAN(16, base + c, 8, ext))) continue;
-            float w[8], e[8];
+            if (!(live && c < q.width && M3_SPAN(16, base + c, 8, ext))) continue;
+            float s[8], d[8], w[8], e[8];
+            Vec8<T>::open(cur.r[0][i], s);
+            Vec8<T>::open(cur.r[1][i], d);
+            Vec8<T>::open(cur.r[2][i], e);
             load_weight8(q.weight, c, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = 0.f;
-            if (q.d_sum) Vec8<T>::load(q.d_sum, base + c, e);
-#pragma unroll
             for (int j = 0; j < 8; ++j) {
-                dw[i][j] = fmaf(d[i][j], s[i][j] * rs, dw[i][j]);
-                e[j] += rs * fmaf(w[j], d[i][j], -s[i][j] * m);
+                dw[i][j] = fmaf(d[j], s[j] * rs, dw[i][j]);
+                e[j] += rs * fmaf(w[j], d[j], -s[j] * m);
             }
             Vec8<T>::store(q.dx, base + c, e);
         }
     }
-    if (q.dweight) {
+    if (!q.dweight) return;
+    // group by group into the CTA's sums
+    for (int g = 0; g < per; ++g) {
+        if (sub == g) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + tpr * i) * 8;
-            if (lane + tpr * i < nvec && M3_SPAN(17, (long long)group * q.width + c, 8, (long long)q.parts * q.width)) {
-                float4* p = reinterpret_cast<float4*>(q.part + (size_t)group * q.width + c);
-                p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-                p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + tpr * i) * 8;
+                if (c < q.width && M3_SPAN(17, c, 8, dyn_smem_bytes() / 4)) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sums[c + j] = g ? sums[c + j] + dw[i][j] : dw[i][j];
+                }
             }
         }
+        __syncthreads();
     }
+    for (int c = threadIdx.x; c < q.width; c += blockDim.x)
+        if (M3_IN(24, (long long)blockIdx.x * q.width + c, (long long)q.parts * q.width))
+            q.part[(size_t)blockIdx.x * q.width + c] = sums[c];
 }
 
 template <typename T>
@@ -345,6 +398,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(NormParams q) {
     const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5, c = blockIdx.x * 32 + cx;
     float v = 0.f;
     if (c < q.width)
+#pragma unroll 4
         for (int i = ry; i < q.parts; i += 32)
             if (M3_IN(22, (long long)i * q.width + c, (long long)q.parts * q.width)) v += q.part[(size_t)i * q.width + c];
     t[ry][cx] = v;
@@ -356,23 +410,38 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(NormParams q) {
     if (cx == 0 && cc < q.width && M3_IN(23, cc, q.width)) q.dweight[cc] = v;
 }
 
-// Threads a row and vectors a thread.  Many rows: 4 vectors a thread keep
-// enough loads in flight with few threads in the reduction; few rows (fewer
-// than a CTA for every SM): one vector a thread, so that a row's latency is
-// one load's.
+// Threads a row and vectors a thread.  Many rows: as many vectors a thread as
+// keep its loads at 64 bytes (two where two arrays are read, else four: a norm
+// without residual of 32768 x 2048 takes 49 us with four, 54 with two; one with
+// residual 82 with two, 86 with one).  Few rows (fewer than 256, at most two
+// CTAs an SM): one vector a thread, so that a row's latency is one load's.
 struct Shape {
     int tpr, nv, threads;
+    long long groups;                    // CTAs that the rows fill
 };
 static Shape shape_of(long long rows, int width, int most_nv) {
     const int nvec = width / 8;
     const int want = rows < 256 ? 1 : most_nv;
-    int tpr = 8;
-    while (tpr < 512 && tpr * want < nvec) tpr *= 2;
-    int nv = 1;
-    while (tpr * nv < nvec) nv *= 2;
-    return {tpr, nv, tpr > 128 ? tpr : 128};
+    Shape s;
+    s.tpr = 16;                          // a scale's 16 lanes in one warp
+    while (s.tpr < 512 && s.tpr * want < nvec) s.tpr *= 2;
+    s.nv = 1;
+    while (s.tpr * s.nv < nvec) s.nv *= 2;
+    s.threads = s.tpr > 128 ? s.tpr : 128;
+    s.groups = (rows + s.threads / s.tpr - 1) / (s.threads / s.tpr);
+    return s;
 }
-static bool vec_ok(int width) { return width % 8 == 0 && width <= 512 * 8 * 8; }
+static bool vec_ok(int width) { return width % 8 == 0 && width <= 512 * 4 * 8; }
+
+template <typename T, int NV>
+static cudaError_t fwd_nv(const NormParams& q, const Shape& s, cudaStream_t st) {
+    const unsigned grid = (unsigned)s.groups;
+    if (q.residual && q.y8) norm_kernel<T, NV, true, true><<<grid, s.threads, 0, st>>>(q, s.tpr);
+    else if (q.residual) norm_kernel<T, NV, true, false><<<grid, s.threads, 0, st>>>(q, s.tpr);
+    else if (q.y8) norm_kernel<T, NV, false, true><<<grid, s.threads, 0, st>>>(q, s.tpr);
+    else norm_kernel<T, NV, false, false><<<grid, s.threads, 0, st>>>(q, s.tpr);
+    return cudaGetLastError();
+}
 
 template <typename T>
 static cudaError_t fwd(const NormParams& q, cudaStream_t st) {
@@ -380,41 +449,42 @@ static cudaError_t fwd(const NormParams& q, cudaStream_t st) {
         norm_any_kernel<T><<<(unsigned)q.rows, 256, 0, st>>>(q);
         return cudaGetLastError();
     }
-    Shape s = shape_of(q.rows, q.width, 4);
-    if (q.block && s.tpr < 16) s.tpr = 16;       // a scale's 16 lanes in one warp
-    const unsigned grid = (unsigned)((q.rows + s.threads / s.tpr - 1) / (s.threads / s.tpr));
-    switch (s.nv) {
-        case 1: norm_kernel<T, 1><<<grid, s.threads, 0, st>>>(q, s.tpr); break;
-        case 2: norm_kernel<T, 2><<<grid, s.threads, 0, st>>>(q, s.tpr); break;
-        case 4: norm_kernel<T, 4><<<grid, s.threads, 0, st>>>(q, s.tpr); break;
-        default: norm_kernel<T, 8><<<grid, s.threads, 0, st>>>(q, s.tpr); break;
-    }
-    return cudaGetLastError();
+    const Shape s = shape_of(q.rows, q.width, q.residual ? 2 : 4);
+    return s.nv == 1 ? fwd_nv<T, 1>(q, s, st) : s.nv == 2 ? fwd_nv<T, 2>(q, s, st) : fwd_nv<T, 4>(q, s, st);
 }
 
+// CTAs of the gradient: as many as its 124 registers let run together, so that a
+// row's loads can go ahead of the row before and few parts are left to add
+// (16384 x 2048: 60 us with four an SM, 118 without loads ahead)
 static unsigned bwd_grid(long long rows, int width) {
-    const long long most = 4LL * device_sm_count();
-    if (!vec_ok(width)) return (unsigned)(rows < most ? rows : most);
+    const long long sms = device_sm_count();
+    if (!vec_ok(width)) return (unsigned)(rows < 4 * sms ? rows : 4 * sms);
     const Shape s = shape_of(rows, width, 2);
-    const long long need = (rows + s.threads / s.tpr - 1) / (s.threads / s.tpr);
-    return (unsigned)(need < most ? need : most);
+    const long long most = (s.threads <= 128 ? 4 : s.threads <= 256 ? 2 : 1) * sms;
+    return (unsigned)(s.groups < most ? s.groups : most);
+}
+
+template <typename T, int NV>
+static cudaError_t bwd_nv(const NormParams& q, const Shape& s, cudaStream_t st) {
+    const int smem = q.dweight ? q.width * 4 : 0;
+    if (smem > 40 * 1024) {              // (the kernel has a little static shared memory too)
+        const cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    norm_bwd_kernel<T, NV><<<bwd_grid(q.rows, q.width), s.threads, smem, st>>>(q, s.tpr);
+    return cudaGetLastError();
 }
 
 template <typename T>
 static cudaError_t bwd(const NormParams& q, cudaStream_t st) {
-    const unsigned grid = bwd_grid(q.rows, q.width);
+    cudaError_t e;
     if (!vec_ok(q.width)) {
-        norm_bwd_any_kernel<T><<<grid, 256, 0, st>>>(q);
+        norm_bwd_any_kernel<T><<<bwd_grid(q.rows, q.width), 256, 0, st>>>(q);
+        e = cudaGetLastError();
     } else {
         const Shape s = shape_of(q.rows, q.width, 2);
-        switch (s.nv) {
-            case 1: norm_bwd_kernel<T, 1><<<grid, s.threads, 0, st>>>(q, s.tpr); break;
-            case 2: norm_bwd_kernel<T, 2><<<grid, s.threads, 0, st>>>(q, s.tpr); break;
-            case 4: norm_bwd_kernel<T, 4><<<grid, s.threads, 0, st>>>(q, s.tpr); break;
-            default: norm_bwd_kernel<T, 8><<<grid, s.threads, 0, st>>>(q, s.tpr); break;
-        }
+        e = s.nv == 1 ? bwd_nv<T, 1>(q, s, st) : s.nv == 2 ? bwd_nv<T, 2>(q, s, st) : bwd_nv<T, 4>(q, s, st);
     }
-    cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && q.dweight) {
         norm_dw_kernel<<<(unsigned)((q.width + 31) / 32), 1024, 0, st>>>(q);
         e = cudaGetLastError();
@@ -425,11 +495,7 @@ static cudaError_t bwd(const NormParams& q, cudaStream_t st) {
 }  // namespace norm
 
 int norm_bwd_parts(long long rows, int width, int) {
-    if (rows <= 0) return 0;
-    const unsigned grid = norm::bwd_grid(rows, width);
-    if (!norm::vec_ok(width)) return (int)grid;
-    const norm::Shape s = norm::shape_of(rows, width, 2);
-    return (int)grid * (s.threads / s.tpr);
+    return rows <= 0 ? 0 : (int)norm::bwd_grid(rows, width);
 }
 
 cudaError_t launch_norm(int io_dtype, const NormParams& q, cudaStream_t st) {

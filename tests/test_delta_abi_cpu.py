@@ -123,10 +123,27 @@ def test_binding_refuses_host_tensors():
             call()
 
 
+class _OnDevice:
+    """A host tensor that says it is on cuda:0 (nothing is launched)."""
+
+    def __init__(self, t):
+        self.t, self.is_cuda, self.dtype, self.device = t, True, t.dtype, torch.device("cuda", 0)
+
+    def get_device(self):
+        return 0
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
 def test_binding_checks_types_and_sizes():
     t = torch.zeros(3, 4)
     with pytest.raises(TypeError, match="beta is"):
-        m3._arg(t, "beta", torch.bfloat16, 12)
+        m3._arg(_OnDevice(t), "beta", torch.bfloat16, 12, 0)
     with pytest.raises(ValueError, match="13 elements"):
-        m3._arg(t, "beta", torch.float32, 13)
-    assert m3._arg(None, "g", torch.float32, 12) is None
+        m3._arg(_OnDevice(t), "beta", torch.float32, 13, 0)
+    with pytest.raises(ValueError, match="one device"):
+        m3._arg(_OnDevice(t), "beta", torch.float32, 12, 1)
+    with pytest.raises(ValueError, match="contiguous"):
+        m3._arg(_OnDevice(t.T), "beta", torch.float32, 12, 0)
+    assert m3._arg(None, "g", torch.float32, 12, 0) is None
