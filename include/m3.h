@@ -330,8 +330,9 @@ m3_status m3_scan_fwd_reflect(const m3_dims* dims, const void* u,
  * their chains of states keep float32 values as sums of bfloat16 parts (16 bits
  * and more), and only products that end in y round an operand to bfloat16. */
 
-/* Bytes of device workspace m3_delta_fwd needs (host-only; at least 256: the
- * status word that m3_device_status reads). */
+/* Bytes of device workspace m3_delta_fwd needs (host-only): 256, the status
+ * word that m3_device_status reads, and on the chunked path 25 KB for every 64
+ * tokens of a (batch, head). */
 m3_status m3_delta_workspace_size(const m3_dims* dims, size_t* bytes);
 
 /* Prefill: y for every token from `init_h` (NULL = zeros), and the state after
@@ -433,7 +434,8 @@ m3_status m3_selftest_bounded_wait(void* workspace, size_t workspace_bytes, void
  * (site = file * 1000 + check: 1 tile prefill, 2 SIMT prefill and segment
  * combine, 3 decode step, 4 rope, 5 transition variants, 6 backward,
  * 7 phase prologues, 8 persistent prefill, 9 this self-test, 10 delta rule,
- * 11 norm, 12 chunked delta rule, 13 its gradient; for a span the
+ * 11 norm, 12 chunked delta rule, 13 its gradient, 14 its
+ * per-chunk matrices; for a span the
  * index is its last element).  `clear` != 0 resets the records after reading.
  * M3_ERR_INVALID_ARG for a NULL `out`, M3_ERR_CUDA if the device cannot be
  * read.  Host call; the release build touches no device. */

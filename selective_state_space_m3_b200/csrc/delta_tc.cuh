@@ -15,13 +15,16 @@ constexpr int kC = 64;             // tokens a chunk
 constexpr int kN = 128;
 constexpr unsigned kFull = 0xffffffffu;
 
-struct Gates {
-    float2 G[kC];                  // sum of g in log2 units, as a sum of two floats
+struct alignas(16) ChainGates {    // what a chunk's chain reads
     float a[kC], at[kC], beta[kC]; // e^G, e^{G_C - G}, beta (0 behind the end)
-    float mid[kC];                 // j < 32: e^{G_31 - G_j}; i >= 32: e^{G_i - G_31}
     float whole;                   // e^{G_C}
-    float pad[3];
+    float pad[63];
 };
+struct alignas(16) Gates : ChainGates {
+    float2 G[kC];                  // sum of g in log2 units, as a sum of two floats
+    float mid[kC];                 // j < 32: e^{G_31 - G_j}; i >= 32: e^{G_i - G_31}
+};
+static_assert(sizeof(ChainGates) == 1024, "gates of a record");
 
 __device__ __forceinline__ float clamp_g(float g) { return g < -1.0e4f ? -1.0e4f : g; }
 __device__ __forceinline__ float ex2(float x) {
@@ -43,6 +46,31 @@ __device__ __forceinline__ uint4 round8(const float2* f) {
     return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
                       pack_bf16x2(f[3].x, f[3].y));
 }
+// Products and commits by one elected lane of a converged warp: the warp runs
+// the loop as one, so that descriptors stay in uniform registers (measured:
+// 47 cycles a 128 x 64 x 16 product instead of 97 from a divergent lane).
+__device__ __forceinline__ void umma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(su32(bar))
+        : "memory");
+}
+
+// 16 bytes at `off` of the tile that starts at `tile` and has `limit` bytes
+__device__ __forceinline__ void put16(uint8_t* smem, int tile, uint32_t off, int limit, uint4 v) {
+    if (M3_SPAN(41, off, 16, limit)) *reinterpret_cast<uint4*>(smem + tile + off) = v;
+}
+
 // a + b of sums of two floats (each a pair with a small second part)
 __device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
     const float s = a.x + b.x, t = s - a.x;
@@ -102,17 +130,23 @@ __device__ __forceinline__ void make_gates(const Raw& raw, Gates* out) {
     if (lane == 0) out->whole = ex2(total.x + total.y);
 }
 
-// Records of the gradient's passes, one a chunk of a (batch, head): bfloat16
-// matrices, rows of 64 columns, each as hi and lo part (elements):
-//   T - I, P = scale Gam o Q K^T       [2][64][64] each
-//   then for every 64 columns of the head
-//   S before the chunk, its gradient behind the chunk   [2][128][64] each
-//   U, dR                                               [2][64][64] each
+// Records, one a chunk of a (batch, head), in bfloat16 elements.  Matrices are
+// images of shared memory: rows of 128 bytes (64 columns), 16-byte groups
+// exchanged by row (sw128).
+//   X      [128][64]: T - I rounded; P = scale Gam o Q K^T rounded (zero rows behind the end)
+//   TL     [64][64]: what the rounding left of T - I
+//   gates  1024 bytes (ChainGates)
+// for the gradient also
+//   PL     [64][64]: what the rounding left of P
+//   then for every 64 columns of the head, plain rows, each as hi and lo part:
+//   S before the chunk and its gradient behind the chunk [2][128][64] each, U and dR [2][64][64] each
 constexpr size_t kTok = 64 * 64, kSt = 128 * 64;
-constexpr size_t kRecT = 0, kRecP = 2 * kTok, kRecSlice = 4 * kTok;
+constexpr size_t kRecX = 0, kRecTL = 2 * kTok, kRecGates = 3 * kTok, kRecPL = kRecGates + 512, kRecSlice = kRecPL + kTok;
 constexpr size_t kSliceS = 0, kSliceDS = 2 * kSt, kSliceU = 4 * kSt, kSliceDR = 4 * kSt + 2 * kTok;
 constexpr size_t kSliceElems = 4 * kSt + 4 * kTok;
-__host__ __device__ constexpr size_t rec_elems(int P) { return kRecSlice + (size_t)(P / 64) * kSliceElems; }
+__host__ __device__ constexpr size_t rec_elems(int P, bool grad) {
+    return grad ? kRecSlice + (size_t)(P / 64) * kSliceElems : kRecPL;
+}
 
 }  // namespace dtc
 }  // namespace m3

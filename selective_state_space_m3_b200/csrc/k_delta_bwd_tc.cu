@@ -13,8 +13,8 @@
 //          E = dP o P + dA o A
 //   dG_C += e^{G_C} <S, dS'> + sum_j e^{G_C-G_j} k_j.Y_j;    dg_t = sum_{i >= t} dG_i
 //
-// Three passes.  The prefill kernel runs once more and records T, P, the state
-// before every chunk and U.  delta_rev_kernel carries dS from the last chunk to
+// Three passes.  The prefill runs once more and records T, P, the state before
+// every chunk and U.  delta_rev_kernel carries dS from the last chunk to
 // the first (one CTA a head and 32 columns; dU and T^T dU are the only
 // dependent products of a chunk) and records dS' and dR.  delta_grad_kernel
 // then takes all chunks at once, one CTA each.  dq and dk of a group's heads
@@ -125,7 +125,7 @@ __device__ __forceinline__ int length_of(const DeltaParams& q, int b) {
     return M3_IN(1, b, q.batch) ? min(max(q.lengths[b], 0), q.seqlen) : 0;
 }
 __device__ __forceinline__ long long ext_rec(const DeltaParams& q) {
-    return (long long)q.batch * q.nheads * q.nck * (long long)rec_elems(q.headdim);
+    return (long long)q.batch * q.nheads * q.nck * (long long)rec_elems(q.headdim, true);
 }
 
 // 64 token rows (chunk c) of q, k or one 64-column tile of v, dy into shared
@@ -144,6 +144,14 @@ __device__ __forceinline__ void load_rec(const DeltaParams& q, uint32_t dst, siz
     for (int e = threadIdx.x; e < rows * 8; e += kThreads) {
         const bool ok = M3_SPAN(3, o + e * 8, 8, ext_rec(q));
         cp16(at(dst, 0, e >> 3, e & 7), q.rec + (ok ? o + e * 8 : 0), ok);
+    }
+}
+
+// 64 rows of a recorded image of shared memory, as it is
+__device__ __forceinline__ void load_image(const DeltaParams& q, uint32_t dst, size_t o) {
+    for (int e = threadIdx.x; e < 512; e += kThreads) {
+        const bool ok = M3_SPAN(18, o + e * 8, 8, ext_rec(q));
+        cp16(dst + e * 16, q.rec + (ok ? o + e * 8 : 0), ok);
     }
 }
 
@@ -170,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_rev_kernel(DeltaParams q) {
     const int mt = warp & 3, nh = warp >> 2, qr = lane >> 2, qc = (lane & 3) * 2;
     const long long ext_k = (long long)q.batch * q.seqlen * q.ngroups * kN, ext_v = (long long)q.batch * q.seqlen * H * P;
     [[maybe_unused]] const long long ext_h = (long long)q.batch * H * kN * P;
-    const size_t rec = rec_elems(P);
+    const size_t rec = rec_elems(P, true);
     auto slice_at = [&](int c) { return ((size_t)bh * q.nck + c) * rec + kRecSlice + (size_t)(p0 >> 6) * kSliceElems + (p0 & 63); };
 
     auto load = [&](int c) {
@@ -181,8 +189,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_rev_kernel(DeltaParams q) {
         load_tokens(st + RV_Q, 8192, q.q, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
         load_tokens(st + RV_DY, 0, q.dy, row0, (size_t)H * P, (size_t)h * P + p0, 4, nt, ext_v);
         const size_t o = ((size_t)bh * q.nck + c) * rec;
-        load_rec(q, st + RV_T, o + kRecT, 128);
-        load_rec(q, st + RV_P, o + kRecP, 128);
+        load_image(q, st + RV_T, o + kRecX);
+        load_image(q, st + RV_T + 8192, o + kRecTL);
+        load_image(q, st + RV_P, o + kRecX + kTok);
+        load_image(q, st + RV_P + 8192, o + kRecPL);
         cp_commit();
     };
     // dS: warp w has rows 16 w .., all 32 columns
@@ -367,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
         }
         return;
     }
-    const size_t rec0 = ((size_t)bh * q.nck + c) * rec_elems(P);
+    const size_t rec0 = ((size_t)bh * q.nck + c) * rec_elems(P, true);
     load_tokens(sb + GR_K, 8192, q.k, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
     load_tokens(sb + GR_Q, 8192, q.q, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
     if (warp == 0) make_gates(load_raw(q, b, h, len, c), gt);
@@ -444,11 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
             const float2 Gi = gt->G[i];
             const float be = gt->beta[i];
             float2 fq, fk;
-            const size_t o = rec0 + kRecP + i * 64 + j;
+            const size_t o = rec0 + (sw128(i, j >> 3) >> 1) + (j & 7);
             float2 pv = make_float2(0.f, 0.f);
-            if (M3_SPAN(14, o + kTok, 2, ext_rec(q)))
-                pv = __fadd2_rn(unpack(*reinterpret_cast<const uint32_t*>(q.rec + o)),
-                                unpack(*reinterpret_cast<const uint32_t*>(q.rec + o + kTok)));
+            if (M3_SPAN(14, o + kRecPL, 2, ext_rec(q)))
+                pv = __fadd2_rn(unpack(*reinterpret_cast<const uint32_t*>(q.rec + o + kRecX + kTok)),
+                                unpack(*reinterpret_cast<const uint32_t*>(q.rec + o + kRecPL)));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float gam = i >= j + e ? ex2(diff_pair(Gi, gt->G[j + e])) : 0.f;
@@ -583,14 +593,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
 
 }  // namespace dbw
 
-size_t delta_record_bytes(const m3_dims& d) { return dtc::rec_elems(d.headdim) * 2; }
-
 cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st) {
     using namespace dbw;
     DeltaParams f = q;                       // records of the prefill
     f.y = nullptr;
     f.final_h = nullptr;
-    cudaError_t e = launch_delta_tc(d, f, status, st);
+    cudaError_t e = launch_delta_tc(d, f, true, status, st);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(delta_rev_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RV_BYTES);
     if (e != cudaSuccess) return e;

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 3 : 1) norm_kernel(NormParams q
                 for (int o = 8; o; o >>= 1) top = nmax(top, __shfl_xor_sync(kFull, top, o));
                 top = nmax(top, kTiny);
                 const int nb = (q.width + 127) >> 7;
-                if (in) __stcs(reinterpret_cast<uint2*>(q.y8 + base + c), e4m3x8(s[i], __fdividef(kE4M3Max, top)));
+                if (in) __stcs(reinterpret_cast<uint2*>(q.y8 + base + c), e4m3x8(s[i], __fdiv_rn(kE4M3Max, top)));
                 if (in && (c & 127) == 0 && M3_IN(7, row * nb + (c >> 7), q.rows * nb)) q.scale[row * nb + (c >> 7)] = top * (1.f / kE4M3Max);
                 top = 0.f;
             }
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 3 : 1) norm_kernel(NormParams q
             for (int i = 0; i < NV; ++i) {
                 const int c = (lane + tpr * i) * 8;
                 if (live && c < q.width && M3_SPAN(8, base + c, 8, ext))
-                    __stcs(reinterpret_cast<uint2*>(q.y8 + base + c), e4m3x8(s[i], __fdividef(kE4M3Max, top)));
+                    __stcs(reinterpret_cast<uint2*>(q.y8 + base + c), e4m3x8(s[i], __fdiv_rn(kE4M3Max, top)));
             }
             if (live && lane == 0 && M3_IN(9, row, q.rows)) q.scale[row] = top * (1.f / kE4M3Max);
         }

@@ -28,6 +28,7 @@ cudaError_t bounds_take_scan_ws(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_delta(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_delta_tc(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_delta_bwd_tc(BoundsRecord* out, bool clear);
+cudaError_t bounds_take_delta_prep(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_norm(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_api(BoundsRecord* out, bool clear);
 
@@ -650,6 +651,8 @@ static m3_status check_delta(const m3_dims* d, bool need_seq) {
 // whether the chunked tensor-core kernels take these dims
 static bool delta_chunked(const m3_dims& d) { return delta_tc_eligible(d) && !env_is("M3_DELTA_PATH", "token"); }
 
+static int delta_chunks(const m3_dims& d) { return (int)((d.seqlen + 63LL) / 64); }
+
 static DeltaParams delta_params(const m3_dims& d, const void* q, const void* k, const void* v, const float* g,
                                 const float* beta, float scale, const int* lengths) {
     DeltaParams p;
@@ -672,7 +675,10 @@ m3_status m3_delta_workspace_size(const m3_dims* d, size_t* bytes) {
     if (!bytes) return M3_ERR_INVALID_ARG;
     const m3_status s = check_delta(d, true);
     if (s != M3_OK) return s;
+    // the chunked path: a record a chunk
     *bytes = kWorkspaceHeaderBytes;
+    if (delta_chunked(*d))
+        *bytes += round256((size_t)d->batch * d->nheads * delta_chunks(*d) * delta_record_bytes(*d, false));
     return M3_OK;
 }
 
@@ -693,7 +699,9 @@ m3_status m3_delta_fwd(const m3_dims* d, const void* q, const void* k, const voi
     p.init_h = init_h;
     p.y = y;
     p.final_h = final_h;
-    const cudaError_t e = delta_chunked(*d) ? launch_delta_tc(*d, p, static_cast<int*>(workspace), st)
+    p.nck = delta_chunks(*d);
+    p.rec = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(workspace) + kWorkspaceHeaderBytes);
+    const cudaError_t e = delta_chunked(*d) ? launch_delta_tc(*d, p, false, static_cast<int*>(workspace), st)
                                             : launch_delta_seq(*d, p, st);
     return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }
@@ -733,7 +741,7 @@ static DeltaBwdLayout delta_bwd_layout(const m3_dims& d) {
     const size_t toks = units * d.seqlen * tiles;
     size_t off = kWorkspaceHeaderBytes;
     l.ckpt = off;    off = round256(off + (l.chunked ? 0 : units * l.nck * NP * sizeof(float)));
-    l.rec = off;     off = round256(off + (l.chunked ? units * l.nck * delta_record_bytes(d) : 0));
+    l.rec = off;     off = round256(off + (l.chunked ? units * l.nck * delta_record_bytes(d, true) : 0));
     l.part_qk = off; off = round256(off + toks * 2 * d.dstate * sizeof(float));
     l.part_g = off;  off = round256(off + toks * 2 * sizeof(float));
     l.total = off;
@@ -847,7 +855,8 @@ m3_status m3_debug_bounds_report(m3_bounds_report* out, int clear) {
     const Take takes[] = {bounds_take_scan_tc, bounds_take_scan_simt, bounds_take_step,
                           bounds_take_rope,    bounds_take_seq,       bounds_take_bwd,
                           bounds_take_phase,   bounds_take_scan_ws,   bounds_take_delta,
-                          bounds_take_delta_tc, bounds_take_delta_bwd_tc, bounds_take_norm,    bounds_take_api};
+                          bounds_take_delta_tc, bounds_take_delta_bwd_tc, bounds_take_delta_prep,
+                          bounds_take_norm,    bounds_take_api};
     out->enabled = 1;
     if (cudaDeviceSynchronize() != cudaSuccess) return M3_ERR_CUDA;
     for (Take take : takes) {

@@ -155,7 +155,7 @@ struct DeltaParams {
     float* ckpt;               // [b][h][nck][n][p]
     float* part_qk;            // [column tile][b][t][h][2][n]: parts of dq, dk
     float* part_g;             // [column tile][b][t][h][2]: parts of dg, dbeta
-    __nv_bfloat16* rec;        // chunked gradient: nck records a (b, h) (delta_tc.cuh)
+    __nv_bfloat16* rec;        // chunked path: nck records a (b, h) (delta_tc.cuh)
 };
 int delta_block_tokens(const m3_dims& d);
 int delta_tiles(const m3_dims& d);
@@ -164,9 +164,12 @@ cudaError_t launch_delta_seq_bwd(const m3_dims& d, const DeltaParams& q, cudaStr
 // chunked prefill on the tensor cores (bf16, N = 128, P a multiple of 64);
 // `status` is the workspace status word its bounded waits report to
 bool delta_tc_eligible(const m3_dims& d);
-cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st);
-// chunked gradient (same shapes): records of delta_record_bytes a chunk of 64 tokens
-size_t delta_record_bytes(const m3_dims& d);
+// (the records of k_delta_prep.cu, then the chain; grad: records for the gradient, no y)
+cudaError_t launch_delta_prep(const m3_dims& d, const DeltaParams& q, bool grad, int* status, cudaStream_t st);
+cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, bool grad, int* status, cudaStream_t st);
+// bytes of a record, one a chunk of 64 tokens of a (batch, head)
+size_t delta_record_bytes(const m3_dims& d, bool grad);
+// chunked gradient (same shapes)
 cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st);
 cudaError_t launch_delta_reduce(const m3_dims& d, const DeltaParams& q, int tiles, cudaStream_t st);
 cudaError_t launch_delta_step(const m3_dims& d, const DeltaParams& q, cudaStream_t st);
