@@ -13,9 +13,9 @@
 //
 // One CTA per (batch, head, PC columns) walks the chunks of its sequence:
 //   warp 0       one elected lane issues the tcgen05.mma
-//   warps 1-8    the arithmetic between them: S lives in registers in float32 (a
-//                thread has one state row and half the columns)
-//   warp 9       one lane issues the loads (three chunks ahead: K, Q by TMA, the
+//   warps 1..    the arithmetic between them: S lives in registers in float32 (a
+//                thread has one state row and 8 or 16 columns)
+//   last warp    one lane issues the loads (three chunks ahead: K, Q by TMA, the
 //                images of T and P; two of V)
 // Every product has M = 128 rows: [K; Q] against S gives K S and Q S at once,
 // and the tile [T - I; P] serves both T R (upper half of the accumulator) and
@@ -48,16 +48,17 @@ bool make_tile_map(CUtensorMap* map, const void* base, int inner, int R, int grp
 namespace dtc {
 
 constexpr int kP = 64;             // columns of a V tile; a CTA takes PC = 64, 32 or 16 of them
-constexpr int kState = 256;        // threads of the chain
-constexpr int kThreads = 32 + kState + 32;
+// Column groups of the arithmetic, four warps each: 16 or 8 columns a thread
+template <int PC> constexpr int kGroups = PC == 16 ? 2 : 4;
+template <int PC> constexpr int kState = 128 * kGroups<PC>;        // threads of the chain
+template <int PC> constexpr int kThreads = 32 + kState<PC> + 32;
 
 constexpr int OFF_KQ = 0;                       // 3 x 32 KB: two 64-column atoms, rows 0..63 K, 64..127 Q
 constexpr int OFF_X = OFF_KQ + 3 * 32768;       // 3 x 24 KB: [T - I hi; P], T - I lo (whose operand reads 64 more rows, unused)
 constexpr int kXBytes = 24576;
 constexpr int OFF_S = OFF_X + 3 * kXBytes;      // S hi, S lo (16 KB each: rows n, 64 p)
 constexpr int OFF_U = OFF_S;                    // R hi, lo; then e^{G_C-G} U in three parts (8 KB each: rows t, 64 p)
-constexpr int OFF_UB = OFF_S + 24576;           // U rounded, for P U
-constexpr int OFF_V = OFF_S + 32768;            // 2 x 8 KB
+constexpr int OFF_V = OFF_S + 32768;            // 2 x 8 KB; U rounded, for P U, takes V's place
 constexpr int OFF_GATES = OFF_V + 2 * 8192;     // 3 x 1 KB
 constexpr int OFF_MISC = OFF_GATES + 3 * (int)sizeof(ChainGates);
 
@@ -222,7 +223,7 @@ __device__ __forceinline__ uint32_t part_at(int row, int part, int ch, int tile_
 
 // DUMP: also write the records that the gradient's passes read
 template <int PC, bool DUMP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<PC>, 1)
     delta_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmV, DeltaParams q, int* status) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!M3_SPAN(5, smem - smem_raw, OFF_MISC + (int)sizeof(Misc), dyn_smem_bytes())) return;
     const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
     const Where w = where_am_i<PC>(q);
-    constexpr int kCols = PC / 2;                  // state columns a thread
+    constexpr int kCols = PC / kGroups<PC>;        // state columns a thread
     constexpr int W = kCols < 16 ? kCols : 16;     // columns of a TMEM load
     constexpr int NH = kCols / W, NG = kCols / 8;  // loads; 16-byte groups
     const int P = q.headdim;
@@ -240,13 +241,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < 3; ++i) { mbar_init(&m->full[i], 1); mbar_init(&m->freed[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&m->v_full[i], 1); mbar_init(&m->v_free[i], kState / 2); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&m->v_full[i], 1); mbar_init(&m->v_free[i], 1); }
         mbar_init(&m->drain, 1);
-        mbar_init(&m->s_ready, kState);
+        mbar_init(&m->s_ready, kState<PC>);
         mbar_init(&m->ks, 1);
-        mbar_init(&m->r, kState);
+        mbar_init(&m->r, kState<PC>);
         mbar_init(&m->tr, 1);
-        mbar_init(&m->u, kState);
+        mbar_init(&m->u, kState<PC>);
         mbar_init(&m->s, 1);
         mbar_init(&m->o, 1);
         m->abort_flag = 0;
@@ -271,10 +272,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idTl = idesc_bf16(128, PC, 0, 1);
         constexpr uint32_t idS = idesc_bf16(128, 3 * PC, 1, 1);    // A MN-major (K^T)
         const uint64_t bS = sdesc(sbase + OFF_S, 16384, 1024), bU = sdesc(sbase + OFF_U, 8192, 1024);
-        const uint64_t bUB = sdesc(sbase + OFF_UB, 8192, 1024);
         for (int c = 0; c < w.nch; ++c) {
             const uint32_t kq = sbase + OFF_KQ + (c % 3) * 32768;
             const uint64_t aKQ = sdesc(kq, 16, 1024), aKT = sdesc(kq, 16384, 1024);
+            const uint64_t bUB = sdesc(sbase + OFF_V + (c & 1) * 8192, 8192, 1024);
             const uint64_t aX = sdesc(sbase + OFF_X + (c % 3) * kXBytes, 16, 1024);
             const uint64_t aTL = sdesc(sbase + OFF_X + (c % 3) * kXBytes + 16384, 16, 1024);
             wait(&m->full[c % 3], c / 3, m, status, 1);
@@ -302,12 +303,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_TR + PC, aX + kk * 2, bUB + kk * 128, idTl, kk > 0);
             commit_one(&m->o);
+            commit_one(&m->v_free[c & 1]);
             commit_one(&m->freed[c % 3]);
         }
         commit_one(&m->drain);
         mbar_wait_flag(&m->drain, 0, &m->drain_flag, nullptr, 0);
         __syncwarp();
-    } else if (warp <= 8) {
+    } else if (warp <= kState<PC> / 32) {
         // ---------------------------------------------- the chain's arithmetic
         const int wk = tid - 32, wg = wk >> 7, quarter = warp & 3, row = quarter * 32 + lane, c0 = wg * kCols;
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
@@ -347,32 +349,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             mbar_arrive(&m->s_ready);
         };
-        if (w.nch > 0) store_state(0);
+        // beta V of chunk c; rows behind the end (other data, possibly not numbers) count as zero
+        float2 buf[kCols / 2];                     // top: beta V, R, then U; else Q S
+        auto load_v = [&](int c) {
+            wait(&m->v_full[c & 1], c >> 1, m, status, 10);
+            wait(&m->full[c % 3], c / 3, m, status, 11);
+            const float be = reinterpret_cast<const ChainGates*>(smem + OFF_GATES)[c % 3].beta[tok];
+            const float2 be2 = make_float2(be, be);
+#pragma unroll
+            for (int ch = 0; ch < NG; ++ch) {
+                const uint32_t o = sw128(tok, vch + ch);
+                uint4 vv = make_uint4(0u, 0u, 0u, 0u);
+                if (c * kC + tok < w.len && M3_SPAN(7, o, 16, 8192))
+                    vv = *reinterpret_cast<const uint4*>(smem + OFF_V + (c & 1) * 8192 + o);
+                const uint32_t u[4] = {vv.x, vv.y, vv.z, vv.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    buf[4 * ch + j] = __fmul2_rn(be2, make_float2(__uint_as_float(u[j] << 16),
+                                                                  __uint_as_float(u[j] & 0xffff0000u)));
+            }
+        };
+        if (w.nch > 0) {
+            store_state(0);
+            if (top) load_v(0);
+        }
 #pragma unroll 1
         for (int c = 0; c < w.nch; ++c) {
             const ChainGates* gt = reinterpret_cast<const ChainGates*>(smem + OFF_GATES) + c % 3;
-            float2 buf[kCols / 2];                 // top: beta V, R, then U; else Q S
             const bool tail = (c + 1) * kC > w.len;
             float whole;
             if (top) {
-                wait(&m->v_full[c & 1], c >> 1, m, status, 10);
-                wait(&m->full[c % 3], c / 3, m, status, 11);
-                const float be = gt->beta[tok], ba = -be * gt->a[tok], at = gt->at[tok];
+                const float ba = -gt->beta[tok] * gt->a[tok], at = gt->at[tok];
                 whole = gt->whole;
                 const bool in = c * kC + tok < w.len;
-                const float2 be2 = make_float2(be, be), ba2 = make_float2(ba, ba), at2 = make_float2(at, at);
-                // beta V; rows behind the end (other data, possibly not numbers) count as zero
-#pragma unroll
-                for (int ch = 0; ch < NG; ++ch) {
-                    const uint32_t o = sw128(tok, vch + ch);
-                    uint4 vv = make_uint4(0u, 0u, 0u, 0u);
-                    if (in && M3_SPAN(7, o, 16, 8192)) vv = *reinterpret_cast<const uint4*>(smem + OFF_V + (c & 1) * 8192 + o);
-                    const uint32_t u[4] = {vv.x, vv.y, vv.z, vv.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        buf[4 * ch + j] = __fmul2_rn(be2, make_float2(__uint_as_float(u[j] << 16),
-                                                                      __uint_as_float(u[j] & 0xffff0000u)));
-                }
+                const float2 ba2 = make_float2(ba, ba), at2 = make_float2(at, at);
                 wait(&m->ks, c, m, status, 12);
                 __syncwarp();
                 tc_fence_after();
@@ -396,9 +406,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_async_smem();
                 tc_fence_before();
                 mbar_arrive(&m->r);
-                // V is free only now: R, which is stored, shows that it has been read
-                // (an arrival right behind the loads let the next V overtake them)
-                mbar_arrive(&m->v_free[c & 1]);
                 wait(&m->tr, c, m, status, 13);
                 __syncwarp();
                 tc_fence_after();
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int ch = 0; ch < W / 8; ++ch) {
                         const int cc = ch0 + W / 8 * hh + ch;
-                        put16(smem, OFF_UB, sw128(tok, cc), 8192, round8(f + 4 * ch));
+                        put16(smem, OFF_V + (c & 1) * 8192, sw128(tok, cc), 8192, round8(f + 4 * ch));
                         if (DUMP) {
                             float2 e[4] = {f[4 * ch], f[4 * ch + 1], f[4 * ch + 2], f[4 * ch + 3]};
                             keep(slice_of(c) + kSliceU + tok * 64, W / 8 * hh + ch, take8(e));
@@ -427,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_async_smem();
                 tc_fence_before();
                 arrive_after(&m->u, __float_as_uint(whole));
+                if (c + 1 < w.nch) load_v(c + 1);  // while the state's update is made
             } else {
                 tc_fence_before();
                 mbar_arrive(&m->r);                // the previous chunk's P U has been read
@@ -448,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // K rows behind the sequence's end (other data, possibly not numbers)
                     // must be zeros: K^T U sums over all rows of the tile
                     const int nt = w.len - c * kC;
-                    for (int e = wg * 64 + tok; e < (kC - nt) * 16; e += kState / 2) {
+                    for (int e = wg * 64 + tok; e < (kC - nt) * 16; e += kState<PC> / 2) {
                         const int r = nt + (e >> 4), ch = e & 15;
                         put16(smem, OFF_KQ + (c % 3) * 32768 + (ch >> 3) * 16384, sw128(r, ch & 7), 16384, make_uint4(0u, 0u, 0u, 0u));
                     }
@@ -468,11 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < W / 2; ++j) S[W / 2 * hh + j] = __ffma2_rn(w2, S[W / 2 * hh + j], d[j]);
             }
-            // S takes the place of the U that P U reads
-            wait(&m->o, c, m, status, 17);
-            __syncwarp();
             if (c + 1 < w.nch) store_state(c + 1);
             if (!top) {
+                wait(&m->o, c, m, status, 17);
+                __syncwarp();
                 tc_fence_after();
                 const size_t o = (((size_t)w.b * q.seqlen + c * kC + tok) * q.nheads + w.h) * P + w.p0 + c0;
                 const bool in = c * kC + tok < w.len && M3_SPAN(8, o, kCols, (long long)q.batch * q.seqlen * q.nheads * P);
@@ -557,7 +564,7 @@ static cudaError_t launch_pc(const CUtensorMap& mK, const CUtensorMap& mQ, const
     const cudaError_t e = cudaFuncSetAttribute(delta_tc_kernel<PC, DUMP>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((long long)d.batch * d.nheads * (d.headdim / PC));
-    delta_tc_kernel<PC, DUMP><<<grid, kThreads, SMEM_BYTES, st>>>(mK, mQ, mV, q, status);
+    delta_tc_kernel<PC, DUMP><<<grid, kThreads<PC>, SMEM_BYTES, st>>>(mK, mQ, mV, q, status);
     return cudaGetLastError();
 }
 
