@@ -37,7 +37,6 @@ namespace dbw {
 
 using namespace dtc;
 
-constexpr int kThreads = 256;
 
 // a matrix in shared memory: rows of 128 bytes (64 columns), 16-byte groups
 // exchanged by row (sw128); columns 64.. go on `atom` bytes further
@@ -130,9 +129,10 @@ __device__ __forceinline__ long long ext_rec(const DeltaParams& q) {
 
 // 64 token rows (chunk c) of q, k or one 64-column tile of v, dy into shared
 // memory: `groups` 16-byte groups a row; rows behind the end are zeros
+template <int NT>
 __device__ __forceinline__ void load_tokens(uint32_t dst, int atom, const void* src, size_t row0, size_t pitch, size_t col,
                                             int groups, int nt, long long ext) {
-    for (int e = threadIdx.x; e < 64 * groups; e += kThreads) {
+    for (int e = threadIdx.x; e < 64 * groups; e += NT) {
         const int r = e / groups, g = e - r * groups;
         const size_t o = (row0 + r) * pitch + col + 8 * g;
         const bool ok = r < nt && M3_SPAN(2, o, 8, ext);
@@ -140,22 +140,25 @@ __device__ __forceinline__ void load_tokens(uint32_t dst, int atom, const void* 
     }
 }
 // `rows` rows of 64 recorded columns
+template <int NT>
 __device__ __forceinline__ void load_rec(const DeltaParams& q, uint32_t dst, size_t o, int rows) {
-    for (int e = threadIdx.x; e < rows * 8; e += kThreads) {
+    for (int e = threadIdx.x; e < rows * 8; e += NT) {
         const bool ok = M3_SPAN(3, o + e * 8, 8, ext_rec(q));
         cp16(at(dst, 0, e >> 3, e & 7), q.rec + (ok ? o + e * 8 : 0), ok);
     }
 }
 
 // 64 rows of a recorded image of shared memory, as it is
+template <int NT>
 __device__ __forceinline__ void load_image(const DeltaParams& q, uint32_t dst, size_t o) {
-    for (int e = threadIdx.x; e < 512; e += kThreads) {
+    for (int e = threadIdx.x; e < 512; e += NT) {
         const bool ok = M3_SPAN(18, o + e * 8, 8, ext_rec(q));
         cp16(dst + e * 16, q.rec + (ok ? o + e * 8 : 0), ok);
     }
 }
 
 // ------------------------------------------------------- the reverse chain --
+constexpr int kRevThreads = 256;
 constexpr int kPS = 32;                      // columns a CTA
 constexpr uint32_t RV_K = 0, RV_Q = 16384, RV_T = 32768, RV_P = 49152, RV_DY = 65536, RV_STAGE = 73728;
 constexpr uint32_t RV_DS = 2 * RV_STAGE;     // dS hi (columns 0..31), lo (32..63): 128 rows
@@ -165,7 +168,7 @@ constexpr uint32_t RV_DYS = RV_DR + 8192;    //   scale e^G dY
 constexpr uint32_t RV_GATES = RV_DYS + 8192;
 constexpr int RV_BYTES = RV_GATES + 2 * sizeof(Gates) + 128;
 
-__global__ void __launch_bounds__(kThreads, 1) delta_rev_kernel(DeltaParams q) {
+__global__ void __launch_bounds__(kRevThreads, 1) delta_rev_kernel(DeltaParams q) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     const uint32_t sb = (su32(smem_raw) + 127u) & ~127u;
     uint8_t* smem = smem_raw + (sb - su32(smem_raw));
@@ -185,14 +188,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_rev_kernel(DeltaParams q) {
         const uint32_t st = sb + (c & 1) * RV_STAGE;
         const int nt = min(kC, len - c * kC);
         const size_t row0 = (size_t)b * q.seqlen + c * kC;
-        load_tokens(st + RV_K, 8192, q.k, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
-        load_tokens(st + RV_Q, 8192, q.q, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
-        load_tokens(st + RV_DY, 0, q.dy, row0, (size_t)H * P, (size_t)h * P + p0, 4, nt, ext_v);
+        load_tokens<kRevThreads>(st + RV_K, 8192, q.k, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
+        load_tokens<kRevThreads>(st + RV_Q, 8192, q.q, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
+        load_tokens<kRevThreads>(st + RV_DY, 0, q.dy, row0, (size_t)H * P, (size_t)h * P + p0, 4, nt, ext_v);
         const size_t o = ((size_t)bh * q.nck + c) * rec;
-        load_image(q, st + RV_T, o + kRecX);
-        load_image(q, st + RV_T + 8192, o + kRecTL);
-        load_image(q, st + RV_P, o + kRecX + kTok);
-        load_image(q, st + RV_P + 8192, o + kRecPL);
+        load_image<kRevThreads>(q, st + RV_T, o + kRecX);
+        load_image<kRevThreads>(q, st + RV_T + 8192, o + kRecTL);
+        load_image<kRevThreads>(q, st + RV_P, o + kRecX + kTok);
+        load_image<kRevThreads>(q, st + RV_P + 8192, o + kRecPL);
         cp_commit();
     };
     // dS: warp w has rows 16 w .., all 32 columns
@@ -324,35 +327,43 @@ __global__ void __launch_bounds__(kThreads, 1) delta_rev_kernel(DeltaParams q) {
             }
     }
     // tokens behind the end of the sequence have no gradient
-    for (size_t e = (size_t)len * (kPS / 8) + tid; e < (size_t)q.seqlen * (kPS / 8); e += kThreads) {
+    for (size_t e = (size_t)len * (kPS / 8) + tid; e < (size_t)q.seqlen * (kPS / 8); e += kRevThreads) {
         const size_t vo = (((size_t)b * q.seqlen + e / (kPS / 8)) * H + h) * P + p0 + 8 * (e % (kPS / 8));
         if (M3_SPAN(10, vo, 8, ext_v)) *reinterpret_cast<uint4*>(dv + vo) = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
 // ------------------------------------------------ the gradients of a chunk --
+// 16 warps: warp w has 16 rows (w & 3) and a quarter of the columns (w >> 2).
+// Loads arrive in three groups, in the order of their use, so that the products
+// begin with the first.
+constexpr int kGradThreads = 512;
 constexpr uint32_t GR_K = 0, GR_Q = 16384, GR_DY = 32768, GR_V = 40960, GR_U = 49152, GR_DR = 65536, GR_S = 81920,
                    GR_DS = 114688, GR_GATES = 147456;
-constexpr uint32_t GR_DQK = GR_S, GR_DKK = GR_S + 16384;       // hi, lo each, where S was
+// where V, U and dR were, after the last slice: P's and A's gradients, rounded
+// (they meet K and Q only in products that end in dq and dk, which are rounded
+// too); the gradient of A with its transposed, one symmetric matrix
+constexpr uint32_t GR_DQK = GR_U, GR_DKK = GR_U + 8192;
 struct GradSums {
-    float row[2][kC], beta[2][kC], tail[2][kC];      // by column half
+    float row[4][kC], beta[4][kC], tail[4][kC];      // by column quarter
     float col[4][kC];                                // by row tile
-    float drv[kC], dot[8];
+    float drv[kC], dot[16];
 };
 constexpr int GR_BYTES = GR_GATES + sizeof(Gates) + sizeof(GradSums) + 128;
 
-__global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, int nchunks) {
+__global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaParams q, int nchunks) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     const uint32_t sb = (su32(smem_raw) + 127u) & ~127u;
     uint8_t* smem = smem_raw + (sb - su32(smem_raw));
     Gates* gt = reinterpret_cast<Gates*>(smem + GR_GATES);
     GradSums* gs = reinterpret_cast<GradSums*>(smem + GR_GATES + sizeof(Gates));
     if (!M3_SPAN(11, sb - su32(smem_raw), GR_GATES + sizeof(Gates) + sizeof(GradSums), dyn_smem_bytes())) return;
+    constexpr int NT = kGradThreads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, P = q.headdim, H = q.nheads;
     const int bh = blockIdx.x / nchunks, c = blockIdx.x % nchunks;
     const int b = bh / H, h = bh % H, hpg = H / q.ngroups, g = h / hpg;
     const int len = length_of(q, b), nt = min(kC, len - c * kC);
-    const int mt = warp & 3, nh = warp >> 2, qr = lane >> 2, qc = (lane & 3) * 2;
+    const int mt = warp & 3, nq = warp >> 2, qr = lane >> 2, qc = (lane & 3) * 2;
     const long long ext_k = (long long)q.batch * q.seqlen * q.ngroups * kN, ext_v = (long long)q.batch * q.seqlen * H * P;
     [[maybe_unused]] const long long toks = (long long)q.batch * q.seqlen * H;
     const size_t row0 = (size_t)b * q.seqlen + c * kC;
@@ -363,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
     __nv_bfloat16* out_b = static_cast<__nv_bfloat16*>(q.dbeta);
     if (nt <= 0) {                                             // behind the end (a group's heads: the sum kernel's zeros)
         if (hpg == 1) {
-            for (int e = tid; e < rows * 16; e += kThreads) {
+            for (int e = tid; e < rows * 16; e += NT) {
                 const size_t o = ((row0 + (e >> 4)) * q.ngroups + g) * kN + 8 * (e & 15);
                 if (M3_SPAN(12, o, 8, ext_k)) {
                     *reinterpret_cast<uint4*>(out_q + o) = make_uint4(0u, 0u, 0u, 0u);
@@ -378,37 +389,56 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
         return;
     }
     const size_t rec0 = ((size_t)bh * q.nck + c) * rec_elems(P, true);
-    load_tokens(sb + GR_K, 8192, q.k, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
-    load_tokens(sb + GR_Q, 8192, q.q, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
-    if (warp == 0) make_gates(load_raw(q, b, h, len, c), gt);
     const Mat K = {sb + GR_K, 8192}, Q = {sb + GR_Q, 8192}, dY = {sb + GR_DY, 0};
     const Mat Uh = {sb + GR_U, 0}, Ul = {sb + GR_U + 8192, 0}, dRh = {sb + GR_DR, 0}, dRl = {sb + GR_DR + 8192, 0};
     const Mat Sh = {sb + GR_S, 0}, Dh = {sb + GR_DS, 0};
 
-    float dP[4][4], dA[4][4], Z[8][4], X[8][4], Y[8][4];
-    zero<4>(dP); zero<4>(dA); zero<8>(Z); zero<8>(X); zero<8>(Y);
-    float dot = 0.f, drv = 0.f;                                // <S, dS'>, dR . v of row tid / 4
+    float kk[2][4], dP[2][4], dA[2][4], Z[4][4], X[4][4], Y[4][4];
+    zero<2>(kk); zero<2>(dP); zero<2>(dA); zero<4>(Z); zero<4>(X); zero<4>(Y);
+    float dot = 0.f, drv = 0.f;                                // <S, dS'>, dR . v of row tid / 8
     for (int sl = 0; sl < P / 64; ++sl) {
         if (sl > 0) __syncthreads();
         const size_t o = rec0 + kRecSlice + sl * kSliceElems;
-        load_tokens(sb + GR_DY, 0, q.dy, row0, (size_t)H * P, (size_t)h * P + 64 * sl, 8, nt, ext_v);
-        load_tokens(sb + GR_V, 0, q.v, row0, (size_t)H * P, (size_t)h * P + 64 * sl, 8, nt, ext_v);
-        load_rec(q, sb + GR_U, o + kSliceU, 128);
-        load_rec(q, sb + GR_DR, o + kSliceDR, 128);
-        load_rec(q, sb + GR_S, o + kSliceS, 256);
-        load_rec(q, sb + GR_DS, o + kSliceDS, 256);
+        load_tokens<NT>(sb + GR_DY, 0, q.dy, row0, (size_t)H * P, (size_t)h * P + 64 * sl, 8, nt, ext_v);
+        load_rec<NT>(q, sb + GR_U, o + kSliceU, 128);
+        load_rec<NT>(q, sb + GR_DR, o + kSliceDR, 128);
         cp_commit();
+        load_rec<NT>(q, sb + GR_S, o + kSliceS, 256);
+        load_tokens<NT>(sb + GR_V, 0, q.v, row0, (size_t)H * P, (size_t)h * P + 64 * sl, 8, nt, ext_v);
+        cp_commit();
+        load_rec<NT>(q, sb + GR_DS, o + kSliceDS, 256);
+        if (sl == 0) {
+            load_tokens<NT>(sb + GR_K, 8192, q.k, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
+            load_tokens<NT>(sb + GR_Q, 8192, q.q, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
+        }
+        cp_commit();
+        if (sl == 0 && warp == 0) make_gates(load_raw(q, b, h, len, c), gt);
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        __syncthreads();
+        mm<2, 64, false, true, true>(dP, dY, 16 * mt, Uh, 16 * nq, Ul.base, 16 * nq);
+        mm<2, 64, false, true, true>(dA, dRh, 16 * mt, Uh, 16 * nq, Ul.base, 16 * nq);
+        mm<2, 64, false, true, false>(dA, dRl, 16 * mt, Uh, 16 * nq, 0, 0);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        mm<4, 64, false, true, true>(Z, dY, 16 * mt, Sh, 32 * nq, Sh.base + 16384, 32 * nq);
+        mm<4, 64, false, true, true>(X, dRh, 16 * mt, Sh, 32 * nq, Sh.base + 16384, 32 * nq);
+        mm<4, 64, false, true, false>(X, dRl, 16 * mt, Sh, 32 * nq, 0, 0);
+        {
+            const uint32_t p = at(0, 0, tid >> 3, tid & 7);
+            const uint4 r0 = lds128(dRh.base + p), r1 = lds128(dRl.base + p), v0 = lds128(sb + GR_V + p);
+            const uint32_t rh[4] = {r0.x, r0.y, r0.z, r0.w}, rl[4] = {r1.x, r1.y, r1.z, r1.w}, vv[4] = {v0.x, v0.y, v0.z, v0.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 d = __fadd2_rn(unpack(rh[j]), unpack(rl[j])), v = unpack(vv[j]);
+                drv = fmaf(d.x, v.x, fmaf(d.y, v.y, drv));
+            }
+        }
         cp_wait();
         __syncthreads();
-        mm<4, 64, false, true, true>(dP, dY, 16 * mt, Uh, 32 * nh, Ul.base, 32 * nh);
-        mm<4, 64, false, true, true>(dA, dRh, 16 * mt, Uh, 32 * nh, Ul.base, 32 * nh);
-        mm<4, 64, false, true, false>(dA, dRl, 16 * mt, Uh, 32 * nh, 0, 0);
-        mm<8, 64, false, true, true>(Z, dY, 16 * mt, Sh, 64 * nh, Sh.base + 16384, 64 * nh);
-        mm<8, 64, false, true, true>(X, dRh, 16 * mt, Sh, 64 * nh, Sh.base + 16384, 64 * nh);
-        mm<8, 64, false, true, false>(X, dRl, 16 * mt, Sh, 64 * nh, 0, 0);
-        mm<8, 64, false, true, true>(Y, Uh, 16 * mt, Dh, 64 * nh, Dh.base + 16384, 64 * nh);
-        mm<8, 64, false, true, false>(Y, Ul, 16 * mt, Dh, 64 * nh, 0, 0);
-        for (int e = tid; e < 128 * 8; e += kThreads) {
+        mm<4, 64, false, true, true>(Y, Uh, 16 * mt, Dh, 32 * nq, Dh.base + 16384, 32 * nq);
+        mm<4, 64, false, true, false>(Y, Ul, 16 * mt, Dh, 32 * nq, 0, 0);
+#pragma unroll
+        for (int e = tid; e < 128 * 8; e += NT) {
             const uint32_t p = at(0, 0, e >> 3, e & 7);
             const uint4 s0 = lds128(sb + GR_S + p), s1 = lds128(sb + GR_S + 16384 + p);
             const uint4 d0 = lds128(sb + GR_DS + p), d1 = lds128(sb + GR_DS + 16384 + p);
@@ -420,40 +450,28 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
                 dot = fmaf(a.x, d.x, fmaf(a.y, d.y, dot));
             }
         }
-#pragma unroll
-        for (int j2 = 0; j2 < 2; ++j2) {
-            const uint32_t p = at(0, 0, tid >> 2, 2 * (tid & 3) + j2);
-            const uint4 r0 = lds128(dRh.base + p), r1 = lds128(dRl.base + p), v0 = lds128(sb + GR_V + p);
-            const uint32_t rh[4] = {r0.x, r0.y, r0.z, r0.w}, rl[4] = {r1.x, r1.y, r1.z, r1.w}, vv[4] = {v0.x, v0.y, v0.z, v0.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 d = __fadd2_rn(unpack(rh[j]), unpack(rl[j])), v = unpack(vv[j]);
-                drv = fmaf(d.x, v.x, fmaf(d.y, v.y, drv));
-            }
-        }
     }
-    float kk[4][4];
-    zero<4>(kk);
-    mm<4, 128, false, true, false>(kk, K, 16 * mt, K, 32 * nh, 0, 0);
-    __syncthreads();                                           // S has been read: its place takes dP and D
+    mm<2, 128, false, true, false>(kk, K, 16 * mt, K, 16 * nq, 0, 0);
+    __syncthreads();                                           // U and dR have been read: their place takes dP and D
     drv += __shfl_xor_sync(kFull, drv, 1);
     drv += __shfl_xor_sync(kFull, drv, 2);
-    if ((tid & 3) == 0) gs->drv[tid >> 2] = drv;
+    drv += __shfl_xor_sync(kFull, drv, 4);
+    if ((tid & 7) == 0) gs->drv[tid >> 3] = drv;
 #pragma unroll
     for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
     if (lane == 0) gs->dot[warp] = dot;
 
     float rowG[2] = {0.f, 0.f}, rowB[2] = {0.f, 0.f}, tail[2] = {0.f, 0.f};
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        const int j = 32 * nh + 8 * n + qc;
+    for (int n = 0; n < 2; ++n) {
+        const int j = 16 * nq + 8 * n + qc;
         float cs[2] = {0.f, 0.f};
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int i = 16 * mt + qr + 8 * r;
             const float2 Gi = gt->G[i];
             const float be = gt->beta[i];
-            float2 fq, fk;
+            float fq[2];
             const size_t o = rec0 + (sw128(i, j >> 3) >> 1) + (j & 7);
             float2 pv = make_float2(0.f, 0.f);
             if (M3_SPAN(14, o + kRecPL, 2, ext_rec(q)))
@@ -469,13 +487,15 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
                 rowG[r] += E;
                 cs[e] += E;
                 rowB[r] += t;
-                (e ? fq.y : fq.x) = q.scale * gam * dp;
-                (e ? fk.y : fk.x) = be * da;
+                fq[e] = q.scale * gam * dp;
+                // D at (i, j) and (j, i); the diagonal is zero
+                const __nv_bfloat16 v = __float2bfloat16_rn(be * da);
+                if (i >= j + e && M3_IN(19, i * 64 + j + e, 4096)) {
+                    *reinterpret_cast<__nv_bfloat16*>(smem + elem(GR_DKK, i, j + e)) = v;
+                    *reinterpret_cast<__nv_bfloat16*>(smem + elem(GR_DKK, j + e, i)) = v;
+                }
             }
-            sts32(elem(sb + GR_DQK, i, j), take2(fq));
-            sts32(elem(sb + GR_DQK + 8192, i, j), pack_bf16x2(fq.x, fq.y));
-            sts32(elem(sb + GR_DKK, i, j), take2(fk));
-            sts32(elem(sb + GR_DKK + 8192, i, j), pack_bf16x2(fk.x, fk.y));
+            sts32(elem(sb + GR_DQK, i, j), pack_bf16x2(fq[0], fq[1]));
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -490,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
         const float a = gt->a[i], tl = gt->at[i], be = gt->beta[i], sa = q.scale * a, ba = be * a;
         float zq = 0.f, xk = 0.f, yk = 0.f;
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const int col = 64 * nh + 8 * n + qc;
+        for (int n = 0; n < 4; ++n) {
+            const int col = 32 * nq + 8 * n + qc;
             const uint32_t p = at(0, 8192, i, col >> 3) + (col & 7) * 2;
             const float2 qv = unpack(lds32(sb + GR_Q + p)), kv = unpack(lds32(sb + GR_K + p));
             zq = fmaf(Z[n][2 * r], qv.x, fmaf(Z[n][2 * r + 1], qv.y, zq));
@@ -513,29 +533,24 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
             tail[r] += __shfl_xor_sync(kFull, tail[r], o);
         }
         if ((lane & 3) == 0) {
-            gs->row[nh][i] = rowG[r];
-            gs->beta[nh][i] = rowB[r];
-            gs->tail[nh][i] = tail[r];
+            gs->row[nq][i] = rowG[r];
+            gs->beta[nq][i] = rowB[r];
+            gs->tail[nq][i] = tail[r];
         }
     }
     __syncthreads();
-    const Mat Pq = {sb + GR_DQK, 0}, Pq2 = {sb + GR_DQK + 8192, 0}, Dk = {sb + GR_DKK, 0}, Dk2 = {sb + GR_DKK + 8192, 0};
-    mm<8, 64, false, false, false>(Z, Pq, 16 * mt, K, 64 * nh, 0, 0);
-    mm<8, 64, false, false, false>(Z, Pq2, 16 * mt, K, 64 * nh, 0, 0);
-    mm<8, 64, true, false, false>(Y, Pq, 16 * mt, Q, 64 * nh, 0, 0);
-    mm<8, 64, true, false, false>(Y, Pq2, 16 * mt, Q, 64 * nh, 0, 0);
-    mm<8, 64, false, false, false>(Y, Dk, 16 * mt, K, 64 * nh, 0, 0);
-    mm<8, 64, false, false, false>(Y, Dk2, 16 * mt, K, 64 * nh, 0, 0);
-    mm<8, 64, true, false, false>(Y, Dk, 16 * mt, K, 64 * nh, 0, 0);
-    mm<8, 64, true, false, false>(Y, Dk2, 16 * mt, K, 64 * nh, 0, 0);
+    const Mat Pq = {sb + GR_DQK, 0}, Dk = {sb + GR_DKK, 0};
+    mm<4, 64, false, false, false>(Z, Pq, 16 * mt, K, 32 * nq, 0, 0);
+    mm<4, 64, true, false, false>(Y, Pq, 16 * mt, Q, 32 * nq, 0, 0);
+    mm<4, 64, false, false, false>(Y, Dk, 16 * mt, K, 32 * nq, 0, 0);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int i = 16 * mt + qr + 8 * r;
         const float m = i < nt ? 1.f : 0.f;
         if (i >= rows) continue;
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const int col = 64 * nh + 8 * n + qc;
+        for (int n = 0; n < 4; ++n) {
+            const int col = 32 * nq + 8 * n + qc;
             const float2 vq = make_float2(m * Z[n][2 * r], m * Z[n][2 * r + 1]), vk = make_float2(m * Y[n][2 * r], m * Y[n][2 * r + 1]);
             if (hpg == 1) {
                 const size_t o = ((row0 + i) * q.ngroups + g) * kN + col;
@@ -558,13 +573,17 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = 2 * lane + e;
-            d[e] = gs->row[0][i] + gs->row[1][i] - (gs->col[0][i] + gs->col[1][i] + gs->col[2][i] + gs->col[3][i]);
-            tl += gs->tail[0][i] + gs->tail[1][i];
+            d[e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                d[e] += gs->row[j][i] - gs->col[j][i];
+                tl += gs->tail[j][i];
+            }
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) tl += __shfl_xor_sync(kFull, tl, o);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) total += gs->dot[j];
+        for (int j = 0; j < 16; ++j) total += gs->dot[j];
         tl += gt->whole * total;
         float sum = d[0] + d[1];
 #pragma unroll
@@ -579,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
             const size_t o = (row0 + i) * H + h;
             if (i >= rows || !M3_IN(17, o, toks)) continue;
             const float vg = i < nt ? dg[e] : 0.f;
-            const float vb = i < nt ? gs->drv[i] + gs->beta[0][i] + gs->beta[1][i] : 0.f;
+            const float vb = i < nt ? gs->drv[i] + gs->beta[0][i] + gs->beta[1][i] + gs->beta[2][i] + gs->beta[3][i] : 0.f;
             if (hpg == 1) {
                 if (out_g) out_g[o] = __float2bfloat16_rn(vg);
                 out_b[o] = __float2bfloat16_rn(vb);
@@ -603,12 +622,12 @@ cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* sta
     e = cudaFuncSetAttribute(delta_rev_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RV_BYTES);
     if (e != cudaSuccess) return e;
     const long long bh = (long long)d.batch * d.nheads;
-    delta_rev_kernel<<<(unsigned)(bh * (d.headdim / kPS)), dbw::kThreads, RV_BYTES, st>>>(q);
+    delta_rev_kernel<<<(unsigned)(bh * (d.headdim / kPS)), kRevThreads, RV_BYTES, st>>>(q);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_BYTES);
     if (e != cudaSuccess) return e;
-    delta_grad_kernel<<<(unsigned)(bh * q.nck), dbw::kThreads, GR_BYTES, st>>>(q, q.nck);
+    delta_grad_kernel<<<(unsigned)(bh * q.nck), kGradThreads, GR_BYTES, st>>>(q, q.nck);
     e = cudaGetLastError();
     if (e != cudaSuccess || d.nheads == d.ngroups) return e;
     return launch_delta_reduce(d, q, 1, st);
