@@ -435,7 +435,7 @@ m3_status m3_selftest_bounded_wait(void* workspace, size_t workspace_bytes, void
  * combine, 3 decode step, 4 rope, 5 transition variants, 6 backward,
  * 7 phase prologues, 8 persistent prefill, 9 this self-test, 10 delta rule,
  * 11 norm, 12 chunked delta rule, 13 its gradient, 14 its
- * per-chunk matrices; for a span the
+ * per-chunk matrices, 15 its gradient's chain; for a span the
  * index is its last element).  `clear` != 0 resets the records after reading.
  * M3_ERR_INVALID_ARG for a NULL `out`, M3_ERR_CUDA if the device cannot be
  * read.  Host call; the release build touches no device. */

@@ -14,10 +14,9 @@
 //   dG_C += e^{G_C} <S, dS'> + sum_j e^{G_C-G_j} k_j.Y_j;    dg_t = sum_{i >= t} dG_i
 //
 // Three passes.  The prefill runs once more and records T, P, the state before
-// every chunk and U.  delta_rev_kernel carries dS from the last chunk to
-// the first (one CTA a head and 32 columns; dU and T^T dU are the only
-// dependent products of a chunk) and records dS' and dR.  delta_grad_kernel
-// then takes all chunks at once, one CTA each.  dq and dk of a group's heads
+// every chunk and U.  k_delta_rev.cu carries dS from the last chunk to the first
+// and records dS' and dR.  delta_grad_kernel here then takes all chunks at once,
+// one CTA each.  dq and dk of a group's heads
 // are added by a further kernel in a fixed order.
 //
 // The chain and all that feeds sums keep float32 values as two bfloat16 parts
@@ -145,191 +144,6 @@ __device__ __forceinline__ void load_rec(const DeltaParams& q, uint32_t dst, siz
     for (int e = threadIdx.x; e < rows * 8; e += NT) {
         const bool ok = M3_SPAN(3, o + e * 8, 8, ext_rec(q));
         cp16(at(dst, 0, e >> 3, e & 7), q.rec + (ok ? o + e * 8 : 0), ok);
-    }
-}
-
-// 64 rows of a recorded image of shared memory, as it is
-template <int NT>
-__device__ __forceinline__ void load_image(const DeltaParams& q, uint32_t dst, size_t o) {
-    for (int e = threadIdx.x; e < 512; e += NT) {
-        const bool ok = M3_SPAN(18, o + e * 8, 8, ext_rec(q));
-        cp16(dst + e * 16, q.rec + (ok ? o + e * 8 : 0), ok);
-    }
-}
-
-// ------------------------------------------------------- the reverse chain --
-constexpr int kRevThreads = 256;
-constexpr int kPS = 32;                      // columns a CTA
-constexpr uint32_t RV_K = 0, RV_Q = 16384, RV_T = 32768, RV_P = 49152, RV_DY = 65536, RV_STAGE = 73728;
-constexpr uint32_t RV_DS = 2 * RV_STAGE;     // dS hi (columns 0..31), lo (32..63): 128 rows
-constexpr uint32_t RV_DU = RV_DS + 16384;    // 64 rows each, hi and lo side by side: dU,
-constexpr uint32_t RV_DR = RV_DU + 8192;     //   - beta e^G dR,
-constexpr uint32_t RV_DYS = RV_DR + 8192;    //   scale e^G dY
-constexpr uint32_t RV_GATES = RV_DYS + 8192;
-constexpr int RV_BYTES = RV_GATES + 2 * sizeof(Gates) + 128;
-
-__global__ void __launch_bounds__(kRevThreads, 1) delta_rev_kernel(DeltaParams q) {
-    extern __shared__ __align__(128) uint8_t smem_raw[];
-    const uint32_t sb = (su32(smem_raw) + 127u) & ~127u;
-    uint8_t* smem = smem_raw + (sb - su32(smem_raw));
-    Gates* gates = reinterpret_cast<Gates*>(smem + RV_GATES);
-    if (!M3_SPAN(4, sb - su32(smem_raw), RV_GATES + 2 * sizeof(Gates), dyn_smem_bytes())) return;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, P = q.headdim, H = q.nheads;
-    const int slices = P / kPS, bh = blockIdx.x / slices, p0 = (blockIdx.x % slices) * kPS;
-    const int b = bh / H, h = bh % H, g = h / (H / q.ngroups);
-    const int len = length_of(q, b), nch = (len + kC - 1) / kC;
-    const int mt = warp & 3, nh = warp >> 2, qr = lane >> 2, qc = (lane & 3) * 2;
-    const long long ext_k = (long long)q.batch * q.seqlen * q.ngroups * kN, ext_v = (long long)q.batch * q.seqlen * H * P;
-    [[maybe_unused]] const long long ext_h = (long long)q.batch * H * kN * P;
-    const size_t rec = rec_elems(P, true);
-    auto slice_at = [&](int c) { return ((size_t)bh * q.nck + c) * rec + kRecSlice + (size_t)(p0 >> 6) * kSliceElems + (p0 & 63); };
-
-    auto load = [&](int c) {
-        const uint32_t st = sb + (c & 1) * RV_STAGE;
-        const int nt = min(kC, len - c * kC);
-        const size_t row0 = (size_t)b * q.seqlen + c * kC;
-        load_tokens<kRevThreads>(st + RV_K, 8192, q.k, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
-        load_tokens<kRevThreads>(st + RV_Q, 8192, q.q, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
-        load_tokens<kRevThreads>(st + RV_DY, 0, q.dy, row0, (size_t)H * P, (size_t)h * P + p0, 4, nt, ext_v);
-        const size_t o = ((size_t)bh * q.nck + c) * rec;
-        load_image<kRevThreads>(q, st + RV_T, o + kRecX);
-        load_image<kRevThreads>(q, st + RV_T + 8192, o + kRecTL);
-        load_image<kRevThreads>(q, st + RV_P, o + kRecX + kTok);
-        load_image<kRevThreads>(q, st + RV_P + 8192, o + kRecPL);
-        cp_commit();
-    };
-    // dS: warp w has rows 16 w .., all 32 columns
-    float dS[4][4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const size_t o = ((size_t)bh * kN + 16 * warp + qr + 8 * (i >> 1)) * P + p0 + 8 * n + qc + (i & 1);
-            dS[n][i] = (q.d_final_h && M3_IN(5, o, ext_h)) ? q.d_final_h[o] : 0.f;
-        }
-    // dS into shared memory and, as the gradient of the state behind chunk c, into the record
-    auto keep_ds = [&](int c) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = 16 * warp + qr + 8 * r, col = 8 * n + qc;
-                float2 f = make_float2(dS[n][2 * r], dS[n][2 * r + 1]);
-                const uint32_t hi = take2(f), lo = pack_bf16x2(f.x, f.y);
-                sts32(elem(sb + RV_DS, row, col), hi);
-                sts32(elem(sb + RV_DS, row, 32 + col), lo);
-                const size_t o = slice_at(c) + kSliceDS + row * 64 + col;
-                if (M3_SPAN(6, o + kSt, 2, ext_rec(q))) {
-                    *reinterpret_cast<uint32_t*>(q.rec + o) = hi;
-                    *reinterpret_cast<uint32_t*>(q.rec + o + kSt) = lo;
-                }
-            }
-    };
-    Raw raw = {};
-    if (nch > 0) {
-        load(nch - 1);
-        keep_ds(nch - 1);
-        if (warp == 0) {
-            raw = load_raw(q, b, h, len, nch - 1);
-            make_gates(raw, &gates[(nch - 1) & 1]);
-            if (nch > 1) raw = load_raw(q, b, h, len, nch - 2);
-        }
-    }
-    __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(q.dv);
-    for (int c = nch - 1; c >= 0; --c) {
-        const uint32_t st = sb + (c & 1) * RV_STAGE;
-        const Gates* gt = &gates[c & 1];
-        const int nt = min(kC, len - c * kC);
-        cp_wait();
-        __syncthreads();
-        if (c > 0) load(c - 1);
-        {                                    // scale e^G dY
-            const int r = tid >> 2, ch = tid & 3;
-            const uint4 v = lds128(at(st + RV_DY, 0, r, ch));
-            const float s = q.scale * gt->a[r];
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-            float2 f[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = __fmul2_rn(make_float2(s, s), unpack(u[j]));
-            sts128(at(sb + RV_DYS, 0, r, ch), take8(f));
-            sts128(at(sb + RV_DYS, 0, r, 4 + ch), round8(f));
-        }
-        float dU[2][4], t[2][4];
-        zero<2>(dU);
-        zero<2>(t);
-        const Mat K = {st + RV_K, 8192}, Q = {st + RV_Q, 8192}, T = {st + RV_T, 0}, Tl = {st + RV_T + 8192, 0};
-        const Mat Ph = {st + RV_P, 0}, Pl = {st + RV_P + 8192, 0}, dY = {st + RV_DY, 0};
-        mm<2, 64, true, false, false>(dU, Ph, 16 * mt, dY, 16 * nh, 0, 0);
-        mm<2, 64, true, false, false>(dU, Pl, 16 * mt, dY, 16 * nh, 0, 0);
-        mm<2, 128, false, false, true>(t, K, 16 * mt, {sb + RV_DS, 0}, 16 * nh, sb + RV_DS, 32 + 16 * nh);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = 16 * mt + qr + 8 * r;
-            const float e = gt->at[row];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int col = 16 * nh + 8 * n + qc;
-                float2 f = make_float2(fmaf(e, t[n][2 * r], dU[n][2 * r]), fmaf(e, t[n][2 * r + 1], dU[n][2 * r + 1]));
-                dU[n][2 * r] = f.x;
-                dU[n][2 * r + 1] = f.y;
-                sts32(elem(sb + RV_DU, row, col), take2(f));
-                sts32(elem(sb + RV_DU, row, 32 + col), pack_bf16x2(f.x, f.y));
-            }
-        }
-        __syncthreads();
-        // dR = dU + (T - I)^T dU
-        mm<2, 64, true, false, true>(dU, T, 16 * mt, {sb + RV_DU, 0}, 16 * nh, sb + RV_DU, 32 + 16 * nh);
-        mm<2, 64, true, false, false>(dU, Tl, 16 * mt, {sb + RV_DU, 0}, 16 * nh, 0, 0);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = 16 * mt + qr + 8 * r;
-            const float be = gt->beta[row], s = -be * gt->a[row];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int col = 16 * nh + 8 * n + qc;
-                const float2 d = make_float2(dU[n][2 * r], dU[n][2 * r + 1]);
-                float2 f = d;
-                const size_t o = slice_at(c) + kSliceDR + row * 64 + col;
-                const uint32_t hi = take2(f), lo = pack_bf16x2(f.x, f.y);
-                if (M3_SPAN(7, o + kTok, 2, ext_rec(q))) {
-                    *reinterpret_cast<uint32_t*>(q.rec + o) = hi;
-                    *reinterpret_cast<uint32_t*>(q.rec + o + kTok) = lo;
-                }
-                const size_t vo = (((size_t)b * q.seqlen + c * kC + row) * H + h) * P + p0 + col;
-                if (row < nt && M3_SPAN(8, vo, 2, ext_v))
-                    *reinterpret_cast<uint32_t*>(dv + vo) = pack_bf16x2(be * d.x, be * d.y);
-                f = make_float2(s * d.x, s * d.y);
-                sts32(elem(sb + RV_DR, row, col), take2(f));
-                sts32(elem(sb + RV_DR, row, 32 + col), pack_bf16x2(f.x, f.y));
-            }
-        }
-        const float whole = gt->whole;
-        if (warp == 0 && c > 0) {
-            make_gates(raw, &gates[(c - 1) & 1]);
-            if (c > 1) raw = load_raw(q, b, h, len, c - 2);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dS[n][i] *= whole;
-        mm<4, 64, true, false, true>(dS, Q, 16 * warp, {sb + RV_DYS, 0}, 0, sb + RV_DYS, 32);
-        mm<4, 64, true, false, true>(dS, K, 16 * warp, {sb + RV_DR, 0}, 0, sb + RV_DR, 32);
-        if (c > 0) keep_ds(c - 1);
-    }
-    if (q.d_init_h) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const size_t o = ((size_t)bh * kN + 16 * warp + qr + 8 * r) * P + p0 + 8 * n + qc;
-                if (M3_SPAN(9, o, 2, ext_h)) *reinterpret_cast<float2*>(q.d_init_h + o) = make_float2(dS[n][2 * r], dS[n][2 * r + 1]);
-            }
-    }
-    // tokens behind the end of the sequence have no gradient
-    for (size_t e = (size_t)len * (kPS / 8) + tid; e < (size_t)q.seqlen * (kPS / 8); e += kRevThreads) {
-        const size_t vo = (((size_t)b * q.seqlen + e / (kPS / 8)) * H + h) * P + p0 + 8 * (e % (kPS / 8));
-        if (M3_SPAN(10, vo, 8, ext_v)) *reinterpret_cast<uint4*>(dv + vo) = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -619,15 +433,11 @@ cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* sta
     f.final_h = nullptr;
     cudaError_t e = launch_delta_tc(d, f, true, status, st);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(delta_rev_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RV_BYTES);
-    if (e != cudaSuccess) return e;
-    const long long bh = (long long)d.batch * d.nheads;
-    delta_rev_kernel<<<(unsigned)(bh * (d.headdim / kPS)), kRevThreads, RV_BYTES, st>>>(q);
-    e = cudaGetLastError();
+    e = launch_delta_rev(d, q, status, st);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_BYTES);
     if (e != cudaSuccess) return e;
-    delta_grad_kernel<<<(unsigned)(bh * q.nck), kGradThreads, GR_BYTES, st>>>(q, q.nck);
+    delta_grad_kernel<<<(unsigned)((long long)d.batch * d.nheads * q.nck), kGradThreads, GR_BYTES, st>>>(q, q.nck);
     e = cudaGetLastError();
     if (e != cudaSuccess || d.nheads == d.ngroups) return e;
     return launch_delta_reduce(d, q, 1, st);

@@ -78,149 +78,6 @@ static_assert(SMEM_BYTES <= 232448, "shared memory of the delta kernel");
 __device__ __forceinline__ bool wait(uint64_t* b, int phase, Misc* m, int* status, int where) {
     return mbar_wait_flag(b, (uint32_t)(phase & 1), &m->abort_flag, status, where);
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(su32(bar)) : "memory");
-}
-__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-
-// arrival that waits for a value loaded from shared memory (not negative, so its
-// sign bit, zero, can stand in the address): an arrival right behind a load does
-// not wait for it, and the next chunk's data may overtake the load
-__device__ __forceinline__ void arrive_after(uint64_t* b, uint32_t loaded) {
-    asm volatile(
-        "{\n\t.reg .b32 t;\n\t"
-        "shr.u32 t, %1, 31;\n\t"
-        "add.u32 t, t, %0;\n\t"
-        "mbarrier.arrive.shared::cta.b64 _, [t];\n\t}" ::"r"(su32(b)), "r"(loaded) : "memory");
-}
-
-struct Where {
-    int b, h, g, p0, len, nch;     // p0: first column of the CTA
-};
-
-template <int PC>
-__device__ __forceinline__ Where where_am_i(const DeltaParams& q) {
-    Where w;
-    const int slices = q.headdim / PC;
-    const int bh = blockIdx.x / slices;
-    w.p0 = (blockIdx.x % slices) * PC;
-    w.b = bh / q.nheads;
-    w.h = bh % q.nheads;
-    w.g = w.h / (q.nheads / q.ngroups);
-    int len = q.seqlen;
-    if (q.lengths && M3_IN(3, w.b, q.batch)) len = min(max(q.lengths[w.b], 0), q.seqlen);
-    w.len = len;
-    w.nch = (len + kC - 1) / kC;
-    return w;
-}
-
-// NP loads of W consecutive columns (32 lanes, thread = lane), `step` columns
-// apart, issued back to back with one wait; their sum
-template <int W, int NP> __device__ __forceinline__ void tmem_sum(uint32_t t, uint32_t step, float2* f);
-template <> __device__ __forceinline__ void tmem_sum<8, 1>(uint32_t t, uint32_t step, float2* f) {
-    uint32_t r[8];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-        : "r"(t + 0)
-        : "memory");
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        f[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-    }
-}
-template <> __device__ __forceinline__ void tmem_sum<8, 2>(uint32_t t, uint32_t step, float2* f) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(t + 0), "r"(t + 1 * step)
-        : "memory");
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        f[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-        f[j] = __fadd2_rn(f[j], make_float2(__uint_as_float(r[8 + 2 * j]), __uint_as_float(r[9 + 2 * j])));
-    }
-}
-template <> __device__ __forceinline__ void tmem_sum<8, 3>(uint32_t t, uint32_t step, float2* f) {
-    uint32_t r[24];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%24];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%25];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%26];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23])
-        : "r"(t + 0), "r"(t + 1 * step), "r"(t + 2 * step)
-        : "memory");
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        f[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-        f[j] = __fadd2_rn(f[j], __fadd2_rn(make_float2(__uint_as_float(r[8 + 2 * j]), __uint_as_float(r[9 + 2 * j])),
-                                           make_float2(__uint_as_float(r[16 + 2 * j]), __uint_as_float(r[17 + 2 * j]))));
-    }
-}
-template <> __device__ __forceinline__ void tmem_sum<16, 1>(uint32_t t, uint32_t step, float2* f) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(t + 0)
-        : "memory");
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        f[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-    }
-}
-template <> __device__ __forceinline__ void tmem_sum<16, 2>(uint32_t t, uint32_t step, float2* f) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(t + 0), "r"(t + 1 * step)
-        : "memory");
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        f[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-        f[j] = __fadd2_rn(f[j], make_float2(__uint_as_float(r[16 + 2 * j]), __uint_as_float(r[17 + 2 * j])));
-    }
-}
-template <> __device__ __forceinline__ void tmem_sum<16, 3>(uint32_t t, uint32_t step, float2* f) {
-    uint32_t r[48];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%48];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%49];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%50];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47])
-        : "r"(t + 0), "r"(t + 1 * step), "r"(t + 2 * step)
-        : "memory");
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        f[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-        f[j] = __fadd2_rn(f[j], __fadd2_rn(make_float2(__uint_as_float(r[16 + 2 * j]), __uint_as_float(r[17 + 2 * j])),
-                                           make_float2(__uint_as_float(r[32 + 2 * j]), __uint_as_float(r[33 + 2 * j]))));
-    }
-}
-
-// Split operands.  A row of a tile has 128 bytes, 64 bfloat16 columns; the parts
-// of an operand stand side by side, PC columns each, and go on in further tiles
-// (16 KB for 128 rows, 8 KB for 64).  Byte offset of part `part`, 16-byte
-// column group `ch` (PC / 8 a part) of row `row`:
-template <int PC>
-__device__ __forceinline__ uint32_t part_at(int row, int part, int ch, int tile_bytes) {
-    const int col = part * (PC / 8) + ch;
-    return (uint32_t)((col >> 3) * tile_bytes) + sw128(row, col & 7);
-}
-
 // DUMP: also write the records that the gradient's passes read
 template <int PC, bool DUMP>
 __global__ void __launch_bounds__(kThreads<PC>, 1)

@@ -29,6 +29,7 @@ cudaError_t bounds_take_delta(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_delta_tc(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_delta_bwd_tc(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_delta_prep(BoundsRecord* out, bool clear);
+cudaError_t bounds_take_delta_rev(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_norm(BoundsRecord* out, bool clear);
 cudaError_t bounds_take_api(BoundsRecord* out, bool clear);
 
@@ -855,7 +856,7 @@ m3_status m3_debug_bounds_report(m3_bounds_report* out, int clear) {
     const Take takes[] = {bounds_take_scan_tc, bounds_take_scan_simt, bounds_take_step,
                           bounds_take_rope,    bounds_take_seq,       bounds_take_bwd,
                           bounds_take_phase,   bounds_take_scan_ws,   bounds_take_delta,
-                          bounds_take_delta_tc, bounds_take_delta_bwd_tc, bounds_take_delta_prep,
+                          bounds_take_delta_tc, bounds_take_delta_bwd_tc, bounds_take_delta_prep, bounds_take_delta_rev,
                           bounds_take_norm,    bounds_take_api};
     out->enabled = 1;
     if (cudaDeviceSynchronize() != cudaSuccess) return M3_ERR_CUDA;

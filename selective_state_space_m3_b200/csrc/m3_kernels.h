@@ -170,6 +170,7 @@ cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, bool grad, i
 // bytes of a record, one a chunk of 64 tokens of a (batch, head)
 size_t delta_record_bytes(const m3_dims& d, bool grad);
 // chunked gradient (same shapes)
+cudaError_t launch_delta_rev(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st);
 cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st);
 cudaError_t launch_delta_reduce(const m3_dims& d, const DeltaParams& q, int tiles, cudaStream_t st);
 cudaError_t launch_delta_step(const m3_dims& d, const DeltaParams& q, cudaStream_t st);
