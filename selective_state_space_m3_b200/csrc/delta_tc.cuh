@@ -281,12 +281,16 @@ __device__ __forceinline__ uint32_t part_at(int row, int part, int ch, int tile_
 //   gates  1024 bytes (ChainGates)
 // for the gradient also
 //   PL     [64][64]: what the rounding left of P
-//   then for every 64 columns of the head, plain rows, each as hi and lo part:
-//   S before the chunk and its gradient behind the chunk [2][128][64] each, U and dR [2][64][64] each
+//   then for every 64 columns of the head, each as hi and lo part, groups of 8
+//   columns one behind the other (so that a warp with a row a lane writes 512
+//   bytes in a piece):
+//   S before the chunk and its gradient behind the chunk [2][8][128][8] each, U and dR [2][8][64][8] each
 constexpr size_t kTok = 64 * 64, kSt = 128 * 64;
 constexpr size_t kRecX = 0, kRecTL = 2 * kTok, kRecGates = 3 * kTok, kRecPL = kRecGates + 512, kRecSlice = kRecPL + kTok;
 constexpr size_t kSliceS = 0, kSliceDS = 2 * kSt, kSliceU = 4 * kSt, kSliceDR = 4 * kSt + 2 * kTok;
 constexpr size_t kSliceElems = 4 * kSt + 4 * kTok;
+// element of row `row`, column `col` of a part with `rows` rows
+__host__ __device__ constexpr size_t rec_at(int rows, int row, int col) { return ((size_t)(col >> 3) * rows + row) * 8 + (col & 7); }
 __host__ __device__ constexpr size_t rec_elems(int P, bool grad) {
     return grad ? kRecSlice + (size_t)(P / 64) * kSliceElems : kRecPL;
 }

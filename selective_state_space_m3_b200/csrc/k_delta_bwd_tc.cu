@@ -138,12 +138,13 @@ __device__ __forceinline__ void load_tokens(uint32_t dst, int atom, const void* 
         cp16(at(dst, atom, r, g), static_cast<const __nv_bfloat16*>(src) + (ok ? o : 0), ok);
     }
 }
-// `rows` rows of 64 recorded columns
-template <int NT>
-__device__ __forceinline__ void load_rec(const DeltaParams& q, uint32_t dst, size_t o, int rows) {
-    for (int e = threadIdx.x; e < rows * 8; e += NT) {
-        const bool ok = M3_SPAN(3, o + e * 8, 8, ext_rec(q));
-        cp16(at(dst, 0, e >> 3, e & 7), q.rec + (ok ? o + e * 8 : 0), ok);
+// hi and lo part of a recorded matrix with R rows, lo R * 128 bytes behind hi
+template <int NT, int R>
+__device__ __forceinline__ void load_rec(const DeltaParams& q, uint32_t dst, size_t o) {
+    for (int e = threadIdx.x; e < 2 * R * 8; e += NT) {
+        const int part = e / (R * 8), f = e % (R * 8);
+        const bool ok = M3_SPAN(3, o + (size_t)e * 8, 8, ext_rec(q));
+        cp16(at(dst + part * R * 128, 0, f % R, f / R), q.rec + (ok ? o + (size_t)e * 8 : 0), ok);
     }
 }
 
@@ -214,13 +215,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaParams
         if (sl > 0) __syncthreads();
         const size_t o = rec0 + kRecSlice + sl * kSliceElems;
         load_tokens<NT>(sb + GR_DY, 0, q.dy, row0, (size_t)H * P, (size_t)h * P + 64 * sl, 8, nt, ext_v);
-        load_rec<NT>(q, sb + GR_U, o + kSliceU, 128);
-        load_rec<NT>(q, sb + GR_DR, o + kSliceDR, 128);
+        load_rec<NT, 64>(q, sb + GR_U, o + kSliceU);
+        load_rec<NT, 64>(q, sb + GR_DR, o + kSliceDR);
         cp_commit();
-        load_rec<NT>(q, sb + GR_S, o + kSliceS, 256);
+        load_rec<NT, 128>(q, sb + GR_S, o + kSliceS);
         load_tokens<NT>(sb + GR_V, 0, q.v, row0, (size_t)H * P, (size_t)h * P + 64 * sl, 8, nt, ext_v);
         cp_commit();
-        load_rec<NT>(q, sb + GR_DS, o + kSliceDS, 256);
+        load_rec<NT, 128>(q, sb + GR_DS, o + kSliceDS);
         if (sl == 0) {
             load_tokens<NT>(sb + GR_K, 8192, q.k, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
             load_tokens<NT>(sb + GR_Q, 8192, q.q, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);

@@ -183,9 +183,10 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
             dS[2 * j] = make_float2(v.x, v.y);
             dS[2 * j + 1] = make_float2(v.z, v.w);
         }
-        // this thread's 8 columns of row r of a recorded matrix of chunk c
-        auto keep = [&](int c, size_t at, int r, uint4 v) {
-            const size_t o = (bh * q.nck + c) * rec + kRecSlice + (size_t)(w.p0 >> 6) * kSliceElems + at + r * 64 + (w.p0 & 63) + c0;
+        // this thread's 8 columns of row r of a recorded part of chunk c with `rows` rows
+        auto keep = [&](int c, size_t at, int rows, int r, uint4 v) {
+            const size_t o = (bh * q.nck + c) * rec + kRecSlice + (size_t)(w.p0 >> 6) * kSliceElems + at +
+                             rec_at(rows, r, (w.p0 & 63) + c0);
             if (M3_SPAN(3, o, 8, ext_rec)) *reinterpret_cast<uint4*>(q.rec + o) = v;
         };
         // dS into shared memory and, as the gradient of the state behind chunk c, into the record
@@ -197,8 +198,8 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(&m->s_ready);
-            keep(c, kSliceDS, row, hi);
-            keep(c, kSliceDS + kSt, row, lo);
+            keep(c, kSliceDS, 128, row, hi);
+            keep(c, kSliceDS + kSt, 128, row, lo);
         };
         // dY of iteration i: as it is and scaled by scale e^G; rows behind the end
         // (other data, possibly not numbers) count as zero
@@ -282,8 +283,8 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
                 for (int j = 0; j < 4; ++j) f[j] = __fmul2_rn(be2, d[j]);
                 const size_t vo = (((size_t)w.b * q.seqlen + c * kC + tok) * H + w.h) * P + w.p0 + c0;
                 if (in && M3_SPAN(5, vo, 8, ext_v)) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(q.dv) + vo) = round8(f);
-                keep(c, kSliceDR, tok, take8(d));
-                keep(c, kSliceDR + kTok, tok, round8(d));
+                keep(c, kSliceDR, 64, tok, take8(d));
+                keep(c, kSliceDR + kTok, 64, tok, round8(d));
             } else {
                 arrive_after(&m->u, __float_as_uint(whole));       // (the stage is free once everybody has its gates)
                 if (i + 1 < nch) {

@@ -182,29 +182,33 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
             S[2 * c4] = make_float2(v.x, v.y);
             S[2 * c4 + 1] = make_float2(v.z, v.w);
         }
-        // this CTA's columns in a record, and this thread's first one
-        auto slice_of = [&](int c) {
-            return q.rec + (bh * q.nck + c) * rec_elems(P, true) + kRecSlice + (size_t)(w.p0 >> 6) * kSliceElems + (w.p0 & 63) + c0;
-        };
-        auto keep = [&](__nv_bfloat16* dst, int ch, uint4 v) {
-            if (M3_SPAN(10, dst + 8 * ch - q.rec, 8, (long long)q.batch * q.nheads * q.nck * rec_elems(P, true)))
-                *reinterpret_cast<uint4*>(dst + 8 * ch) = v;
+        // 8 columns (group ch of this thread's) of row r of a recorded part with `rows` rows
+        auto keep = [&](int c, size_t at, int rows, int r, int ch, uint4 v) {
+            const size_t o = (bh * q.nck + c) * rec_elems(P, true) + kRecSlice + (size_t)(w.p0 >> 6) * kSliceElems + at +
+                             rec_at(rows, r, (w.p0 & 63) + c0 + 8 * ch);
+            if (M3_SPAN(10, o, 8, (long long)q.batch * q.nheads * q.nck * rec_elems(P, true)))
+                *reinterpret_cast<uint4*>(q.rec + o) = v;
         };
         auto store_state = [&](int c) {            // S hi, S lo before chunk c
+            uint4 hi[NG], lo[NG];
 #pragma unroll
             for (int ch = 0; ch < NG; ++ch) {
                 float2 f[4] = {S[4 * ch], S[4 * ch + 1], S[4 * ch + 2], S[4 * ch + 3]};
-                const uint4 hi = take8(f), lo = round8(f);
-                put16(smem, OFF_S, part_at<PC>(row, 0, ch0 + ch, 16384), 32768, hi);
-                put16(smem, OFF_S, part_at<PC>(row, 1, ch0 + ch, 16384), 32768, lo);
-                if (DUMP) {
-                    keep(slice_of(c) + kSliceS + row * 64, ch, hi);
-                    keep(slice_of(c) + kSliceS + kSt + row * 64, ch, lo);
-                }
+                hi[ch] = take8(f);
+                lo[ch] = round8(f);
+                put16(smem, OFF_S, part_at<PC>(row, 0, ch0 + ch, 16384), 32768, hi[ch]);
+                put16(smem, OFF_S, part_at<PC>(row, 1, ch0 + ch, 16384), 32768, lo[ch]);
             }
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(&m->s_ready);
+            if (DUMP) {
+#pragma unroll
+                for (int ch = 0; ch < NG; ++ch) {
+                    keep(c, kSliceS, 128, row, ch, hi[ch]);
+                    keep(c, kSliceS + kSt, 128, row, ch, lo[ch]);
+                }
+            }
         };
         // beta V of chunk c; rows behind the end (other data, possibly not numbers) count as zero
         float2 buf[kCols / 2];                     // top: beta V, R, then U; else Q S
@@ -277,9 +281,8 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
                         const int cc = ch0 + W / 8 * hh + ch;
                         put16(smem, OFF_V + (c & 1) * 8192, sw128(tok, cc), 8192, round8(f + 4 * ch));
                         if (DUMP) {
-                            float2 e[4] = {f[4 * ch], f[4 * ch + 1], f[4 * ch + 2], f[4 * ch + 3]};
-                            keep(slice_of(c) + kSliceU + tok * 64, W / 8 * hh + ch, take8(e));
-                            keep(slice_of(c) + kSliceU + kTok + tok * 64, W / 8 * hh + ch, round8(e));
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) buf[W / 2 * hh + 4 * ch + j] = f[4 * ch + j];
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) f[4 * ch + j] = __fmul2_rn(at2, f[4 * ch + j]);
@@ -291,6 +294,13 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
                 fence_async_smem();
                 tc_fence_before();
                 arrive_after(&m->u, __float_as_uint(whole));
+                if (DUMP) {
+#pragma unroll
+                    for (int ch = 0; ch < NG; ++ch) {
+                        keep(c, kSliceU, 64, tok, ch, take8(buf + 4 * ch));
+                        keep(c, kSliceU + kTok, 64, tok, ch, round8(buf + 4 * ch));
+                    }
+                }
                 if (c + 1 < w.nch) load_v(c + 1);  // while the state's update is made
             } else {
                 tc_fence_before();
