@@ -16,17 +16,27 @@
 // Three passes.  The prefill runs once more and records T, P, the state before
 // every chunk and U.  k_delta_rev.cu carries dS from the last chunk to the first
 // and records dS' and dR.  delta_grad_kernel here then takes all chunks at once,
-// one CTA each.  dq and dk of a group's heads
-// are added by a further kernel in a fixed order.
+// one CTA each.  dq and dk of a group's heads are added by a further kernel in a
+// fixed order.
 //
-// The chain and all that feeds sums keep float32 values as two bfloat16 parts
-// (hi + lo); a product with two split operands drops lo x lo (2^-17 of the
-// product).  Products are 16 x 8 x 16 warp-level mma with register
-// accumulators: the matrices of a chunk (64 x 64 to 64 x 128) are masked,
-// scaled and split between one product and the next, and register fragments
-// take these steps without a way through tensor memory.
+// Products (tcgen05, M = 128 rows, accumulators in TMEM; rows 0..63 and 64..127
+// of the left operand are two matrices, so that a thread finds all that belongs
+// to a token in its row):
+//   [Q; K] K^T,  [dY; dR] U^T,  [dY; dR] S^T,  [.; U] dS'^T
+//   [scale Gam o dP; D + D^T] K,  [.; (scale Gam o dP)^T] Q
+// D + D^T is one symmetric matrix, since D is strictly lower.  All that feeds
+// dg and dbeta (sums with cancellation) keeps float32 values as two bfloat16
+// parts (hi + lo; a product of two split operands drops lo x lo); the last two
+// products take rounded left operands, for they end in dq and dk, which are
+// rounded too.  The records are stored in the layout that the products read
+// (8 columns a piece), so no matrix is rearranged.
 //
-// Times on one B200 stand with the launcher.
+// Bound by the records' traffic (about 200 KB a chunk in and out of L2 and HBM);
+// loads arrive in three groups, in the order of their use.
+//
+// Every wait on an mbarrier is bounded (1 s); on expiry the kernel records
+// M3_ERR_DEVICE_TIMEOUT in the workspace status word and runs out without
+// further waiting.
 #define M3_BOUNDS_FILE 13
 #include "m3_bounds.cuh"
 #include "delta_tc.cuh"
@@ -36,151 +46,86 @@ namespace dbw {
 
 using namespace dtc;
 
+constexpr int kThreads = 512;        // 4 row quarters x 4 column groups of warps
 
-// a matrix in shared memory: rows of 128 bytes (64 columns), 16-byte groups
-// exchanged by row (sw128); columns 64.. go on `atom` bytes further
-__device__ __forceinline__ uint32_t at(uint32_t base, int atom, int row, int col8) {
-    return base + (col8 >> 3) * atom + row * 128 + (((col8 & 7) ^ (row & 7)) << 4);
-}
-__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
+constexpr int OFF_QK = 0;                        // Q rows 0..63, K rows 64..127 (two 64-column atoms, sw128)
+constexpr int OFF_A2 = 32768;                    // [0; dR lo] (16 KB; pieces of 8 columns, 128 rows each)
+constexpr int OFF_U = OFF_A2 + 16384;            // U hi, lo (8 KB each; pieces of 64 rows)
+constexpr int OFF_A = OFF_U + 16384;             // [dY; dR hi] (16 KB)
+constexpr int OFF_S = OFF_A + 16384;             // S hi, lo (16 KB each; pieces of 128 rows)
+constexpr int OFF_DS = OFF_S + 32768;            // dS' hi, lo
+constexpr int OFF_D = OFF_DS + 32768;            // [scale Gam o dP; D + D^T] (16 KB, sw128)
+constexpr int OFF_MISC = OFF_D + 16384;
+// TMEM columns; the last product takes the place of the first two
+constexpr uint32_t D_PA = 0, D_QK = 64, D_ZX = 128, D_Y = 256, D_LAST = 384, D_T = 0;
 
-struct Mat {
-    uint32_t base;
-    int atom;
+struct Misc {
+    Gates gates;
+    float row[4][2 * kC], beta[4][kC], tail[4][kC];    // by column group (row: upper and lower rows' parts)
+    float col[4][kC];                                  // by row quarter (its 16 columns a group)
+    float drv[4][kC], dot[16];
+    uint64_t done[4];
+    uint32_t tmem_base;
+    int abort_flag, drain_flag, pad;
 };
-
-// acc (16 rows from m0, 8 NT columns from n0) += A (B + B2), K steps of 16.
-// AT: A is stored transposed ([k][m]); BT: B is stored as [n][k], else [k][n].
-// B2 (same layout) is left out where its base is 0; n2 is its first column.
-template <int NT, int K, bool AT, bool BT, bool TWO>
-__device__ __forceinline__ void mm(float (*acc)[4], Mat A, int m0, Mat B, int n0, uint32_t base2, int n2) {
-    const int lane = threadIdx.x & 31, mi = lane >> 3, l7 = lane & 7;
-#pragma unroll 2
-    for (int k0 = 0; k0 < K; k0 += 16) {
-        uint32_t a[4];
-        if (AT) ldsm4t(a, at(A.base, A.atom, k0 + (mi >> 1) * 8 + l7, (m0 >> 3) + (mi & 1)));
-        else ldsm4(a, at(A.base, A.atom, m0 + (mi & 1) * 8 + l7, (k0 >> 3) + (mi >> 1)));
-#pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-            uint32_t b[4];
-            if (BT) ldsm4(b, at(B.base, B.atom, n0 + 8 * n + (mi >> 1) * 8 + l7, (k0 >> 3) + (mi & 1)));
-            else ldsm4t(b, at(B.base, B.atom, k0 + (mi & 1) * 8 + l7, (n0 >> 3) + n + (mi >> 1)));
-            mma16816(acc[n], a, b[0], b[1]);
-            mma16816(acc[n + 1], a, b[2], b[3]);
-            if (TWO) {
-                if (BT) ldsm4(b, at(base2, B.atom, n2 + 8 * n + (mi >> 1) * 8 + l7, (k0 >> 3) + (mi & 1)));
-                else ldsm4t(b, at(base2, B.atom, k0 + (mi & 1) * 8 + l7, (n2 >> 3) + n + (mi >> 1)));
-                mma16816(acc[n], a, b[0], b[1]);
-                mma16816(acc[n + 1], a, b[2], b[3]);
-            }
-        }
-    }
-}
-
-template <int NT> __device__ __forceinline__ void zero(float (*acc)[4]) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-}
+constexpr int SMEM_BYTES = OFF_MISC + (int)sizeof(Misc) + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory of the chunk gradients");
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
     const int n = ok ? 16 : 0;               // 0: the destination gets zeros, the source is not read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
+// matrix descriptor without exchange of 16-byte groups: 8 rows x 16 bytes lie
+// together, `lbo` bytes to the next 8 columns, `sbo` to the next 8 rows
+__device__ __forceinline__ uint64_t sdesc0(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46);
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
+
 __device__ __forceinline__ float2 unpack(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
-__device__ __forceinline__ uint32_t elem(uint32_t base, int row, int col) { return at(base, 0, row, col >> 3) + (col & 7) * 2; }
-
-__device__ __forceinline__ int length_of(const DeltaParams& q, int b) {
-    if (!q.lengths) return q.seqlen;
-    return M3_IN(1, b, q.batch) ? min(max(q.lengths[b], 0), q.seqlen) : 0;
-}
-__device__ __forceinline__ long long ext_rec(const DeltaParams& q) {
-    return (long long)q.batch * q.nheads * q.nck * (long long)rec_elems(q.headdim, true);
-}
-
-// 64 token rows (chunk c) of q, k or one 64-column tile of v, dy into shared
-// memory: `groups` 16-byte groups a row; rows behind the end are zeros
-template <int NT>
-__device__ __forceinline__ void load_tokens(uint32_t dst, int atom, const void* src, size_t row0, size_t pitch, size_t col,
-                                            int groups, int nt, long long ext) {
-    for (int e = threadIdx.x; e < 64 * groups; e += NT) {
-        const int r = e / groups, g = e - r * groups;
-        const size_t o = (row0 + r) * pitch + col + 8 * g;
-        const bool ok = r < nt && M3_SPAN(2, o, 8, ext);
-        cp16(at(dst, atom, r, g), static_cast<const __nv_bfloat16*>(src) + (ok ? o : 0), ok);
-    }
-}
-// hi and lo part of a recorded matrix with R rows, lo R * 128 bytes behind hi
-template <int NT, int R>
-__device__ __forceinline__ void load_rec(const DeltaParams& q, uint32_t dst, size_t o) {
-    for (int e = threadIdx.x; e < 2 * R * 8; e += NT) {
-        const int part = e / (R * 8), f = e % (R * 8);
-        const bool ok = M3_SPAN(3, o + (size_t)e * 8, 8, ext_rec(q));
-        cp16(at(dst + part * R * 128, 0, f % R, f / R), q.rec + (ok ? o + (size_t)e * 8 : 0), ok);
+__device__ __forceinline__ void unpack8(uint4 v, float* f) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 t = unpack(u[j]);
+        f[2 * j] = t.x;
+        f[2 * j + 1] = t.y;
     }
 }
 
-// ------------------------------------------------ the gradients of a chunk --
-// 16 warps: warp w has 16 rows (w & 3) and a quarter of the columns (w >> 2).
-// Loads arrive in three groups, in the order of their use, so that the products
-// begin with the first.
-constexpr int kGradThreads = 512;
-constexpr uint32_t GR_K = 0, GR_Q = 16384, GR_DY = 32768, GR_V = 40960, GR_U = 49152, GR_DR = 65536, GR_S = 81920,
-                   GR_DS = 114688, GR_GATES = 147456;
-// where V, U and dR were, after the last slice: P's and A's gradients, rounded
-// (they meet K and Q only in products that end in dq and dk, which are rounded
-// too); the gradient of A with its transposed, one symmetric matrix
-constexpr uint32_t GR_DQK = GR_U, GR_DKK = GR_U + 8192;
-struct GradSums {
-    float row[4][kC], beta[4][kC], tail[4][kC];      // by column quarter
-    float col[4][kC];                                // by row tile
-    float drv[kC], dot[16];
-};
-constexpr int GR_BYTES = GR_GATES + sizeof(Gates) + sizeof(GradSums) + 128;
+// sums over a warp's 32 rows of 16 columns, one row a lane: lane l gets column l & 15
+__device__ __forceinline__ float column_sums(float* v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] += __shfl_xor_sync(kFull, v[k], 16);
+#pragma unroll
+    for (int s = 8; s; s >>= 1)
+#pragma unroll
+        for (int k = 0; k < s; ++k) {
+            const bool up = lane & s;
+            const float give = up ? v[k] : v[k + s], own = up ? v[k + s] : v[k];
+            v[k] = own + __shfl_xor_sync(kFull, give, s);
+        }
+    return v[0];
+}
 
-__global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaParams q, int nchunks) {
-    extern __shared__ __align__(128) uint8_t smem_raw[];
-    const uint32_t sb = (su32(smem_raw) + 127u) & ~127u;
-    uint8_t* smem = smem_raw + (sb - su32(smem_raw));
-    Gates* gt = reinterpret_cast<Gates*>(smem + GR_GATES);
-    GradSums* gs = reinterpret_cast<GradSums*>(smem + GR_GATES + sizeof(Gates));
-    if (!M3_SPAN(11, sb - su32(smem_raw), GR_GATES + sizeof(Gates) + sizeof(GradSums), dyn_smem_bytes())) return;
-    constexpr int NT = kGradThreads;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, P = q.headdim, H = q.nheads;
+__global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, int nchunks, int* status) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (su32(smem_raw) & 1023u)) & 1023u);
+    Misc* m = reinterpret_cast<Misc*>(smem + OFF_MISC);
+    const uint32_t sb = su32(smem);
+    if (!M3_SPAN(1, smem - smem_raw, OFF_MISC + (int)sizeof(Misc), dyn_smem_bytes())) return;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31, P = q.headdim, H = q.nheads;
     const int bh = blockIdx.x / nchunks, c = blockIdx.x % nchunks;
     const int b = bh / H, h = bh % H, hpg = H / q.ngroups, g = h / hpg;
-    const int len = length_of(q, b), nt = min(kC, len - c * kC);
-    const int mt = warp & 3, nq = warp >> 2, qr = lane >> 2, qc = (lane & 3) * 2;
-    const long long ext_k = (long long)q.batch * q.seqlen * q.ngroups * kN, ext_v = (long long)q.batch * q.seqlen * H * P;
+    int len = q.seqlen;
+    if (q.lengths && M3_IN(2, b, q.batch)) len = min(max(q.lengths[b], 0), q.seqlen);
+    const int nt = min(kC, len - c * kC);
+    [[maybe_unused]] const long long ext_k = (long long)q.batch * q.seqlen * q.ngroups * kN, ext_v = (long long)q.batch * q.seqlen * H * P;
     [[maybe_unused]] const long long toks = (long long)q.batch * q.seqlen * H;
+    [[maybe_unused]] const long long ext_rec = (long long)q.batch * H * q.nck * (long long)rec_elems(P, true);
     const size_t row0 = (size_t)b * q.seqlen + c * kC;
     const int rows = min(kC, q.seqlen - c * kC);               // rows of the outputs in this chunk
     __nv_bfloat16* out_q = static_cast<__nv_bfloat16*>(q.dq);
@@ -189,231 +134,347 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaParams
     __nv_bfloat16* out_b = static_cast<__nv_bfloat16*>(q.dbeta);
     if (nt <= 0) {                                             // behind the end (a group's heads: the sum kernel's zeros)
         if (hpg == 1) {
-            for (int e = tid; e < rows * 16; e += NT) {
+            for (int e = tid; e < rows * 16; e += kThreads) {
                 const size_t o = ((row0 + (e >> 4)) * q.ngroups + g) * kN + 8 * (e & 15);
-                if (M3_SPAN(12, o, 8, ext_k)) {
+                if (M3_SPAN(3, o, 8, ext_k)) {
                     *reinterpret_cast<uint4*>(out_q + o) = make_uint4(0u, 0u, 0u, 0u);
                     *reinterpret_cast<uint4*>(out_k + o) = make_uint4(0u, 0u, 0u, 0u);
                 }
             }
-            if (tid < rows && M3_IN(13, (row0 + tid) * H + h, toks)) {
+            if (tid < rows && M3_IN(4, (row0 + tid) * H + h, toks)) {
                 if (out_g) out_g[(row0 + tid) * H + h] = __float2bfloat16_rn(0.f);
                 out_b[(row0 + tid) * H + h] = __float2bfloat16_rn(0.f);
             }
         }
         return;
     }
-    const size_t rec0 = ((size_t)bh * q.nck + c) * rec_elems(P, true);
-    const Mat K = {sb + GR_K, 8192}, Q = {sb + GR_Q, 8192}, dY = {sb + GR_DY, 0};
-    const Mat Uh = {sb + GR_U, 0}, Ul = {sb + GR_U + 8192, 0}, dRh = {sb + GR_DR, 0}, dRl = {sb + GR_DR + 8192, 0};
-    const Mat Sh = {sb + GR_S, 0}, Dh = {sb + GR_DS, 0};
-
-    float kk[2][4], dP[2][4], dA[2][4], Z[4][4], X[4][4], Y[4][4];
-    zero<2>(kk); zero<2>(dP); zero<2>(dA); zero<4>(Z); zero<4>(X); zero<4>(Y);
-    float dot = 0.f, drv = 0.f;                                // <S, dS'>, dR . v of row tid / 8
-    for (int sl = 0; sl < P / 64; ++sl) {
-        if (sl > 0) __syncthreads();
-        const size_t o = rec0 + kRecSlice + sl * kSliceElems;
-        load_tokens<NT>(sb + GR_DY, 0, q.dy, row0, (size_t)H * P, (size_t)h * P + 64 * sl, 8, nt, ext_v);
-        load_rec<NT, 64>(q, sb + GR_U, o + kSliceU);
-        load_rec<NT, 64>(q, sb + GR_DR, o + kSliceDR);
-        cp_commit();
-        load_rec<NT, 128>(q, sb + GR_S, o + kSliceS);
-        load_tokens<NT>(sb + GR_V, 0, q.v, row0, (size_t)H * P, (size_t)h * P + 64 * sl, 8, nt, ext_v);
-        cp_commit();
-        load_rec<NT, 128>(q, sb + GR_DS, o + kSliceDS);
-        if (sl == 0) {
-            load_tokens<NT>(sb + GR_K, 8192, q.k, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
-            load_tokens<NT>(sb + GR_Q, 8192, q.q, row0, (size_t)q.ngroups * kN, (size_t)g * kN, 16, nt, ext_k);
-        }
-        cp_commit();
-        if (sl == 0 && warp == 0) make_gates(load_raw(q, b, h, len, c), gt);
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-        __syncthreads();
-        mm<2, 64, false, true, true>(dP, dY, 16 * mt, Uh, 16 * nq, Ul.base, 16 * nq);
-        mm<2, 64, false, true, true>(dA, dRh, 16 * mt, Uh, 16 * nq, Ul.base, 16 * nq);
-        mm<2, 64, false, true, false>(dA, dRl, 16 * mt, Uh, 16 * nq, 0, 0);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncthreads();
-        mm<4, 64, false, true, true>(Z, dY, 16 * mt, Sh, 32 * nq, Sh.base + 16384, 32 * nq);
-        mm<4, 64, false, true, true>(X, dRh, 16 * mt, Sh, 32 * nq, Sh.base + 16384, 32 * nq);
-        mm<4, 64, false, true, false>(X, dRl, 16 * mt, Sh, 32 * nq, 0, 0);
-        {
-            const uint32_t p = at(0, 0, tid >> 3, tid & 7);
-            const uint4 r0 = lds128(dRh.base + p), r1 = lds128(dRl.base + p), v0 = lds128(sb + GR_V + p);
-            const uint32_t rh[4] = {r0.x, r0.y, r0.z, r0.w}, rl[4] = {r1.x, r1.y, r1.z, r1.w}, vv[4] = {v0.x, v0.y, v0.z, v0.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 d = __fadd2_rn(unpack(rh[j]), unpack(rl[j])), v = unpack(vv[j]);
-                drv = fmaf(d.x, v.x, fmaf(d.y, v.y, drv));
-            }
-        }
-        cp_wait();
-        __syncthreads();
-        mm<4, 64, false, true, true>(Y, Uh, 16 * mt, Dh, 32 * nq, Dh.base + 16384, 32 * nq);
-        mm<4, 64, false, true, false>(Y, Ul, 16 * mt, Dh, 32 * nq, 0, 0);
-#pragma unroll
-        for (int e = tid; e < 128 * 8; e += NT) {
-            const uint32_t p = at(0, 0, e >> 3, e & 7);
-            const uint4 s0 = lds128(sb + GR_S + p), s1 = lds128(sb + GR_S + 16384 + p);
-            const uint4 d0 = lds128(sb + GR_DS + p), d1 = lds128(sb + GR_DS + 16384 + p);
-            const uint32_t sh[4] = {s0.x, s0.y, s0.z, s0.w}, s2[4] = {s1.x, s1.y, s1.z, s1.w};
-            const uint32_t dh[4] = {d0.x, d0.y, d0.z, d0.w}, d2[4] = {d1.x, d1.y, d1.z, d1.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 a = __fadd2_rn(unpack(sh[j]), unpack(s2[j])), d = __fadd2_rn(unpack(dh[j]), unpack(d2[j]));
-                dot = fmaf(a.x, d.x, fmaf(a.y, d.y, dot));
-            }
-        }
-    }
-    mm<2, 128, false, true, false>(kk, K, 16 * mt, K, 16 * nq, 0, 0);
-    __syncthreads();                                           // U and dR have been read: their place takes dP and D
-    drv += __shfl_xor_sync(kFull, drv, 1);
-    drv += __shfl_xor_sync(kFull, drv, 2);
-    drv += __shfl_xor_sync(kFull, drv, 4);
-    if ((tid & 7) == 0) gs->drv[tid >> 3] = drv;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-    if (lane == 0) gs->dot[warp] = dot;
-
-    float rowG[2] = {0.f, 0.f}, rowB[2] = {0.f, 0.f}, tail[2] = {0.f, 0.f};
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const int j = 16 * nq + 8 * n + qc;
-        float cs[2] = {0.f, 0.f};
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int i = 16 * mt + qr + 8 * r;
-            const float2 Gi = gt->G[i];
-            const float be = gt->beta[i];
-            float fq[2];
-            const size_t o = rec0 + (sw128(i, j >> 3) >> 1) + (j & 7);
-            float2 pv = make_float2(0.f, 0.f);
-            if (M3_SPAN(14, o + kRecPL, 2, ext_rec(q)))
-                pv = __fadd2_rn(unpack(*reinterpret_cast<const uint32_t*>(q.rec + o + kRecX + kTok)),
-                                unpack(*reinterpret_cast<const uint32_t*>(q.rec + o + kRecPL)));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float gam = i >= j + e ? ex2(diff_pair(Gi, gt->G[j + e])) : 0.f;
-                const float dp = i >= j + e ? dP[n][2 * r + e] : 0.f;
-                const float da = i > j + e ? -dA[n][2 * r + e] * gam : 0.f;
-                const float t = da * kk[n][2 * r + e];
-                const float E = fmaf(dp, e ? pv.y : pv.x, be * t);
-                rowG[r] += E;
-                cs[e] += E;
-                rowB[r] += t;
-                fq[e] = q.scale * gam * dp;
-                // D at (i, j) and (j, i); the diagonal is zero
-                const __nv_bfloat16 v = __float2bfloat16_rn(be * da);
-                if (i >= j + e && M3_IN(19, i * 64 + j + e, 4096)) {
-                    *reinterpret_cast<__nv_bfloat16*>(smem + elem(GR_DKK, i, j + e)) = v;
-                    *reinterpret_cast<__nv_bfloat16*>(smem + elem(GR_DKK, j + e, i)) = v;
-                }
-            }
-            sts32(elem(sb + GR_DQK, i, j), pack_bf16x2(fq[0], fq[1]));
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) cs[e] += __shfl_xor_sync(kFull, cs[e], o);
-            if (qr == 0) gs->col[mt][j + e] = cs[e];
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int i = 16 * mt + qr + 8 * r;
-        const float a = gt->a[i], tl = gt->at[i], be = gt->beta[i], sa = q.scale * a, ba = be * a;
-        float zq = 0.f, xk = 0.f, yk = 0.f;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int col = 32 * nq + 8 * n + qc;
-            const uint32_t p = at(0, 8192, i, col >> 3) + (col & 7) * 2;
-            const float2 qv = unpack(lds32(sb + GR_Q + p)), kv = unpack(lds32(sb + GR_K + p));
-            zq = fmaf(Z[n][2 * r], qv.x, fmaf(Z[n][2 * r + 1], qv.y, zq));
-            xk = fmaf(X[n][2 * r], kv.x, fmaf(X[n][2 * r + 1], kv.y, xk));
-            yk = fmaf(Y[n][2 * r], kv.x, fmaf(Y[n][2 * r + 1], kv.y, yk));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                Z[n][2 * r + e] *= sa;
-                Y[n][2 * r + e] = fmaf(tl, Y[n][2 * r + e], -ba * X[n][2 * r + e]);
-            }
-        }
-        rowG[r] += sa * zq - ba * xk - tl * yk;
-        rowB[r] -= a * xk;
-        tail[r] = tl * yk;
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            rowG[r] += __shfl_xor_sync(kFull, rowG[r], o);
-            rowB[r] += __shfl_xor_sync(kFull, rowB[r], o);
-            tail[r] += __shfl_xor_sync(kFull, tail[r], o);
-        }
-        if ((lane & 3) == 0) {
-            gs->row[nq][i] = rowG[r];
-            gs->beta[nq][i] = rowB[r];
-            gs->tail[nq][i] = tail[r];
-        }
-    }
-    __syncthreads();
-    const Mat Pq = {sb + GR_DQK, 0}, Dk = {sb + GR_DKK, 0};
-    mm<4, 64, false, false, false>(Z, Pq, 16 * mt, K, 32 * nq, 0, 0);
-    mm<4, 64, true, false, false>(Y, Pq, 16 * mt, Q, 32 * nq, 0, 0);
-    mm<4, 64, false, false, false>(Y, Dk, 16 * mt, K, 32 * nq, 0, 0);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int i = 16 * mt + qr + 8 * r;
-        const float m = i < nt ? 1.f : 0.f;
-        if (i >= rows) continue;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int col = 32 * nq + 8 * n + qc;
-            const float2 vq = make_float2(m * Z[n][2 * r], m * Z[n][2 * r + 1]), vk = make_float2(m * Y[n][2 * r], m * Y[n][2 * r + 1]);
-            if (hpg == 1) {
-                const size_t o = ((row0 + i) * q.ngroups + g) * kN + col;
-                if (M3_SPAN(15, o, 2, ext_k)) {
-                    *reinterpret_cast<uint32_t*>(out_q + o) = pack_bf16x2(vq.x, vq.y);
-                    *reinterpret_cast<uint32_t*>(out_k + o) = pack_bf16x2(vk.x, vk.y);
-                }
-            } else {
-                const size_t o = ((row0 + i) * H + h) * 2 * kN + col;
-                if (M3_SPAN(16, o + kN, 2, toks * 2 * kN)) {
-                    *reinterpret_cast<float2*>(q.part_qk + o) = vq;
-                    *reinterpret_cast<float2*>(q.part_qk + o + kN) = vk;
-                }
-            }
-        }
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(&m->done[i], 1);
+        m->abort_flag = 0;
+        m->drain_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
+        tmem_alloc(&m->tmem_base, 512);
+        tmem_relinquish();
+    }
+    const size_t rec0 = ((size_t)bh * q.nck + c) * rec_elems(P, true);
+    // `pieces` recorded pieces of 16 bytes a row, `rows_` rows each, `pitch` bytes apart in shared memory
+    auto load_rec = [&](uint32_t dst, size_t o, int rows_, int pitch) {
+        for (int e = tid; e < rows_ * 8; e += kThreads) {
+            const bool ok = M3_SPAN(5, o + (size_t)e * 8, 8, ext_rec);
+            cp16(dst + (e / rows_) * pitch + (e % rows_) * 16, q.rec + (ok ? o + (size_t)e * 8 : 0), ok);
+        }
+    };
+    auto load_slice = [&](int sl) {
+        const size_t o = rec0 + kRecSlice + sl * kSliceElems;
+        if (sl == 0)                                           // rows behind the end are zeros
+            for (int e = tid; e < 64 * 32; e += kThreads) {
+                const int r = e >> 5, ch = e & 31;             // 16 groups of Q, 16 of K
+                const size_t ko = ((row0 + r) * q.ngroups + g) * kN + 8 * (ch & 15);
+                const bool ok = r < nt && M3_SPAN(6, ko, 8, ext_k);
+                cp16(sb + OFF_QK + ((ch >> 3) & 1) * 16384 + sw128(r + (ch >> 4) * 64, ch & 7),
+                     static_cast<const __nv_bfloat16*>((ch >> 4) ? q.k : q.q) + (ok ? ko : 0), ok);
+            }
+        {
+            const int r = tid >> 3, p = tid & 7;
+            const size_t vo = ((row0 + r) * H + h) * P + 64 * sl + 8 * p;
+            const bool ok = r < nt && M3_SPAN(7, vo, 8, ext_v);
+            cp16(sb + OFF_A + p * 2048 + r * 16, static_cast<const __nv_bfloat16*>(q.dy) + (ok ? vo : 0), ok);
+            cp16(sb + OFF_A2 + p * 2048 + r * 16, q.rec, false);           // zeros
+        }
+        load_rec(sb + OFF_A + 1024, o + kSliceDR, 64, 2048);
+        load_rec(sb + OFF_U, o + kSliceU, 64, 1024);
+        load_rec(sb + OFF_U + 8192, o + kSliceU + kTok, 64, 1024);
+        cp_commit();
+        load_rec(sb + OFF_A2 + 1024, o + kSliceDR + kTok, 64, 2048);
+        load_rec(sb + OFF_S, o + kSliceS, 128, 2048);
+        load_rec(sb + OFF_S + 16384, o + kSliceS + kSt, 128, 2048);
+        cp_commit();
+        load_rec(sb + OFF_DS, o + kSliceDS, 128, 2048);
+        load_rec(sb + OFF_DS + 16384, o + kSliceDS + kSt, 128, 2048);
+        cp_commit();
+    };
+    load_slice(0);
+    if (warp == 4) make_gates(load_raw(q, b, h, len, c), &m->gates);
+
+    // all threads' copies of a group are in place and visible to the products
+    auto arrived = [&]() {
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    };
+    const uint64_t aQK = sdesc(sb + OFF_QK, 16, 1024), bK = sdesc(sb + OFF_QK + 8192, 16, 1024);
+    const uint64_t aA = sdesc0(sb + OFF_A, 2048, 128), aA2 = sdesc0(sb + OFF_A2, 2048, 128);
+    const uint64_t bU = sdesc0(sb + OFF_U, 1024, 128), bUl = sdesc0(sb + OFF_U + 8192, 1024, 128);
+    const uint64_t aU = sdesc0(sb + OFF_U - 1024, 1024, 128), aUl = sdesc0(sb + OFF_U + 8192 - 1024, 1024, 128);   // rows 64..127
+    const uint64_t bS = sdesc0(sb + OFF_S, 2048, 128), bSl = sdesc0(sb + OFF_S + 16384, 2048, 128);
+    const uint64_t bDS = sdesc0(sb + OFF_DS, 2048, 128), bDSl = sdesc0(sb + OFF_DS + 16384, 2048, 128);
+    constexpr uint32_t id64 = idesc_bf16(128, 64, 0, 0), id128 = idesc_bf16(128, 128, 0, 0);
+    const int quarter = warp & 3, cg = warp >> 2, row = quarter * 32 + lane, tok = row & 63;
+    const bool up = quarter < 2;                   // rows 0..63: dq's side; 64..127: dk's
+    uint32_t tmem = 0;
+    float dot = 0.f, drv = 0.f;                    // <S, dS'>; dR . v
+    const int slices = P / 64;
+    for (int sl = 0; sl < slices; ++sl) {
+        if (sl > 0) {
+            mbar_wait_flag(&m->done[3], (sl - 1) & 1, &m->abort_flag, status, 1);
+            __syncthreads();
+            load_slice(sl);
+        }
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        arrived();
+        tmem = m->tmem_base;
+        if (warp == 0) {
+            if (sl == 0)
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    umma_one(tmem + D_QK, aQK + (kk >> 2) * 1024 + (kk & 3) * 2, bK + (kk >> 2) * 1024 + (kk & 3) * 2, id64, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_PA, aA + kk * 256, bU + kk * 128, id64, sl + kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_PA, aA + kk * 256, bUl + kk * 128, id64, 1);
+        }
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        arrived();
+        if (warp == 0) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_PA, aA2 + kk * 256, bU + kk * 128, id64, 1);
+            if (sl == slices - 1) commit_one(&m->done[0]);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_ZX, aA + kk * 256, bS + kk * 256, id128, sl + kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_ZX, aA + kk * 256, bSl + kk * 256, id128, 1);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_ZX, aA2 + kk * 256, bS + kk * 256, id128, 1);
+        }
+        if (!up) {                                 // dR . v: 16 of the slice's columns
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int p = 2 * cg + j;
+                const size_t vo = ((row0 + tok) * H + h) * P + 64 * sl + 8 * p;
+                float v[8], r[8], l[8];
+                unpack8(tok < nt && M3_SPAN(8, vo, 8, ext_v) ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(q.v) + vo))
+                                                             : make_uint4(0u, 0u, 0u, 0u), v);
+                unpack8(*reinterpret_cast<const uint4*>(smem + OFF_A + p * 2048 + row * 16), r);
+                unpack8(*reinterpret_cast<const uint4*>(smem + OFF_A2 + p * 2048 + row * 16), l);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) drv = fmaf(r[e] + l[e], v[e], drv);
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        arrived();
+        if (warp == 0) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_Y, aU + kk * 128, bDS + kk * 256, id128, sl + kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_Y, aU + kk * 128, bDSl + kk * 256, id128, 1);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_Y, aUl + kk * 128, bDS + kk * 256, id128, 1);
+            commit_one(&m->done[3]);
+        }
+#pragma unroll
+        for (int e = tid; e < 1024; e += kThreads) {
+            float s0[8], s1[8], d0[8], d1[8];
+            unpack8(*reinterpret_cast<const uint4*>(smem + OFF_S + e * 16), s0);
+            unpack8(*reinterpret_cast<const uint4*>(smem + OFF_S + 16384 + e * 16), s1);
+            unpack8(*reinterpret_cast<const uint4*>(smem + OFF_DS + e * 16), d0);
+            unpack8(*reinterpret_cast<const uint4*>(smem + OFF_DS + 16384 + e * 16), d1);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dot = fmaf(s0[j] + s1[j], d0[j] + d1[j], dot);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+    if (lane == 0) m->dot[warp] = dot;
+    if (!up) m->drv[cg][tok] = drv;
+
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    const Gates* gt = &m->gates;
+    const float2 Gi = gt->G[tok];
+    const float a = gt->a[tok], at = gt->at[tok], be = gt->beta[tok], sa = q.scale * a, ba = be * a;
+    const bool live = tok < nt;
+    float rowG = 0.f, rowB = 0.f, tail = 0.f;
+    mbar_wait_flag(&m->done[0], 0, &m->abort_flag, status, 2);
+    __syncwarp();
+    tc_fence_after();
+    {
+        // 16 columns: up, scale Gam o dP (dP of rows behind the end is that of zero rows of dY);
+        // down, D, and each side's part of E
+        float d[16], s[16], e[16];
+        tmem_ld16x2(tl + D_PA + 16 * cg, tl + D_QK + 16 * cg, d, s);
+        float2 f[8];
+#pragma unroll
+        for (int k2 = 0; k2 < 8; ++k2) {
+            const int j = 16 * cg + 2 * k2;
+            const float4 Gj = *reinterpret_cast<const float4*>(&gt->G[j]);
+            float v[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int k = 2 * k2 + x;
+                const float2 gj = x ? make_float2(Gj.z, Gj.w) : make_float2(Gj.x, Gj.y);
+                const bool in = live && (up ? j + x <= tok : j + x < tok);
+                const float gam = in ? ex2(diff_pair(Gi, gj)) : 0.f;
+                const float t = in ? d[k] * gam : 0.f;             // Gam o dP, or - Gam o dA
+                const float ts = in ? t * s[k] : 0.f;
+                if (up) {
+                    e[k] = q.scale * ts;
+                    v[x] = q.scale * t;
+                } else {
+                    rowB -= ts;
+                    e[k] = -be * ts;
+                    v[x] = -be * t;
+                }
+                rowG += e[k];
+            }
+            f[k2] = make_float2(v[0], v[1]);
+            if (!up) {
+                // D at (tok, j) and (j, tok); its diagonal is zero
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const __nv_bfloat16 w = __float2bfloat16_rn(v[x]);
+                    const int jj = j + x;
+                    if (jj <= tok && M3_IN(9, tok * 64 + jj, 4096)) {
+                        *reinterpret_cast<__nv_bfloat16*>(smem + OFF_D + sw128(64 + tok, jj >> 3) + (jj & 7) * 2) = w;
+                        *reinterpret_cast<__nv_bfloat16*>(smem + OFF_D + sw128(64 + jj, tok >> 3) + (tok & 7) * 2) = w;
+                    }
+                }
+            }
+        }
+        if (up) {
+            put16(smem, OFF_D, sw128(tok, 2 * cg), 16384, round8(f));
+            put16(smem, OFF_D, sw128(tok, 2 * cg + 1), 16384, round8(f + 4));
+        }
+        const float cs = column_sums(e);
+        if (lane < 16) m->col[quarter][16 * cg + lane] = cs;
+    }
+    arrived();
+    if (warp == 0) {
+        const uint64_t aD = sdesc(sb + OFF_D, 16, 1024), aDT = sdesc(sb + OFF_D - 8192, 8192, 1024);   // second atom: rows 64..127
+        const uint64_t mK = sdesc(sb + OFF_QK + 8192, 16384, 1024), mQ = sdesc(sb + OFF_QK, 16384, 1024);
+        constexpr uint32_t idL = idesc_bf16(128, 128, 0, 1), idT = idesc_bf16(128, 128, 1, 1);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_LAST, aD + kk * 2, mK + kk * 128, idL, kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_T, aDT + kk * 128, mQ + kk * 128, idT, kk > 0);
+        commit_one(&m->done[1]);
+    }
+    // 32 columns of Z (up) or X and Y (down)
+    mbar_wait_flag(&m->done[3], (slices - 1) & 1, &m->abort_flag, status, 3);
+    __syncwarp();
+    tc_fence_after();
+    float r[32];
+    tmem_ld32(tl + D_ZX + 32 * cg, r);
+    {
+        float t0 = 0.f, t1 = 0.f;
+        float y[32];
+        if (!up) tmem_ld32(tl + D_Y + 32 * cg, y);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+            const int col8 = 4 * cg + ch;
+            float k[8];
+            unpack8(*reinterpret_cast<const uint4*>(smem + OFF_QK + (col8 >> 3) * 16384 + sw128(row, col8 & 7)), k);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                t0 = fmaf(r[8 * ch + j], k[j], t0);
+                if (up) {
+                    r[8 * ch + j] *= sa;
+                } else {
+                    t1 = fmaf(y[8 * ch + j], k[j], t1);
+                    r[8 * ch + j] = fmaf(at, y[8 * ch + j], -ba * r[8 * ch + j]);
+                }
+            }
+        }
+        if (up) {
+            rowG += sa * t0;
+        } else {
+            rowG += -ba * t0 - at * t1;
+            rowB -= a * t0;
+            tail = at * t1;
+        }
+    }
+    m->row[cg][row] = rowG;
+    if (!up) {
+        m->beta[cg][tok] = rowB;
+        m->tail[cg][tok] = tail;
+    }
+    mbar_wait_flag(&m->done[1], 0, &m->abort_flag, status, 4);
+    __syncwarp();
+    tc_fence_after();
+    {
+        float l[32];
+        tmem_ld32(tl + D_LAST + 32 * cg, l);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) r[j] += l[j];
+        if (!up) {
+            tmem_ld32(tl + D_T + 32 * cg, l);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] += l[j];
+        }
+        if (tok < rows) {
+            if (!live)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = 0.f;
+            if (hpg == 1) {
+                const size_t o = ((row0 + tok) * q.ngroups + g) * kN + 32 * cg;
+                if (M3_SPAN(10, o, 32, ext_k)) {
+                    uint4* dst = reinterpret_cast<uint4*>((up ? out_q : out_k) + o);
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) dst[ch] = pack_chunk(r + 8 * ch);
+                }
+            } else {
+                const size_t o = (((row0 + tok) * H + h) * 2 + (up ? 0 : 1)) * kN + 32 * cg;
+                if (M3_SPAN(11, o, 32, toks * 2 * kN)) {
+                    float4* dst = reinterpret_cast<float4*>(q.part_qk + o);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) dst[j] = make_float4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        // (the last commit follows all products; after an expired wait this lets them end)
+        mbar_wait_flag(&m->done[1], 0, &m->drain_flag, nullptr, 0);
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
         // lane l has tokens 2 l, 2 l + 1; dg is the sum from a token to the chunk's end
-        float d[2], tl = 0.f, total = 0.f;
+        float d[2], tl2 = 0.f, total = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = 2 * lane + e;
             d[e] = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                d[e] += gs->row[j][i] - gs->col[j][i];
-                tl += gs->tail[j][i];
+                d[e] += m->row[j][i] + m->row[j][64 + i] - m->col[j][i];
+                tl2 += m->tail[j][i];
             }
         }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) tl += __shfl_xor_sync(kFull, tl, o);
+        for (int o = 16; o; o >>= 1) tl2 += __shfl_xor_sync(kFull, tl2, o);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) total += gs->dot[j];
-        tl += gt->whole * total;
+        for (int j = 0; j < 16; ++j) total += m->dot[j];
+        tl2 += gt->whole * total;
         float sum = d[0] + d[1];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const float u = __shfl_down_sync(kFull, sum, o);
             if (lane + o < 32) sum += u;
         }
-        const float dg[2] = {sum + tl, sum - d[0] + tl};
+        const float dg[2] = {sum + tl2, sum - d[0] + tl2};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = 2 * lane + e;
             const size_t o = (row0 + i) * H + h;
-            if (i >= rows || !M3_IN(17, o, toks)) continue;
+            if (i >= rows || !M3_IN(12, o, toks)) continue;
+            float vb = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) vb += m->drv[j][i] + m->beta[j][i];
             const float vg = i < nt ? dg[e] : 0.f;
-            const float vb = i < nt ? gs->drv[i] + gs->beta[0][i] + gs->beta[1][i] + gs->beta[2][i] + gs->beta[3][i] : 0.f;
+            vb = i < nt ? vb : 0.f;
             if (hpg == 1) {
                 if (out_g) out_g[o] = __float2bfloat16_rn(vg);
                 out_b[o] = __float2bfloat16_rn(vb);
@@ -436,9 +497,9 @@ cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* sta
     if (e != cudaSuccess) return e;
     e = launch_delta_rev(d, q, status, st);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_BYTES);
+    e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    delta_grad_kernel<<<(unsigned)((long long)d.batch * d.nheads * q.nck), kGradThreads, GR_BYTES, st>>>(q, q.nck);
+    delta_grad_kernel<<<(unsigned)((long long)d.batch * d.nheads * q.nck), kThreads, SMEM_BYTES, st>>>(q, q.nck, status);
     e = cudaGetLastError();
     if (e != cudaSuccess || d.nheads == d.ngroups) return e;
     return launch_delta_reduce(d, q, 1, st);
