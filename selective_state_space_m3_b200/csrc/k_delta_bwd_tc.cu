@@ -111,7 +111,7 @@ __device__ __forceinline__ float column_sums(float* v) {
     return v[0];
 }
 
-__global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, int nchunks, int* status) {
+__global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, int nchunks, int ahead, int* status) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (su32(smem_raw) & 1023u)) & 1023u);
     Misc* m = reinterpret_cast<Misc*>(smem + OFF_MISC);
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
         tmem_alloc(&m->tmem_base, 512);
         tmem_relinquish();
     }
+    const int slices = P / 64;
     const size_t rec0 = ((size_t)bh * q.nck + c) * rec_elems(P, true);
     // `pieces` recorded pieces of 16 bytes a row, `rows_` rows each, `pitch` bytes apart in shared memory
     auto load_rec = [&](uint32_t dst, size_t o, int rows_, int pitch) {
@@ -196,6 +197,27 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
         cp_commit();
     };
     load_slice(0);
+    // the chunk that follows on this SM, into L2 (one CTA an SM: `ahead` CTAs run together)
+    if ((long long)blockIdx.x + ahead < (long long)gridDim.x) {
+        const int nb = blockIdx.x + ahead, bh2 = nb / nchunks, c2 = nb % nchunks, b2 = bh2 / H, h2 = bh2 % H;
+        if (tid < slices)
+            bulk_prefetch(q.rec + (size_t)nb * rec_elems(P, true) + kRecSlice + tid * kSliceElems, (uint32_t)(kSliceElems * 2));
+        if (tid >= 64 && tid < 128 && c2 * kC + tid - 64 < q.seqlen) {
+            const size_t r = (size_t)b2 * q.seqlen + c2 * kC + tid - 64;
+            const size_t ko = (r * q.ngroups + h2 / hpg) * kN, vo = (r * H + h2) * P;
+            if (M3_SPAN(13, ko, kN, ext_k) && M3_SPAN(14, vo, P, ext_v)) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    prefetch_l2(static_cast<const __nv_bfloat16*>(q.k) + ko + 64 * j);
+                    prefetch_l2(static_cast<const __nv_bfloat16*>(q.q) + ko + 64 * j);
+                }
+                for (int j = 0; j < slices; ++j) {
+                    prefetch_l2(static_cast<const __nv_bfloat16*>(q.dy) + vo + 64 * j);
+                    prefetch_l2(static_cast<const __nv_bfloat16*>(q.v) + vo + 64 * j);
+                }
+            }
+        }
+    }
     if (warp == 4) make_gates(load_raw(q, b, h, len, c), &m->gates);
 
     // all threads' copies of a group are in place and visible to the products
@@ -216,7 +238,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
     const bool up = quarter < 2;                   // rows 0..63: dq's side; 64..127: dk's
     uint32_t tmem = 0;
     float dot = 0.f, drv = 0.f;                    // <S, dS'>; dR . v
-    const int slices = P / 64;
     for (int sl = 0; sl < slices; ++sl) {
         if (sl > 0) {
             mbar_wait_flag(&m->done[3], (sl - 1) & 1, &m->abort_flag, status, 1);
@@ -499,7 +520,8 @@ cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* sta
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    delta_grad_kernel<<<(unsigned)((long long)d.batch * d.nheads * q.nck), kThreads, SMEM_BYTES, st>>>(q, q.nck, status);
+    delta_grad_kernel<<<(unsigned)((long long)d.batch * d.nheads * q.nck), kThreads, SMEM_BYTES, st>>>(q, q.nck,
+                                                                                                                device_sm_count(), status);
     e = cudaGetLastError();
     if (e != cudaSuccess || d.nheads == d.ngroups) return e;
     return launch_delta_reduce(d, q, 1, st);
