@@ -23,8 +23,8 @@
 // of the left operand are two matrices, so that a thread finds all that belongs
 // to a token in its row):
 //   [Q; K] K^T,  [dY; dR] U^T,  [dY; dR] S^T,  [.; U] dS'^T
-//   [scale Gam o dP; D + D^T] K,  [.; (scale Gam o dP)^T] Q
-// D + D^T is one symmetric matrix, since D is strictly lower.  All that feeds
+//   [scale Gam o dP; D] K,  [.; (scale Gam o dP)^T] Q + [.; D^T] K
+// All that feeds
 // dg and dbeta (sums with cancellation) keeps float32 values as two bfloat16
 // parts (hi + lo; a product of two split operands drops lo x lo); the last two
 // products take rounded left operands, for they end in dq and dk, which are
@@ -42,6 +42,9 @@
 #include "delta_tc.cuh"
 
 namespace m3 {
+
+bool make_tile_map(CUtensorMap* map, const void* base, int inner, int R, int grp, int L, int batch, int T);
+
 namespace dbw {
 
 using namespace dtc;
@@ -54,7 +57,7 @@ constexpr int OFF_U = OFF_A2 + 16384;            // U hi, lo (8 KB each; pieces 
 constexpr int OFF_A = OFF_U + 16384;             // [dY; dR hi] (16 KB)
 constexpr int OFF_S = OFF_A + 16384;             // S hi, lo (16 KB each; pieces of 128 rows)
 constexpr int OFF_DS = OFF_S + 32768;            // dS' hi, lo
-constexpr int OFF_D = OFF_DS + 32768;            // [scale Gam o dP; D + D^T] (16 KB, sw128)
+constexpr int OFF_D = OFF_DS + 32768;            // [scale Gam o dP; D] (16 KB, sw128)
 constexpr int OFF_MISC = OFF_D + 16384;
 // TMEM columns; the last product takes the place of the first two
 constexpr uint32_t D_PA = 0, D_QK = 64, D_ZX = 128, D_Y = 256, D_LAST = 384, D_T = 0;
@@ -64,18 +67,12 @@ struct Misc {
     float row[4][2 * kC], beta[4][kC], tail[4][kC];    // by column group (row: upper and lower rows' parts)
     float col[4][kC];                                  // by row quarter (its 16 columns a group)
     float drv[4][kC], dot[16];
-    uint64_t done[4];
+    uint64_t full[3], done[3];
     uint32_t tmem_base;
     int abort_flag, drain_flag, pad;
 };
 constexpr int SMEM_BYTES = OFF_MISC + (int)sizeof(Misc) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory of the chunk gradients");
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-    const int n = ok ? 16 : 0;               // 0: the destination gets zeros, the source is not read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // matrix descriptor without exchange of 16-byte groups: 8 rows x 16 bytes lie
 // together, `lbo` bytes to the next 8 columns, `sbo` to the next 8 rows
@@ -111,7 +108,9 @@ __device__ __forceinline__ float column_sums(float* v) {
     return v[0];
 }
 
-__global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, int nchunks, int ahead, int* status) {
+__global__ void __launch_bounds__(kThreads, 1) 
+    delta_grad_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ, DeltaParams q,
+                      int nchunks, int ahead, int* status) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (su32(smem_raw) & 1023u)) & 1023u);
     Misc* m = reinterpret_cast<Misc*>(smem + OFF_MISC);
@@ -149,7 +148,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(&m->done[i], 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&m->full[i], 1);
+            mbar_init(&m->done[i], 1);
+        }
         m->abort_flag = 0;
         m->drain_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -160,42 +162,35 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
     }
     const int slices = P / 64;
     const size_t rec0 = ((size_t)bh * q.nck + c) * rec_elems(P, true);
-    // `pieces` recorded pieces of 16 bytes a row, `rows_` rows each, `pitch` bytes apart in shared memory
-    auto load_rec = [&](uint32_t dst, size_t o, int rows_, int pitch) {
-        for (int e = tid; e < rows_ * 8; e += kThreads) {
-            const bool ok = M3_SPAN(5, o + (size_t)e * 8, 8, ext_rec);
-            cp16(dst + (e / rows_) * pitch + (e % rows_) * 16, q.rec + (ok ? o + (size_t)e * 8 : 0), ok);
-        }
-    };
+    // dY of the slice, rows behind the end (other data, possibly not numbers) as
+    // zeros; the other matrices by the copy engine, in three groups
     auto load_slice = [&](int sl) {
-        const size_t o = rec0 + kRecSlice + sl * kSliceElems;
-        if (sl == 0)                                           // rows behind the end are zeros
-            for (int e = tid; e < 64 * 32; e += kThreads) {
-                const int r = e >> 5, ch = e & 31;             // 16 groups of Q, 16 of K
-                const size_t ko = ((row0 + r) * q.ngroups + g) * kN + 8 * (ch & 15);
-                const bool ok = r < nt && M3_SPAN(6, ko, 8, ext_k);
-                cp16(sb + OFF_QK + ((ch >> 3) & 1) * 16384 + sw128(r + (ch >> 4) * 64, ch & 7),
-                     static_cast<const __nv_bfloat16*>((ch >> 4) ? q.k : q.q) + (ok ? ko : 0), ok);
+        if (tid == 0) {
+            const __nv_bfloat16* src = q.rec + rec0 + kRecSlice + sl * kSliceElems;
+            M3_NOTE(5, rec0 + kRecSlice + (sl + 1) * kSliceElems - 1, ext_rec);
+            mbar_expect_tx(&m->full[0], (sl == 0 ? 32768u : 0u) + 16384u + 8192u);
+            if (sl == 0) {
+                tma_load_5d(sb + OFF_QK, &tmQ, &m->full[0], 0, 0, g, c * kC, b);
+                tma_load_5d(sb + OFF_QK + 16384, &tmQ, &m->full[0], 64, 0, g, c * kC, b);
+                tma_load_5d(sb + OFF_QK + 8192, &tmK, &m->full[0], 0, 0, g, c * kC, b);
+                tma_load_5d(sb + OFF_QK + 24576, &tmK, &m->full[0], 64, 0, g, c * kC, b);
             }
-        {
-            const int r = tid >> 3, p = tid & 7;
-            const size_t vo = ((row0 + r) * H + h) * P + 64 * sl + 8 * p;
-            const bool ok = r < nt && M3_SPAN(7, vo, 8, ext_v);
-            cp16(sb + OFF_A + p * 2048 + r * 16, static_cast<const __nv_bfloat16*>(q.dy) + (ok ? vo : 0), ok);
-            cp16(sb + OFF_A2 + p * 2048 + r * 16, q.rec, false);           // zeros
+            bulk_load(sb + OFF_U, src + kSliceU, 16384, &m->full[0]);
+            for (int p = 0; p < 8; ++p) bulk_load(sb + OFF_A + p * 2048 + 1024, src + kSliceDR + p * 512, 1024, &m->full[0]);
+            mbar_expect_tx(&m->full[1], 8192 + 32768);
+            for (int p = 0; p < 8; ++p) bulk_load(sb + OFF_A2 + p * 2048 + 1024, src + kSliceDR + kTok + p * 512, 1024, &m->full[1]);
+            bulk_load(sb + OFF_S, src + kSliceS, 32768, &m->full[1]);
+            mbar_expect_tx(&m->full[2], 32768);
+            bulk_load(sb + OFF_DS, src + kSliceDS, 32768, &m->full[2]);
         }
-        load_rec(sb + OFF_A + 1024, o + kSliceDR, 64, 2048);
-        load_rec(sb + OFF_U, o + kSliceU, 64, 1024);
-        load_rec(sb + OFF_U + 8192, o + kSliceU + kTok, 64, 1024);
-        cp_commit();
-        load_rec(sb + OFF_A2 + 1024, o + kSliceDR + kTok, 64, 2048);
-        load_rec(sb + OFF_S, o + kSliceS, 128, 2048);
-        load_rec(sb + OFF_S + 16384, o + kSliceS + kSt, 128, 2048);
-        cp_commit();
-        load_rec(sb + OFF_DS, o + kSliceDS, 128, 2048);
-        load_rec(sb + OFF_DS + 16384, o + kSliceDS + kSt, 128, 2048);
-        cp_commit();
+        const int r = tid >> 3, p = tid & 7;
+        const size_t vo = ((row0 + r) * H + h) * P + 64 * sl + 8 * p;
+        const uint32_t o = p * 2048 + r * 16;
+        put16(smem, OFF_A, o, 16384, r < nt && M3_SPAN(7, vo, 8, ext_v) ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(q.dy) + vo))
+                                                                    : make_uint4(0u, 0u, 0u, 0u));
+        if (sl == 0) put16(smem, OFF_A2, o, 16384, make_uint4(0u, 0u, 0u, 0u));
     };
+    __syncthreads();                               // (barriers are ready)
     load_slice(0);
     // the chunk that follows on this SM, into L2 (one CTA an SM: `ahead` CTAs run together)
     if ((long long)blockIdx.x + ahead < (long long)gridDim.x) {
@@ -237,14 +232,22 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
     const int quarter = warp & 3, cg = warp >> 2, row = quarter * 32 + lane, tok = row & 63;
     const bool up = quarter < 2;                   // rows 0..63: dq's side; 64..127: dk's
     uint32_t tmem = 0;
-    float dot = 0.f, drv = 0.f;                    // <S, dS'>; dR . v
+    float2 dot2 = make_float2(0.f, 0.f);           // <S, dS'>
+    float drv = 0.f;                               // dR . v
     for (int sl = 0; sl < slices; ++sl) {
         if (sl > 0) {
-            mbar_wait_flag(&m->done[3], (sl - 1) & 1, &m->abort_flag, status, 1);
-            __syncthreads();
+            mbar_wait_flag(&m->done[2], (sl - 1) & 1, &m->abort_flag, status, 1);
+            // (a barrier that waits for the sums, so that all they read has been read)
+            __syncthreads_or(drv != drv && dot2.x != dot2.x);
             load_slice(sl);
         }
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        mbar_wait_flag(&m->full[0], sl & 1, &m->abort_flag, status, 5);
+        if (sl == 0 && nt < kC)
+            // Q and K rows behind the end must be zeros: the last products sum over all rows of the tiles
+            for (int e = tid; e < (kC - nt) * 32; e += kThreads) {
+                const int r = nt + (e >> 5), ch = e & 31;
+                put16(smem, OFF_QK + ((ch >> 3) & 1) * 16384, sw128(r + (ch >> 4) * 64, ch & 7), 16384, make_uint4(0u, 0u, 0u, 0u));
+            }
         arrived();
         tmem = m->tmem_base;
         if (warp == 0) {
@@ -257,9 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_PA, aA + kk * 256, bUl + kk * 128, id64, 1);
         }
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        arrived();
+        mbar_wait_flag(&m->full[1], sl & 1, &m->abort_flag, status, 6);
         if (warp == 0) {
+            __syncwarp();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_PA, aA2 + kk * 256, bU + kk * 128, id64, 1);
             if (sl == slices - 1) commit_one(&m->done[0]);
@@ -284,28 +287,29 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
                 for (int e = 0; e < 8; ++e) drv = fmaf(r[e] + l[e], v[e], drv);
             }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        arrived();
+        mbar_wait_flag(&m->full[2], sl & 1, &m->abort_flag, status, 7);
         if (warp == 0) {
+            __syncwarp();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_Y, aU + kk * 128, bDS + kk * 256, id128, sl + kk > 0);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_Y, aU + kk * 128, bDSl + kk * 256, id128, 1);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_Y, aUl + kk * 128, bDS + kk * 256, id128, 1);
-            commit_one(&m->done[3]);
+            commit_one(&m->done[2]);
         }
 #pragma unroll
         for (int e = tid; e < 1024; e += kThreads) {
-            float s0[8], s1[8], d0[8], d1[8];
-            unpack8(*reinterpret_cast<const uint4*>(smem + OFF_S + e * 16), s0);
-            unpack8(*reinterpret_cast<const uint4*>(smem + OFF_S + 16384 + e * 16), s1);
-            unpack8(*reinterpret_cast<const uint4*>(smem + OFF_DS + e * 16), d0);
-            unpack8(*reinterpret_cast<const uint4*>(smem + OFF_DS + 16384 + e * 16), d1);
+            const uint4 s0 = *reinterpret_cast<const uint4*>(smem + OFF_S + e * 16), s1 = *reinterpret_cast<const uint4*>(smem + OFF_S + 16384 + e * 16);
+            const uint4 d0 = *reinterpret_cast<const uint4*>(smem + OFF_DS + e * 16), d1 = *reinterpret_cast<const uint4*>(smem + OFF_DS + 16384 + e * 16);
+            const uint32_t a0[4] = {s0.x, s0.y, s0.z, s0.w}, a1[4] = {s1.x, s1.y, s1.z, s1.w};
+            const uint32_t b0[4] = {d0.x, d0.y, d0.z, d0.w}, b1[4] = {d1.x, d1.y, d1.z, d1.w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dot = fmaf(s0[j] + s1[j], d0[j] + d1[j], dot);
+            for (int j = 0; j < 4; ++j)
+                dot2 = __ffma2_rn(__fadd2_rn(unpack(a0[j]), unpack(a1[j])), __fadd2_rn(unpack(b0[j]), unpack(b1[j])), dot2);
         }
     }
+    float dot = dot2.x + dot2.y;
 #pragma unroll
     for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
     if (lane == 0) m->dot[warp] = dot;
@@ -320,7 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
     mbar_wait_flag(&m->done[0], 0, &m->abort_flag, status, 2);
     __syncwarp();
     tc_fence_after();
-    {
+    if (16 * cg > (tok | 31)) {                    // right of the diagonal for all of the warp
+        put16(smem, OFF_D, sw128(row, 2 * cg), 16384, make_uint4(0u, 0u, 0u, 0u));
+        put16(smem, OFF_D, sw128(row, 2 * cg + 1), 16384, make_uint4(0u, 0u, 0u, 0u));
+        if (lane < 16) m->col[quarter][16 * cg + lane] = 0.f;
+    } else {
         // 16 columns: up, scale Gam o dP (dP of rows behind the end is that of zero rows of dY);
         // down, D, and each side's part of E
         float d[16], s[16], e[16];
@@ -350,23 +358,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
                 rowG += e[k];
             }
             f[k2] = make_float2(v[0], v[1]);
-            if (!up) {
-                // D at (tok, j) and (j, tok); its diagonal is zero
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const __nv_bfloat16 w = __float2bfloat16_rn(v[x]);
-                    const int jj = j + x;
-                    if (jj <= tok && M3_IN(9, tok * 64 + jj, 4096)) {
-                        *reinterpret_cast<__nv_bfloat16*>(smem + OFF_D + sw128(64 + tok, jj >> 3) + (jj & 7) * 2) = w;
-                        *reinterpret_cast<__nv_bfloat16*>(smem + OFF_D + sw128(64 + jj, tok >> 3) + (tok & 7) * 2) = w;
-                    }
-                }
-            }
         }
-        if (up) {
-            put16(smem, OFF_D, sw128(tok, 2 * cg), 16384, round8(f));
-            put16(smem, OFF_D, sw128(tok, 2 * cg + 1), 16384, round8(f + 4));
-        }
+        put16(smem, OFF_D, sw128(row, 2 * cg), 16384, round8(f));
+        put16(smem, OFF_D, sw128(row, 2 * cg + 1), 16384, round8(f + 4));
         const float cs = column_sums(e);
         if (lane < 16) m->col[quarter][16 * cg + lane] = cs;
     }
@@ -379,10 +373,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(DeltaParams q, 
         for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_LAST, aD + kk * 2, mK + kk * 128, idL, kk > 0);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_T, aDT + kk * 128, mQ + kk * 128, idT, kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_T, aDT + 512 + kk * 128, mK + kk * 128, idT, 1);
         commit_one(&m->done[1]);
     }
     // 32 columns of Z (up) or X and Y (down)
-    mbar_wait_flag(&m->done[3], (slices - 1) & 1, &m->abort_flag, status, 3);
+    mbar_wait_flag(&m->done[2], (slices - 1) & 1, &m->abort_flag, status, 3);
     __syncwarp();
     tc_fence_after();
     float r[32];
@@ -520,8 +516,12 @@ cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* sta
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    delta_grad_kernel<<<(unsigned)((long long)d.batch * d.nheads * q.nck), kThreads, SMEM_BYTES, st>>>(q, q.nck,
-                                                                                                                device_sm_count(), status);
+    CUtensorMap mK, mQ;
+    if (!make_tile_map(&mK, q.k, kN, 1, d.ngroups, d.seqlen, d.batch, kC) ||
+        !make_tile_map(&mQ, q.q, kN, 1, d.ngroups, d.seqlen, d.batch, kC))
+        return cudaErrorInvalidValue;
+    delta_grad_kernel<<<(unsigned)((long long)d.batch * d.nheads * q.nck), kThreads, SMEM_BYTES, st>>>(
+        mK, mQ, q, q.nck, device_sm_count(), status);
     e = cudaGetLastError();
     if (e != cudaSuccess || d.nheads == d.ngroups) return e;
     return launch_delta_reduce(d, q, 1, st);
