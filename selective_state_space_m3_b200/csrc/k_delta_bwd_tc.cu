@@ -15,8 +15,9 @@
 //
 // Three passes.  The prefill runs once more and records T, P, the state before
 // every chunk and U.  k_delta_rev.cu carries dS from the last chunk to the first
-// and records dS' and dR.  delta_grad_kernel here then takes all chunks at once,
-// one CTA each.  dq and dk of a group's heads are added by a further kernel in a
+// and records dS' and dR.  delta_grad_kernel here then takes all chunks in any
+// order, one CTA an SM, the next chunk's records on their way while the present
+// one is finished.  dq and dk of a group's heads are added by a further kernel in a
 // fixed order.
 //
 // Products (tcgen05, M = 128 rows, accumulators in TMEM; rows 0..63 and 64..127
@@ -63,11 +64,11 @@ constexpr int OFF_MISC = OFF_D + 16384;
 constexpr uint32_t D_PA = 0, D_QK = 64, D_ZX = 128, D_Y = 256, D_LAST = 384, D_T = 0;
 
 struct Misc {
-    Gates gates;
+    Gates gates[2];
     float row[4][2 * kC], beta[4][kC], tail[4][kC];    // by column group (row: upper and lower rows' parts)
     float col[4][kC];                                  // by row quarter (its 16 columns a group)
     float drv[4][kC], dot[16];
-    uint64_t full[3], done[3];
+    uint64_t full[4], done[3], drain;
     uint32_t tmem_base;
     int abort_flag, drain_flag, pad;
 };
@@ -108,399 +109,467 @@ __device__ __forceinline__ float column_sums(float* v) {
     return v[0];
 }
 
-__global__ void __launch_bounds__(kThreads, 1) 
+// The CTAs (one an SM) walk the chunks; the records of a CTA's next chunk are on
+// their way while it finishes the present one.
+__global__ void __launch_bounds__(kThreads, 1)
     delta_grad_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ, DeltaParams q,
-                      int nchunks, int ahead, int* status) {
+                      int total_chunks, int* status) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (su32(smem_raw) & 1023u)) & 1023u);
     Misc* m = reinterpret_cast<Misc*>(smem + OFF_MISC);
     const uint32_t sb = su32(smem);
     if (!M3_SPAN(1, smem - smem_raw, OFF_MISC + (int)sizeof(Misc), dyn_smem_bytes())) return;
     const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31, P = q.headdim, H = q.nheads;
-    const int bh = blockIdx.x / nchunks, c = blockIdx.x % nchunks;
-    const int b = bh / H, h = bh % H, hpg = H / q.ngroups, g = h / hpg;
-    int len = q.seqlen;
-    if (q.lengths && M3_IN(2, b, q.batch)) len = min(max(q.lengths[b], 0), q.seqlen);
-    const int nt = min(kC, len - c * kC);
-    [[maybe_unused]] const long long ext_k = (long long)q.batch * q.seqlen * q.ngroups * kN, ext_v = (long long)q.batch * q.seqlen * H * P;
+    const int hpg = H / q.ngroups, slices = P / 64;
+    [[maybe_unused]] const long long ext_k = (long long)q.batch * q.seqlen * q.ngroups * kN;
+    [[maybe_unused]] const long long ext_v = (long long)q.batch * q.seqlen * H * P;
     [[maybe_unused]] const long long toks = (long long)q.batch * q.seqlen * H;
     [[maybe_unused]] const long long ext_rec = (long long)q.batch * H * q.nck * (long long)rec_elems(P, true);
-    const size_t row0 = (size_t)b * q.seqlen + c * kC;
-    const int rows = min(kC, q.seqlen - c * kC);               // rows of the outputs in this chunk
     __nv_bfloat16* out_q = static_cast<__nv_bfloat16*>(q.dq);
     __nv_bfloat16* out_k = static_cast<__nv_bfloat16*>(q.dk);
     __nv_bfloat16* out_g = static_cast<__nv_bfloat16*>(q.dg);
     __nv_bfloat16* out_b = static_cast<__nv_bfloat16*>(q.dbeta);
-    if (nt <= 0) {                                             // behind the end (a group's heads: the sum kernel's zeros)
-        if (hpg == 1) {
-            for (int e = tid; e < rows * 16; e += kThreads) {
-                const size_t o = ((row0 + (e >> 4)) * q.ngroups + g) * kN + 8 * (e & 15);
-                if (M3_SPAN(3, o, 8, ext_k)) {
-                    *reinterpret_cast<uint4*>(out_q + o) = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(out_k + o) = make_uint4(0u, 0u, 0u, 0u);
-                }
-            }
-            if (tid < rows && M3_IN(4, (row0 + tid) * H + h, toks)) {
-                if (out_g) out_g[(row0 + tid) * H + h] = __float2bfloat16_rn(0.f);
-                out_b[(row0 + tid) * H + h] = __float2bfloat16_rn(0.f);
-            }
-        }
-        return;
-    }
+    struct At {
+        int b, h, g, c, len, nt;                   // nt <= 0: behind the sequence's end
+    };
+    auto locate = [&](int n) {
+        At t;
+        const int bh = n / q.nck;
+        t.c = n % q.nck;
+        t.b = bh / H;
+        t.h = bh % H;
+        t.g = t.h / hpg;
+        t.len = q.seqlen;
+        if (q.lengths && M3_IN(2, t.b, q.batch)) t.len = min(max(q.lengths[t.b], 0), q.seqlen);
+        t.nt = min(kC, t.len - t.c * kC);
+        return t;
+    };
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i) {
-            mbar_init(&m->full[i], 1);
-            mbar_init(&m->done[i], 1);
-        }
+        for (int i = 0; i < 4; ++i) mbar_init(&m->full[i], 1);
+        for (int i = 0; i < 3; ++i) mbar_init(&m->done[i], 1);
+        mbar_init(&m->drain, 1);
         m->abort_flag = 0;
         m->drain_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
     }
+    __syncwarp();
     if (warp == 0) {
         tmem_alloc(&m->tmem_base, 512);
         tmem_relinquish();
     }
-    const int slices = P / 64;
-    const size_t rec0 = ((size_t)bh * q.nck + c) * rec_elems(P, true);
-    // dY of the slice, rows behind the end (other data, possibly not numbers) as
-    // zeros; the other matrices by the copy engine, in three groups
-    auto load_slice = [&](int sl) {
+    put16(smem, OFF_A2, (tid & 7) * 2048 + (tid >> 3) * 16, 16384, make_uint4(0u, 0u, 0u, 0u));    // (rows 0..63 stay zero)
+    __syncthreads();
+    int asked = 0;                                 // sets of records asked for (thread 0)
+    // the recorded matrices of a slice, by the copy engine, in three groups
+    auto load_records = [&](int n, int sl) {
+        const size_t o = (size_t)n * rec_elems(P, true) + kRecSlice + sl * kSliceElems;
+        const __nv_bfloat16* src = q.rec + o;
+        M3_NOTE(5, o + kSliceElems - 1, ext_rec);
+        mbar_expect_tx(&m->full[0], 16384 + 8192);
+        bulk_load(sb + OFF_U, src + kSliceU, 16384, &m->full[0]);
+        for (int p = 0; p < 8; ++p) bulk_load(sb + OFF_A + p * 2048 + 1024, src + kSliceDR + p * 512, 1024, &m->full[0]);
+        mbar_expect_tx(&m->full[1], 8192 + 32768);
+        for (int p = 0; p < 8; ++p) bulk_load(sb + OFF_A2 + p * 2048 + 1024, src + kSliceDR + kTok + p * 512, 1024, &m->full[1]);
+        bulk_load(sb + OFF_S, src + kSliceS, 32768, &m->full[1]);
+        mbar_expect_tx(&m->full[2], 32768);
+        ++asked;
+        bulk_load(sb + OFF_DS, src + kSliceDS, 32768, &m->full[2]);
+    };
+    // 16 bytes a thread of the slice's dY; rows behind the end (other data, possibly not numbers) are zeros
+    auto fetch_dy = [&](const At& t, int sl) {
+        const int r = tid >> 3;
+        const size_t vo = (((size_t)t.b * q.seqlen + t.c * kC + r) * H + t.h) * P + 64 * sl + 8 * (tid & 7);
+        if (r >= t.nt || !M3_SPAN(7, vo, 8, ext_v)) return make_uint4(0u, 0u, 0u, 0u);
+        return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(q.dy) + vo));
+    };
+    int fph = 0, done_y = 0, done_c = 0, par = 0;  // phases: records, Y, a chunk's other products; gates
+    bool loaded = false;
+    uint4 dy = make_uint4(0u, 0u, 0u, 0u);
+    int stop = 0;
+    for (int n = blockIdx.x; n < total_chunks && !stop; n += gridDim.x) {
+        const At me = locate(n);
+        const int b = me.b, h = me.h, g = me.g, c = me.c, len = me.len, nt = me.nt;
+        const size_t row0 = (size_t)b * q.seqlen + c * kC;
+        const int rows = min(kC, q.seqlen - c * kC);               // rows of the outputs in this chunk
+        if (nt <= 0) {                                             // behind the end (a group's heads: the sum kernel's zeros)
+            if (hpg == 1) {
+                for (int e = tid; e < rows * 16; e += kThreads) {
+                    const size_t o = ((row0 + (e >> 4)) * q.ngroups + g) * kN + 8 * (e & 15);
+                    if (M3_SPAN(3, o, 8, ext_k)) {
+                        *reinterpret_cast<uint4*>(out_q + o) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(out_k + o) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                if (tid < rows && M3_IN(4, (row0 + tid) * H + h, toks)) {
+                    if (out_g) out_g[(row0 + tid) * H + h] = __float2bfloat16_rn(0.f);
+                    out_b[(row0 + tid) * H + h] = __float2bfloat16_rn(0.f);
+                }
+            }
+            continue;
+        }
         if (tid == 0) {
-            const __nv_bfloat16* src = q.rec + rec0 + kRecSlice + sl * kSliceElems;
-            M3_NOTE(5, rec0 + kRecSlice + (sl + 1) * kSliceElems - 1, ext_rec);
-            mbar_expect_tx(&m->full[0], (sl == 0 ? 32768u : 0u) + 16384u + 8192u);
-            if (sl == 0) {
-                tma_load_5d(sb + OFF_QK, &tmQ, &m->full[0], 0, 0, g, c * kC, b);
-                tma_load_5d(sb + OFF_QK + 16384, &tmQ, &m->full[0], 64, 0, g, c * kC, b);
-                tma_load_5d(sb + OFF_QK + 8192, &tmK, &m->full[0], 0, 0, g, c * kC, b);
-                tma_load_5d(sb + OFF_QK + 24576, &tmK, &m->full[0], 64, 0, g, c * kC, b);
-            }
-            bulk_load(sb + OFF_U, src + kSliceU, 16384, &m->full[0]);
-            for (int p = 0; p < 8; ++p) bulk_load(sb + OFF_A + p * 2048 + 1024, src + kSliceDR + p * 512, 1024, &m->full[0]);
-            mbar_expect_tx(&m->full[1], 8192 + 32768);
-            for (int p = 0; p < 8; ++p) bulk_load(sb + OFF_A2 + p * 2048 + 1024, src + kSliceDR + kTok + p * 512, 1024, &m->full[1]);
-            bulk_load(sb + OFF_S, src + kSliceS, 32768, &m->full[1]);
-            mbar_expect_tx(&m->full[2], 32768);
-            bulk_load(sb + OFF_DS, src + kSliceDS, 32768, &m->full[2]);
+            mbar_expect_tx(&m->full[3], 32768);
+            tma_load_5d(sb + OFF_QK, &tmQ, &m->full[3], 0, 0, g, c * kC, b);
+            tma_load_5d(sb + OFF_QK + 16384, &tmQ, &m->full[3], 64, 0, g, c * kC, b);
+            tma_load_5d(sb + OFF_QK + 8192, &tmK, &m->full[3], 0, 0, g, c * kC, b);
+            tma_load_5d(sb + OFF_QK + 24576, &tmK, &m->full[3], 64, 0, g, c * kC, b);
+            if (!loaded) load_records(n, 0);
         }
-        const int r = tid >> 3, p = tid & 7;
-        const size_t vo = ((row0 + r) * H + h) * P + 64 * sl + 8 * p;
-        const uint32_t o = p * 2048 + r * 16;
-        put16(smem, OFF_A, o, 16384, r < nt && M3_SPAN(7, vo, 8, ext_v) ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(q.dy) + vo))
-                                                                    : make_uint4(0u, 0u, 0u, 0u));
-        if (sl == 0) put16(smem, OFF_A2, o, 16384, make_uint4(0u, 0u, 0u, 0u));
-    };
-    __syncthreads();                               // (barriers are ready)
-    load_slice(0);
-    // the chunk that follows on this SM, into L2 (one CTA an SM: `ahead` CTAs run together)
-    if ((long long)blockIdx.x + ahead < (long long)gridDim.x) {
-        const int nb = blockIdx.x + ahead, bh2 = nb / nchunks, c2 = nb % nchunks, b2 = bh2 / H, h2 = bh2 % H;
-        if (tid < slices)
-            bulk_prefetch(q.rec + (size_t)nb * rec_elems(P, true) + kRecSlice + tid * kSliceElems, (uint32_t)(kSliceElems * 2));
-        if (tid >= 64 && tid < 128 && c2 * kC + tid - 64 < q.seqlen) {
-            const size_t r = (size_t)b2 * q.seqlen + c2 * kC + tid - 64;
-            const size_t ko = (r * q.ngroups + h2 / hpg) * kN, vo = (r * H + h2) * P;
-            if (M3_SPAN(13, ko, kN, ext_k) && M3_SPAN(14, vo, P, ext_v)) {
+        __syncwarp();
+        if (!loaded) dy = fetch_dy(me, 0);
+        if (warp == 4) make_gates(load_raw(q, b, h, len, c), &m->gates[par]);
+        // the chunk after next into L2
+        if ((long long)n + 2LL * gridDim.x < total_chunks) {
+            const int n2 = n + 2 * gridDim.x;
+            const At t = locate(n2);
+            if (tid < slices)
+                bulk_prefetch(q.rec + (size_t)n2 * rec_elems(P, true) + kRecSlice + tid * kSliceElems, (uint32_t)(kSliceElems * 2));
+            if (tid >= 64 && tid < 128 && t.c * kC + tid - 64 < q.seqlen) {
+                const size_t r = (size_t)t.b * q.seqlen + t.c * kC + tid - 64;
+                const size_t ko = (r * q.ngroups + t.g) * kN, vo = (r * H + t.h) * P;
+                if (M3_SPAN(13, ko, kN, ext_k) && M3_SPAN(14, vo, P, ext_v)) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    prefetch_l2(static_cast<const __nv_bfloat16*>(q.k) + ko + 64 * j);
-                    prefetch_l2(static_cast<const __nv_bfloat16*>(q.q) + ko + 64 * j);
-                }
-                for (int j = 0; j < slices; ++j) {
-                    prefetch_l2(static_cast<const __nv_bfloat16*>(q.dy) + vo + 64 * j);
-                    prefetch_l2(static_cast<const __nv_bfloat16*>(q.v) + vo + 64 * j);
+                    for (int j = 0; j < 2; ++j) {
+                        prefetch_l2(static_cast<const __nv_bfloat16*>(q.k) + ko + 64 * j);
+                        prefetch_l2(static_cast<const __nv_bfloat16*>(q.q) + ko + 64 * j);
+                    }
+                    for (int j = 0; j < slices; ++j) {
+                        prefetch_l2(static_cast<const __nv_bfloat16*>(q.dy) + vo + 64 * j);
+                        prefetch_l2(static_cast<const __nv_bfloat16*>(q.v) + vo + 64 * j);
+                    }
                 }
             }
         }
-    }
-    if (warp == 4) make_gates(load_raw(q, b, h, len, c), &m->gates);
 
-    // all threads' copies of a group are in place and visible to the products
-    auto arrived = [&]() {
-        fence_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-    };
-    const uint64_t aQK = sdesc(sb + OFF_QK, 16, 1024), bK = sdesc(sb + OFF_QK + 8192, 16, 1024);
-    const uint64_t aA = sdesc0(sb + OFF_A, 2048, 128), aA2 = sdesc0(sb + OFF_A2, 2048, 128);
-    const uint64_t bU = sdesc0(sb + OFF_U, 1024, 128), bUl = sdesc0(sb + OFF_U + 8192, 1024, 128);
-    const uint64_t aU = sdesc0(sb + OFF_U - 1024, 1024, 128), aUl = sdesc0(sb + OFF_U + 8192 - 1024, 1024, 128);   // rows 64..127
-    const uint64_t bS = sdesc0(sb + OFF_S, 2048, 128), bSl = sdesc0(sb + OFF_S + 16384, 2048, 128);
-    const uint64_t bDS = sdesc0(sb + OFF_DS, 2048, 128), bDSl = sdesc0(sb + OFF_DS + 16384, 2048, 128);
-    constexpr uint32_t id64 = idesc_bf16(128, 64, 0, 0), id128 = idesc_bf16(128, 128, 0, 0);
-    const int quarter = warp & 3, cg = warp >> 2, row = quarter * 32 + lane, tok = row & 63;
-    const bool up = quarter < 2;                   // rows 0..63: dq's side; 64..127: dk's
-    uint32_t tmem = 0;
-    float2 dot2 = make_float2(0.f, 0.f);           // <S, dS'>
-    float drv = 0.f;                               // dR . v
-    for (int sl = 0; sl < slices; ++sl) {
-        if (sl > 0) {
-            mbar_wait_flag(&m->done[2], (sl - 1) & 1, &m->abort_flag, status, 1);
-            // (a barrier that waits for the sums, so that all they read has been read)
-            __syncthreads_or(drv != drv && dot2.x != dot2.x);
-            load_slice(sl);
-        }
-        mbar_wait_flag(&m->full[0], sl & 1, &m->abort_flag, status, 5);
-        if (sl == 0 && nt < kC)
-            // Q and K rows behind the end must be zeros: the last products sum over all rows of the tiles
-            for (int e = tid; e < (kC - nt) * 32; e += kThreads) {
-                const int r = nt + (e >> 5), ch = e & 31;
-                put16(smem, OFF_QK + ((ch >> 3) & 1) * 16384, sw128(r + (ch >> 4) * 64, ch & 7), 16384, make_uint4(0u, 0u, 0u, 0u));
+        // all threads' copies of a group are in place and visible to the products
+        auto arrived = [&]() {
+            fence_async_smem();
+            tc_fence_before();
+            __syncthreads();
+            tc_fence_after();
+        };
+        const uint64_t aQK = sdesc(sb + OFF_QK, 16, 1024), bK = sdesc(sb + OFF_QK + 8192, 16, 1024);
+        const uint64_t aA = sdesc0(sb + OFF_A, 2048, 128), aA2 = sdesc0(sb + OFF_A2, 2048, 128);
+        const uint64_t bU = sdesc0(sb + OFF_U, 1024, 128), bUl = sdesc0(sb + OFF_U + 8192, 1024, 128);
+        const uint64_t aU = sdesc0(sb + OFF_U - 1024, 1024, 128), aUl = sdesc0(sb + OFF_U + 8192 - 1024, 1024, 128);   // rows 64..127
+        const uint64_t bS = sdesc0(sb + OFF_S, 2048, 128), bSl = sdesc0(sb + OFF_S + 16384, 2048, 128);
+        const uint64_t bDS = sdesc0(sb + OFF_DS, 2048, 128), bDSl = sdesc0(sb + OFF_DS + 16384, 2048, 128);
+        constexpr uint32_t id64 = idesc_bf16(128, 64, 0, 0), id128 = idesc_bf16(128, 128, 0, 0);
+        const int quarter = warp & 3, cg = warp >> 2, row = quarter * 32 + lane, tok = row & 63;
+        const bool up = quarter < 2;                   // rows 0..63: dq's side; 64..127: dk's
+        const uint32_t tmem = m->tmem_base;
+        float2 dot2 = make_float2(0.f, 0.f);           // <S, dS'>
+        float drv = 0.f;                               // dR . v
+        for (int sl = 0; sl < slices; ++sl) {
+            if (sl > 0) {
+                mbar_wait_flag(&m->done[2], (done_y - 1) & 1, &m->abort_flag, status, 1);
+                // (a barrier that waits for the sums, so that all they read has been read)
+                __syncthreads_or(drv != drv && dot2.x != dot2.x);
+                if (tid == 0 && !m->abort_flag) load_records(n, sl);
+                __syncwarp();
+                dy = fetch_dy(me, sl);
             }
-        arrived();
-        tmem = m->tmem_base;
-        if (warp == 0) {
-            if (sl == 0)
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    umma_one(tmem + D_QK, aQK + (kk >> 2) * 1024 + (kk & 3) * 2, bK + (kk >> 2) * 1024 + (kk & 3) * 2, id64, kk > 0);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_PA, aA + kk * 256, bU + kk * 128, id64, sl + kk > 0);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_PA, aA + kk * 256, bUl + kk * 128, id64, 1);
-        }
-        mbar_wait_flag(&m->full[1], sl & 1, &m->abort_flag, status, 6);
-        if (warp == 0) {
-            __syncwarp();
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_PA, aA2 + kk * 256, bU + kk * 128, id64, 1);
-            if (sl == slices - 1) commit_one(&m->done[0]);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_ZX, aA + kk * 256, bS + kk * 256, id128, sl + kk > 0);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_ZX, aA + kk * 256, bSl + kk * 256, id128, 1);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_ZX, aA2 + kk * 256, bS + kk * 256, id128, 1);
-        }
-        if (!up) {                                 // dR . v: 16 of the slice's columns
+            put16(smem, OFF_A, (tid & 7) * 2048 + (tid >> 3) * 16, 16384, dy);
+            // V for dR . v: 16 of the slice's columns
+            uint4 vv[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int p = 2 * cg + j;
-                const size_t vo = ((row0 + tok) * H + h) * P + 64 * sl + 8 * p;
-                float v[8], r[8], l[8];
-                unpack8(tok < nt && M3_SPAN(8, vo, 8, ext_v) ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(q.v) + vo))
-                                                             : make_uint4(0u, 0u, 0u, 0u), v);
-                unpack8(*reinterpret_cast<const uint4*>(smem + OFF_A + p * 2048 + row * 16), r);
-                unpack8(*reinterpret_cast<const uint4*>(smem + OFF_A2 + p * 2048 + row * 16), l);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) drv = fmaf(r[e] + l[e], v[e], drv);
+                const size_t vo = ((row0 + tok) * H + h) * P + 64 * sl + 8 * (2 * cg + j);
+                vv[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (!up && tok < nt && M3_SPAN(8, vo, 8, ext_v))
+                    vv[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(q.v) + vo));
             }
+            if (sl == 0) {
+                mbar_wait_flag(&m->full[3], done_c & 1, &m->abort_flag, status, 8);
+                if (nt < kC)
+                    // Q and K rows behind the end must be zeros: the last products sum over all rows of the tiles
+                    for (int e = tid; e < (kC - nt) * 32; e += kThreads) {
+                        const int r = nt + (e >> 5), ch = e & 31;
+                        put16(smem, OFF_QK + ((ch >> 3) & 1) * 16384, sw128(r + (ch >> 4) * 64, ch & 7), 16384,
+                              make_uint4(0u, 0u, 0u, 0u));
+                    }
+            }
+            mbar_wait_flag(&m->full[0], fph & 1, &m->abort_flag, status, 5);
+            arrived();
+            if (warp == 0) {
+                if (sl == 0)
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_one(tmem + D_QK, aQK + (kk >> 2) * 1024 + (kk & 3) * 2, bK + (kk >> 2) * 1024 + (kk & 3) * 2, id64,
+                                 kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_PA, aA + kk * 256, bU + kk * 128, id64, sl + kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_PA, aA + kk * 256, bUl + kk * 128, id64, 1);
+            }
+            mbar_wait_flag(&m->full[1], fph & 1, &m->abort_flag, status, 6);
+            if (warp == 0) {
+                __syncwarp();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_PA, aA2 + kk * 256, bU + kk * 128, id64, 1);
+                if (sl == slices - 1) commit_one(&m->done[0]);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_ZX, aA + kk * 256, bS + kk * 256, id128, sl + kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_ZX, aA + kk * 256, bSl + kk * 256, id128, 1);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_ZX, aA2 + kk * 256, bS + kk * 256, id128, 1);
+            }
+            if (!up) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int p = 2 * cg + j;
+                    float v[8], r[8], l[8];
+                    unpack8(vv[j], v);
+                    unpack8(*reinterpret_cast<const uint4*>(smem + OFF_A + p * 2048 + row * 16), r);
+                    unpack8(*reinterpret_cast<const uint4*>(smem + OFF_A2 + p * 2048 + row * 16), l);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) drv = fmaf(r[e] + l[e], v[e], drv);
+                }
+            }
+            mbar_wait_flag(&m->full[2], fph & 1, &m->abort_flag, status, 7);
+            if (warp == 0) {
+                __syncwarp();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_Y, aU + kk * 128, bDS + kk * 256, id128, sl + kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_Y, aU + kk * 128, bDSl + kk * 256, id128, 1);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_Y, aUl + kk * 128, bDS + kk * 256, id128, 1);
+                commit_one(&m->done[2]);
+            }
+#pragma unroll
+            for (int e = tid; e < 1024; e += kThreads) {
+                const uint4 s0 = *reinterpret_cast<const uint4*>(smem + OFF_S + e * 16);
+                const uint4 s1 = *reinterpret_cast<const uint4*>(smem + OFF_S + 16384 + e * 16);
+                const uint4 d0 = *reinterpret_cast<const uint4*>(smem + OFF_DS + e * 16);
+                const uint4 d1 = *reinterpret_cast<const uint4*>(smem + OFF_DS + 16384 + e * 16);
+                const uint32_t a0[4] = {s0.x, s0.y, s0.z, s0.w}, a1[4] = {s1.x, s1.y, s1.z, s1.w};
+                const uint32_t b0[4] = {d0.x, d0.y, d0.z, d0.w}, b1[4] = {d1.x, d1.y, d1.z, d1.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    dot2 = __ffma2_rn(__fadd2_rn(unpack(a0[j]), unpack(a1[j])), __fadd2_rn(unpack(b0[j]), unpack(b1[j])), dot2);
+            }
+            ++fph;
+            ++done_y;
         }
-        mbar_wait_flag(&m->full[2], sl & 1, &m->abort_flag, status, 7);
-        if (warp == 0) {
-            __syncwarp();
+        float dot = dot2.x + dot2.y;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_Y, aU + kk * 128, bDS + kk * 256, id128, sl + kk > 0);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_Y, aU + kk * 128, bDSl + kk * 256, id128, 1);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_Y, aUl + kk * 128, bDS + kk * 256, id128, 1);
-            commit_one(&m->done[2]);
-        }
-#pragma unroll
-        for (int e = tid; e < 1024; e += kThreads) {
-            const uint4 s0 = *reinterpret_cast<const uint4*>(smem + OFF_S + e * 16), s1 = *reinterpret_cast<const uint4*>(smem + OFF_S + 16384 + e * 16);
-            const uint4 d0 = *reinterpret_cast<const uint4*>(smem + OFF_DS + e * 16), d1 = *reinterpret_cast<const uint4*>(smem + OFF_DS + 16384 + e * 16);
-            const uint32_t a0[4] = {s0.x, s0.y, s0.z, s0.w}, a1[4] = {s1.x, s1.y, s1.z, s1.w};
-            const uint32_t b0[4] = {d0.x, d0.y, d0.z, d0.w}, b1[4] = {d1.x, d1.y, d1.z, d1.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                dot2 = __ffma2_rn(__fadd2_rn(unpack(a0[j]), unpack(a1[j])), __fadd2_rn(unpack(b0[j]), unpack(b1[j])), dot2);
-        }
-    }
-    float dot = dot2.x + dot2.y;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-    if (lane == 0) m->dot[warp] = dot;
-    if (!up) m->drv[cg][tok] = drv;
+        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+        if (lane == 0) m->dot[warp] = dot;
+        if (!up) m->drv[cg][tok] = drv;
 
-    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
-    const Gates* gt = &m->gates;
-    const float2 Gi = gt->G[tok];
-    const float a = gt->a[tok], at = gt->at[tok], be = gt->beta[tok], sa = q.scale * a, ba = be * a;
-    const bool live = tok < nt;
-    float rowG = 0.f, rowB = 0.f, tail = 0.f;
-    mbar_wait_flag(&m->done[0], 0, &m->abort_flag, status, 2);
-    __syncwarp();
-    tc_fence_after();
-    if (16 * cg > (tok | 31)) {                    // right of the diagonal for all of the warp
-        put16(smem, OFF_D, sw128(row, 2 * cg), 16384, make_uint4(0u, 0u, 0u, 0u));
-        put16(smem, OFF_D, sw128(row, 2 * cg + 1), 16384, make_uint4(0u, 0u, 0u, 0u));
-        if (lane < 16) m->col[quarter][16 * cg + lane] = 0.f;
-    } else {
-        // 16 columns: up, scale Gam o dP (dP of rows behind the end is that of zero rows of dY);
-        // down, D, and each side's part of E
-        float d[16], s[16], e[16];
-        tmem_ld16x2(tl + D_PA + 16 * cg, tl + D_QK + 16 * cg, d, s);
-        float2 f[8];
-#pragma unroll
-        for (int k2 = 0; k2 < 8; ++k2) {
-            const int j = 16 * cg + 2 * k2;
-            const float4 Gj = *reinterpret_cast<const float4*>(&gt->G[j]);
-            float v[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int k = 2 * k2 + x;
-                const float2 gj = x ? make_float2(Gj.z, Gj.w) : make_float2(Gj.x, Gj.y);
-                const bool in = live && (up ? j + x <= tok : j + x < tok);
-                const float gam = in ? ex2(diff_pair(Gi, gj)) : 0.f;
-                const float t = in ? d[k] * gam : 0.f;             // Gam o dP, or - Gam o dA
-                const float ts = in ? t * s[k] : 0.f;
-                if (up) {
-                    e[k] = q.scale * ts;
-                    v[x] = q.scale * t;
-                } else {
-                    rowB -= ts;
-                    e[k] = -be * ts;
-                    v[x] = -be * t;
-                }
-                rowG += e[k];
-            }
-            f[k2] = make_float2(v[0], v[1]);
-        }
-        put16(smem, OFF_D, sw128(row, 2 * cg), 16384, round8(f));
-        put16(smem, OFF_D, sw128(row, 2 * cg + 1), 16384, round8(f + 4));
-        const float cs = column_sums(e);
-        if (lane < 16) m->col[quarter][16 * cg + lane] = cs;
-    }
-    arrived();
-    if (warp == 0) {
-        const uint64_t aD = sdesc(sb + OFF_D, 16, 1024), aDT = sdesc(sb + OFF_D - 8192, 8192, 1024);   // second atom: rows 64..127
-        const uint64_t mK = sdesc(sb + OFF_QK + 8192, 16384, 1024), mQ = sdesc(sb + OFF_QK, 16384, 1024);
-        constexpr uint32_t idL = idesc_bf16(128, 128, 0, 1), idT = idesc_bf16(128, 128, 1, 1);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_LAST, aD + kk * 2, mK + kk * 128, idL, kk > 0);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_T, aDT + kk * 128, mQ + kk * 128, idT, kk > 0);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_T, aDT + 512 + kk * 128, mK + kk * 128, idT, 1);
-        commit_one(&m->done[1]);
-    }
-    // 32 columns of Z (up) or X and Y (down)
-    mbar_wait_flag(&m->done[2], (slices - 1) & 1, &m->abort_flag, status, 3);
-    __syncwarp();
-    tc_fence_after();
-    float r[32];
-    tmem_ld32(tl + D_ZX + 32 * cg, r);
-    {
-        float t0 = 0.f, t1 = 0.f;
-        float y[32];
-        if (!up) tmem_ld32(tl + D_Y + 32 * cg, y);
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-            const int col8 = 4 * cg + ch;
-            float k[8];
-            unpack8(*reinterpret_cast<const uint4*>(smem + OFF_QK + (col8 >> 3) * 16384 + sw128(row, col8 & 7)), k);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                t0 = fmaf(r[8 * ch + j], k[j], t0);
-                if (up) {
-                    r[8 * ch + j] *= sa;
-                } else {
-                    t1 = fmaf(y[8 * ch + j], k[j], t1);
-                    r[8 * ch + j] = fmaf(at, y[8 * ch + j], -ba * r[8 * ch + j]);
-                }
-            }
-        }
-        if (up) {
-            rowG += sa * t0;
+        const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+        const Gates* gt = &m->gates[par];
+        const float2 Gi = gt->G[tok];
+        const float a = gt->a[tok], at = gt->at[tok], be = gt->beta[tok], sa = q.scale * a, ba = be * a;
+        const bool live = tok < nt;
+        float rowG = 0.f, rowB = 0.f, tail = 0.f;
+        mbar_wait_flag(&m->done[0], done_c & 1, &m->abort_flag, status, 2);
+        __syncwarp();
+        tc_fence_after();
+        if (16 * cg > (tok | 31)) {                    // right of the diagonal for all of the warp
+            put16(smem, OFF_D, sw128(row, 2 * cg), 16384, make_uint4(0u, 0u, 0u, 0u));
+            put16(smem, OFF_D, sw128(row, 2 * cg + 1), 16384, make_uint4(0u, 0u, 0u, 0u));
+            if (lane < 16) m->col[quarter][16 * cg + lane] = 0.f;
         } else {
-            rowG += -ba * t0 - at * t1;
-            rowB -= a * t0;
-            tail = at * t1;
-        }
-    }
-    m->row[cg][row] = rowG;
-    if (!up) {
-        m->beta[cg][tok] = rowB;
-        m->tail[cg][tok] = tail;
-    }
-    mbar_wait_flag(&m->done[1], 0, &m->abort_flag, status, 4);
-    __syncwarp();
-    tc_fence_after();
-    {
-        float l[32];
-        tmem_ld32(tl + D_LAST + 32 * cg, l);
+            // 16 columns: up, scale Gam o dP (dP of rows behind the end is that of zero rows of dY);
+            // down, D, and each side's part of E
+            float d[16], s[16], e[16];
+            tmem_ld16x2(tl + D_PA + 16 * cg, tl + D_QK + 16 * cg, d, s);
+            float2 f[8];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) r[j] += l[j];
+            for (int k2 = 0; k2 < 8; ++k2) {
+                const int j = 16 * cg + 2 * k2;
+                const float4 Gj = *reinterpret_cast<const float4*>(&gt->G[j]);
+                float v[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int k = 2 * k2 + x;
+                    const float2 gj = x ? make_float2(Gj.z, Gj.w) : make_float2(Gj.x, Gj.y);
+                    const bool in = live && (up ? j + x <= tok : j + x < tok);
+                    const float gam = in ? ex2(diff_pair(Gi, gj)) : 0.f;
+                    const float t = in ? d[k] * gam : 0.f;             // Gam o dP, or - Gam o dA
+                    const float ts = in ? t * s[k] : 0.f;
+                    if (up) {
+                        e[k] = q.scale * ts;
+                        v[x] = q.scale * t;
+                    } else {
+                        rowB -= ts;
+                        e[k] = -be * ts;
+                        v[x] = -be * t;
+                    }
+                    rowG += e[k];
+                }
+                f[k2] = make_float2(v[0], v[1]);
+            }
+            put16(smem, OFF_D, sw128(row, 2 * cg), 16384, round8(f));
+            put16(smem, OFF_D, sw128(row, 2 * cg + 1), 16384, round8(f + 4));
+            const float cs = column_sums(e);
+            if (lane < 16) m->col[quarter][16 * cg + lane] = cs;
+        }
+        arrived();
+        if (warp == 0) {
+            const uint64_t aD = sdesc(sb + OFF_D, 16, 1024), aDT = sdesc(sb + OFF_D - 8192, 8192, 1024);   // second atom: rows 64..127
+            const uint64_t mK = sdesc(sb + OFF_QK + 8192, 16384, 1024), mQ = sdesc(sb + OFF_QK, 16384, 1024);
+            constexpr uint32_t idL = idesc_bf16(128, 128, 0, 1), idT = idesc_bf16(128, 128, 1, 1);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_LAST, aD + kk * 2, mK + kk * 128, idL, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_T, aDT + kk * 128, mQ + kk * 128, idT, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_T, aDT + 512 + kk * 128, mK + kk * 128, idT, 1);
+            commit_one(&m->done[1]);
+        }
+        // 32 columns of Z (up) or X and Y (down)
+        mbar_wait_flag(&m->done[2], (done_y - 1) & 1, &m->abort_flag, status, 3);
+        __syncwarp();
+        tc_fence_after();
+        // the next chunk's matrices: the products and (before the barrier above) the
+        // sums that read their places are done
+        loaded = false;
+        if ((long long)n + gridDim.x < total_chunks) {
+            const At t = locate(n + gridDim.x);
+            if (t.nt > 0) {
+                if (tid == 0 && !m->abort_flag) load_records(n + gridDim.x, 0);
+                __syncwarp();
+                dy = fetch_dy(t, 0);
+                loaded = true;
+            }
+        }
+        float r[32];
+        tmem_ld32(tl + D_ZX + 32 * cg, r);
+        {
+            float t0 = 0.f, t1 = 0.f;
+            float y[32];
+            if (!up) tmem_ld32(tl + D_Y + 32 * cg, y);
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+                const int col8 = 4 * cg + ch;
+                float k[8];
+                unpack8(*reinterpret_cast<const uint4*>(smem + OFF_QK + (col8 >> 3) * 16384 + sw128(row, col8 & 7)), k);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    t0 = fmaf(r[8 * ch + j], k[j], t0);
+                    if (up) {
+                        r[8 * ch + j] *= sa;
+                    } else {
+                        t1 = fmaf(y[8 * ch + j], k[j], t1);
+                        r[8 * ch + j] = fmaf(at, y[8 * ch + j], -ba * r[8 * ch + j]);
+                    }
+                }
+            }
+            if (up) {
+                rowG += sa * t0;
+            } else {
+                rowG += -ba * t0 - at * t1;
+                rowB -= a * t0;
+                tail = at * t1;
+            }
+        }
+        m->row[cg][row] = rowG;
         if (!up) {
-            tmem_ld32(tl + D_T + 32 * cg, l);
+            m->beta[cg][tok] = rowB;
+            m->tail[cg][tok] = tail;
+        }
+        mbar_wait_flag(&m->done[1], done_c & 1, &m->abort_flag, status, 4);
+        __syncwarp();
+        tc_fence_after();
+        {
+            float l[32];
+            tmem_ld32(tl + D_LAST + 32 * cg, l);
 #pragma unroll
             for (int j = 0; j < 32; ++j) r[j] += l[j];
-        }
-        if (tok < rows) {
-            if (!live)
+            if (!up) {
+                tmem_ld32(tl + D_T + 32 * cg, l);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = 0.f;
-            if (hpg == 1) {
-                const size_t o = ((row0 + tok) * q.ngroups + g) * kN + 32 * cg;
-                if (M3_SPAN(10, o, 32, ext_k)) {
-                    uint4* dst = reinterpret_cast<uint4*>((up ? out_q : out_k) + o);
+                for (int j = 0; j < 32; ++j) r[j] += l[j];
+            }
+            if (tok < rows) {
+                if (!live)
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) dst[ch] = pack_chunk(r + 8 * ch);
-                }
-            } else {
-                const size_t o = (((row0 + tok) * H + h) * 2 + (up ? 0 : 1)) * kN + 32 * cg;
-                if (M3_SPAN(11, o, 32, toks * 2 * kN)) {
-                    float4* dst = reinterpret_cast<float4*>(q.part_qk + o);
+                    for (int j = 0; j < 32; ++j) r[j] = 0.f;
+                if (hpg == 1) {
+                    const size_t o = ((row0 + tok) * q.ngroups + g) * kN + 32 * cg;
+                    if (M3_SPAN(10, o, 32, ext_k)) {
+                        uint4* dst = reinterpret_cast<uint4*>((up ? out_q : out_k) + o);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) dst[j] = make_float4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                        for (int ch = 0; ch < 4; ++ch) dst[ch] = pack_chunk(r + 8 * ch);
+                    }
+                } else {
+                    const size_t o = (((row0 + tok) * H + h) * 2 + (up ? 0 : 1)) * kN + 32 * cg;
+                    if (M3_SPAN(11, o, 32, toks * 2 * kN)) {
+                        float4* dst = reinterpret_cast<float4*>(q.part_qk + o);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) dst[j] = make_float4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                    }
                 }
             }
         }
+        tc_fence_before();
+        stop = __syncthreads_or(m->abort_flag);
+        tc_fence_after();
+        ++done_c;
+        par ^= 1;
+        if (warp == 0) {
+            // lane l has tokens 2 l, 2 l + 1; dg is the sum from a token to the chunk's end
+            float d[2], tl2 = 0.f, total = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                d[e] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    d[e] += m->row[j][i] + m->row[j][64 + i] - m->col[j][i];
+                    tl2 += m->tail[j][i];
+                }
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) tl2 += __shfl_xor_sync(kFull, tl2, o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) total += m->dot[j];
+            tl2 += gt->whole * total;
+            float sum = d[0] + d[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float u = __shfl_down_sync(kFull, sum, o);
+                if (lane + o < 32) sum += u;
+            }
+            const float dg[2] = {sum + tl2, sum - d[0] + tl2};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                const size_t o = (row0 + i) * H + h;
+                if (i >= rows || !M3_IN(12, o, toks)) continue;
+                float vb = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) vb += m->drv[j][i] + m->beta[j][i];
+                const float vg = i < nt ? dg[e] : 0.f;
+                vb = i < nt ? vb : 0.f;
+                if (hpg == 1) {
+                    if (out_g) out_g[o] = __float2bfloat16_rn(vg);
+                    out_b[o] = __float2bfloat16_rn(vb);
+                } else {
+                    q.part_g[2 * o] = vg;
+                    q.part_g[2 * o + 1] = vb;
+                }
+            }
+        }
+    }
+    if (stop && warp == 0) {                       // a wait ran out: what is still on its way has a second to end
+        commit_one(&m->drain);
+        mbar_wait_flag(&m->drain, 0, &m->drain_flag, nullptr, 0);
+        if (tid == 0) {
+            for (int i = 0; i < 3; ++i) mbar_wait_flag(&m->full[i], (asked - 1) & 1, &m->drain_flag, nullptr, 0);
+            mbar_wait_flag(&m->full[3], (done_c - 1) & 1, &m->drain_flag, nullptr, 0);
+        }
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
-        // (the last commit follows all products; after an expired wait this lets them end)
-        mbar_wait_flag(&m->done[1], 0, &m->drain_flag, nullptr, 0);
-        __syncwarp();
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
-        // lane l has tokens 2 l, 2 l + 1; dg is the sum from a token to the chunk's end
-        float d[2], tl2 = 0.f, total = 0.f;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = 2 * lane + e;
-            d[e] = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                d[e] += m->row[j][i] + m->row[j][64 + i] - m->col[j][i];
-                tl2 += m->tail[j][i];
-            }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) tl2 += __shfl_xor_sync(kFull, tl2, o);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) total += m->dot[j];
-        tl2 += gt->whole * total;
-        float sum = d[0] + d[1];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float u = __shfl_down_sync(kFull, sum, o);
-            if (lane + o < 32) sum += u;
-        }
-        const float dg[2] = {sum + tl2, sum - d[0] + tl2};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = 2 * lane + e;
-            const size_t o = (row0 + i) * H + h;
-            if (i >= rows || !M3_IN(12, o, toks)) continue;
-            float vb = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) vb += m->drv[j][i] + m->beta[j][i];
-            const float vg = i < nt ? dg[e] : 0.f;
-            vb = i < nt ? vb : 0.f;
-            if (hpg == 1) {
-                if (out_g) out_g[o] = __float2bfloat16_rn(vg);
-                out_b[o] = __float2bfloat16_rn(vb);
-            } else {
-                q.part_g[2 * o] = vg;
-                q.part_g[2 * o + 1] = vb;
-            }
-        }
-    }
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(m->tmem_base, 512);
 }
 
 }  // namespace dbw
@@ -520,8 +589,8 @@ cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* sta
     if (!make_tile_map(&mK, q.k, kN, 1, d.ngroups, d.seqlen, d.batch, kC) ||
         !make_tile_map(&mQ, q.q, kN, 1, d.ngroups, d.seqlen, d.batch, kC))
         return cudaErrorInvalidValue;
-    delta_grad_kernel<<<(unsigned)((long long)d.batch * d.nheads * q.nck), kThreads, SMEM_BYTES, st>>>(
-        mK, mQ, q, q.nck, device_sm_count(), status);
+    const long long total = (long long)d.batch * d.nheads * q.nck, sms = device_sm_count();
+    delta_grad_kernel<<<(unsigned)(total < sms ? total : sms), kThreads, SMEM_BYTES, st>>>(mK, mQ, q, (int)total, status);
     e = cudaGetLastError();
     if (e != cudaSuccess || d.nheads == d.ngroups) return e;
     return launch_delta_reduce(d, q, 1, st);
