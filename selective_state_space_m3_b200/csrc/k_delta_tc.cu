@@ -27,8 +27,8 @@
 // chain keeps float32: S, R, U and T are split into bfloat16 parts (hi + lo, 16
 // to 17 bits; the state's update of S takes three parts), the products of the
 // parts add up in the float32 accumulators, and the identity of T is left out
-// of the product and added in registers.  Only P and the U that it meets
-// are rounded to bfloat16, since y is.
+// of the product and added in registers.  P alone is rounded to bfloat16 (half a
+// step of 2^-8 relative, as y itself is); the U that it meets has two parts.
 //
 // Shared memory (KB): K, Q 3 x 32, [T - I; P] 3 x 16, T lo 3 x 8, V 2 x 8, S hi/lo
 // 32 (R and U take its place between the first product's end and the new state):
@@ -58,17 +58,17 @@ constexpr int OFF_X = OFF_KQ + 3 * 32768;       // 3 x 24 KB: [T - I hi; P], T -
 constexpr int kXBytes = 24576;
 constexpr int OFF_S = OFF_X + 3 * kXBytes;      // S hi, S lo (16 KB each: rows n, 64 p)
 constexpr int OFF_U = OFF_S;                    // R hi, lo; then e^{G_C-G} U in three parts (8 KB each: rows t, 64 p)
-constexpr int OFF_V = OFF_S + 32768;            // 2 x 8 KB; U rounded, for P U, takes V's place
+constexpr int OFF_V = OFF_S + 32768;            // 2 x 8 KB; U hi (and lo beside it, for PC = 64 in T lo's place) for P U takes V's place
 constexpr int OFF_GATES = OFF_V + 2 * 8192;     // 3 x 1 KB
 constexpr int OFF_MISC = OFF_GATES + 3 * (int)sizeof(ChainGates);
 
 // TMEM columns: K S, Q S against [S hi | S lo] and, once they are read, the
-// state's update in three parts; T R against [R hi | R lo] and, once read, P U
-constexpr uint32_t D_KS = 0, D_S = 0, D_TR = 192;
+// state's update in three parts; T R against [R hi | R lo]; P U against [U hi | U lo]
+constexpr uint32_t D_KS = 0, D_S = 0, D_TR = 192, D_O = 320;
 
 struct Misc {
     uint64_t full[3], freed[3], v_full[2], v_free[2];
-    uint64_t s_ready, ks, r, tr, u, s, o, drain;
+    uint64_t s_ready, ks, r, tr, u, ub, s, o, drain;
     uint32_t tmem_base;
     int abort_flag, drain_flag, pad;
 };
@@ -102,9 +102,10 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
         mbar_init(&m->drain, 1);
         mbar_init(&m->s_ready, kState<PC>);
         mbar_init(&m->ks, 1);
-        mbar_init(&m->r, kState<PC>);
+        mbar_init(&m->r, kState<PC> / 2);
         mbar_init(&m->tr, 1);
         mbar_init(&m->u, kState<PC>);
+        mbar_init(&m->ub, kState<PC> / 2);
         mbar_init(&m->s, 1);
         mbar_init(&m->o, 1);
         m->abort_flag = 0;
@@ -132,7 +133,9 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
         for (int c = 0; c < w.nch; ++c) {
             const uint32_t kq = sbase + OFF_KQ + (c % 3) * 32768;
             const uint64_t aKQ = sdesc(kq, 16, 1024), aKT = sdesc(kq, 16384, 1024);
-            const uint64_t bUB = sdesc(sbase + OFF_V + (c & 1) * 8192, 8192, 1024);
+            // (PC = 64: the lo part first, the hi part that many bytes behind it)
+            const uint32_t hi = OFF_V + (c & 1) * 8192, lo = OFF_X + (c % 3) * kXBytes + 16384;
+            const uint64_t bUB = PC == 64 ? sdesc(sbase + lo, hi - lo, 1024) : sdesc(sbase + hi, 8192, 1024);
             const uint64_t aX = sdesc(sbase + OFF_X + (c % 3) * kXBytes, 16, 1024);
             const uint64_t aTL = sdesc(sbase + OFF_X + (c % 3) * kXBytes + 16384, 16, 1024);
             wait(&m->full[c % 3], c / 3, m, status, 1);
@@ -157,9 +160,14 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_S, aKT + kk * 128, bU + kk * 128, idS, kk > 0);
             commit_one(&m->s);
+            if (!DUMP) {
+                wait(&m->ub, c, m, status, 7);
+                __syncwarp();
+                tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_TR + PC, aX + kk * 2, bUB + kk * 128, idTl, kk > 0);
-            commit_one(&m->o);
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_O, aX + kk * 2, bUB + kk * 128, idKS, kk > 0);
+                commit_one(&m->o);
+            }
             commit_one(&m->v_free[c & 1]);
             commit_one(&m->freed[c % 3]);
         }
@@ -279,11 +287,8 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
 #pragma unroll
                     for (int ch = 0; ch < W / 8; ++ch) {
                         const int cc = ch0 + W / 8 * hh + ch;
-                        put16(smem, OFF_V + (c & 1) * 8192, sw128(tok, cc), 8192, round8(f + 4 * ch));
-                        if (DUMP) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) buf[W / 2 * hh + 4 * ch + j] = f[4 * ch + j];
-                        }
+                        for (int j = 0; j < 4; ++j) buf[W / 2 * hh + 4 * ch + j] = f[4 * ch + j];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) f[4 * ch + j] = __fmul2_rn(at2, f[4 * ch + j]);
                         put16(smem, OFF_U, part_at<PC>(tok, 0, cc, 8192), 24576, take8(f + 4 * ch));
@@ -294,17 +299,25 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
                 fence_async_smem();
                 tc_fence_before();
                 arrive_after(&m->u, __float_as_uint(whole));
-                if (DUMP) {
+                // U's parts for P U, while the state's update is made
 #pragma unroll
-                    for (int ch = 0; ch < NG; ++ch) {
-                        keep(c, kSliceU, 64, tok, ch, take8(buf + 4 * ch));
-                        keep(c, kSliceU + kTok, 64, tok, ch, round8(buf + 4 * ch));
+                for (int ch = 0; ch < NG; ++ch) {
+                    const uint4 hi = take8(buf + 4 * ch), lo = round8(buf + 4 * ch);
+                    if (DUMP) {
+                        keep(c, kSliceU, 64, tok, ch, hi);
+                        keep(c, kSliceU + kTok, 64, tok, ch, lo);
+                    } else {
+                        put16(smem, OFF_V + (c & 1) * 8192, sw128(tok, ch0 + ch), 8192, hi);
+                        if (PC == 64) put16(smem, OFF_X + (c % 3) * kXBytes + 16384, sw128(tok, ch0 + ch), 8192, lo);
+                        else put16(smem, OFF_V + (c & 1) * 8192, part_at<PC>(tok, 1, ch0 + ch, 8192), 8192, lo);
                     }
+                }
+                if (!DUMP) {
+                    fence_async_smem();
+                    mbar_arrive(&m->ub);
                 }
                 if (c + 1 < w.nch) load_v(c + 1);  // while the state's update is made
             } else {
-                tc_fence_before();
-                mbar_arrive(&m->r);                // the previous chunk's P U has been read
                 wait(&m->full[c % 3], c / 3, m, status, 14);
                 const float a = gt->a[tok];
                 whole = gt->whole;
@@ -344,7 +357,7 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
                 for (int j = 0; j < W / 2; ++j) S[W / 2 * hh + j] = __ffma2_rn(w2, S[W / 2 * hh + j], d[j]);
             }
             if (c + 1 < w.nch) store_state(c + 1);
-            if (!top) {
+            if (!DUMP && !top) {
                 wait(&m->o, c, m, status, 17);
                 __syncwarp();
                 tc_fence_after();
@@ -354,10 +367,10 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
 #pragma unroll
                 for (int hh = 0; hh < NH; ++hh) {
                     float2 f[W / 2];
-                    tmem_sum<W, 1>(tl + D_TR + PC + W * hh, PC, f);
+                    tmem_sum<W, 2>(tl + D_O + W * hh, PC, f);
 #pragma unroll
                     for (int j = 0; j < W / 2; ++j) f[j] = __fadd2_rn(buf[W / 2 * hh + j], f[j]);
-                    if (!DUMP && in) {
+                    if (in) {
 #pragma unroll
                         for (int ch = 0; ch < W / 8; ++ch) dst[W / 8 * hh + ch] = round8(f + 4 * ch);
                     }
