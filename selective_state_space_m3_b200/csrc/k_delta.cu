@@ -520,7 +520,7 @@ cudaError_t launch_delta_seq(const m3_dims& d, const DeltaParams& q, cudaStream_
     return d.io_dtype == M3_BF16 ? delta::seq<__nv_bfloat16>(q, grid, st) : delta::seq<float>(q, grid, st);
 }
 
-cudaError_t launch_delta_reduce(const m3_dims& d, const DeltaParams& q, int tiles, cudaStream_t st) {
+static cudaError_t launch_delta_reduce(const m3_dims& d, const DeltaParams& q, int tiles, cudaStream_t st) {
     const unsigned rows = (unsigned)((long long)d.batch * d.seqlen * d.ngroups);
     if (d.io_dtype == M3_BF16) delta::delta_reduce_kernel<__nv_bfloat16><<<rows, delta::kThreads, 0, st>>>(q, tiles);
     else delta::delta_reduce_kernel<float><<<rows, delta::kThreads, 0, st>>>(q, tiles);

@@ -9,9 +9,12 @@
 //   dQ  = scale e^G o Z + (scale Gam o dP) K
 //   dK  = (scale Gam o dP)^T Q + D K + D^T K + e^{G_C-G} o Y - beta e^G o X,   D = beta Gam o dA
 //   dbeta_i = dR_i . v_i - e^{G_i} k_i . X_i + sum_j dA_ij Gam_ij k_i.k_j
-//   dG_i = (rows - columns of E)_i + scale e^{G_i} q_i.Z_i - beta_i e^{G_i} k_i.X_i - e^{G_C-G_i} k_i.Y_i,
-//          E = dP o P + dA o A
+//   dG_i = q_i.dQ_i - k_i.dK_i + 2 k_i.(D K)_i - 2 beta_i e^{G_i} k_i.X_i
 //   dG_C += e^{G_C} <S, dS'> + sum_j e^{G_C-G_j} k_j.Y_j;    dg_t = sum_{i >= t} dG_i
+// (dG_i: e^{G_i} multiplies whatever q_i and the row of D meet, and divides what
+// k_i's other uses meet, so the sums of rows less columns of dP o P + dA o A and
+// the terms of Z, X and Y are the inner products of q and k with their gradients,
+// but for the sign of D K and X.)
 //
 // Three passes.  The prefill runs once more and records T, P, the state before
 // every chunk and U.  k_delta_rev.cu carries dS from the last chunk to the first
@@ -25,12 +28,10 @@
 // to a token in its row):
 //   [Q; K] K^T,  [dY; dR] U^T,  [dY; dR] S^T,  [.; U] dS'^T
 //   [scale Gam o dP; D] K,  [.; (scale Gam o dP)^T] Q + [.; D^T] K
-// All that feeds
-// dg and dbeta (sums with cancellation) keeps float32 values as two bfloat16
-// parts (hi + lo; a product of two split operands drops lo x lo); the last two
-// products take rounded left operands, for they end in dq and dk, which are
-// rounded too.  The records are stored in the layout that the products read
-// (8 columns a piece), so no matrix is rearranged.
+// Float32 values enter as two bfloat16 parts (hi + lo; a product of two split
+// operands drops lo x lo): dg and dbeta are sums with cancellation.  The records
+// are stored in the layout that the products read (8 columns a piece), so no
+// matrix is rearranged.
 //
 // Bound by the records' traffic (about 200 KB a chunk in and out of L2 and HBM);
 // loads arrive in three groups, in the order of their use.
@@ -58,15 +59,15 @@ constexpr int OFF_U = OFF_A2 + 16384;            // U hi, lo (8 KB each; pieces 
 constexpr int OFF_A = OFF_U + 16384;             // [dY; dR hi] (16 KB)
 constexpr int OFF_S = OFF_A + 16384;             // S hi, lo (16 KB each; pieces of 128 rows)
 constexpr int OFF_DS = OFF_S + 32768;            // dS' hi, lo
-constexpr int OFF_D = OFF_DS + 32768;            // [scale Gam o dP; D] (16 KB, sw128)
-constexpr int OFF_MISC = OFF_D + 16384;
+constexpr int OFF_D = OFF_DS + 32768;            // [scale Gam o dP; D] hi, lo (16 KB each, sw128)
+constexpr int OFF_OUT = OFF_D + 32768;           // dQ, dK on their way out (as Q, K)
+constexpr int OFF_MISC = OFF_OUT + 32768;
 // TMEM columns; the last product takes the place of the first two
 constexpr uint32_t D_PA = 0, D_QK = 64, D_ZX = 128, D_Y = 256, D_LAST = 384, D_T = 0;
 
 struct Misc {
     Gates gates[2];
-    float row[4][2 * kC], beta[4][kC], tail[4][kC];    // by column group (row: upper and lower rows' parts)
-    float col[4][kC];                                  // by row quarter (its 16 columns a group)
+    float row[4][2 * kC], beta[4][kC], tail[4][kC];    // by column group (row: dq's and dk's rows)
     float drv[4][kC], dot[16];
     uint64_t full[4], done[3], drain;
     uint32_t tmem_base;
@@ -93,26 +94,24 @@ __device__ __forceinline__ void unpack8(uint4 v, float* f) {
     }
 }
 
-// sums over a warp's 32 rows of 16 columns, one row a lane: lane l gets column l & 15
-__device__ __forceinline__ float column_sums(float* v) {
-    const int lane = threadIdx.x & 31;
+// part of a row's inner product: 8 columns
+__device__ __forceinline__ float dot8(const float* x, const float* y, float t) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] += __shfl_xor_sync(kFull, v[k], 16);
-#pragma unroll
-    for (int s = 8; s; s >>= 1)
-#pragma unroll
-        for (int k = 0; k < s; ++k) {
-            const bool up = lane & s;
-            const float give = up ? v[k] : v[k + s], own = up ? v[k + s] : v[k];
-            v[k] = own + __shfl_xor_sync(kFull, give, s);
-        }
-    return v[0];
+    for (int j = 0; j < 8; ++j) t = fmaf(x[j], y[j], t);
+    return t;
+}
+// a tile of shared memory into the tensor, rows behind its end left out
+__device__ __forceinline__ void tma_store_5d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3, int c4) {
+    asm volatile("cp.async.bulk.tensor.5d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5, %6}], [%1];"
+                 ::"l"((uint64_t)map), "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+                 : "memory");
 }
 
 // The CTAs (one an SM) walk the chunks; the records of a CTA's next chunk are on
 // their way while it finishes the present one.
 __global__ void __launch_bounds__(kThreads, 1)
-    delta_grad_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ, DeltaParams q,
+    delta_grad_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDQ, DeltaParams q,
                       int total_chunks, int* status) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (su32(smem_raw) & 1023u)) & 1023u);
@@ -201,10 +200,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4*>(out_k + o) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
-                if (tid < rows && M3_IN(4, (row0 + tid) * H + h, toks)) {
-                    if (out_g) out_g[(row0 + tid) * H + h] = __float2bfloat16_rn(0.f);
-                    out_b[(row0 + tid) * H + h] = __float2bfloat16_rn(0.f);
-                }
+            }
+            if (tid < rows && M3_IN(4, (row0 + tid) * H + h, toks)) {
+                if (out_g) out_g[(row0 + tid) * H + h] = __float2bfloat16_rn(0.f);
+                out_b[(row0 + tid) * H + h] = __float2bfloat16_rn(0.f);
             }
             continue;
         }
@@ -365,20 +364,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 Gi = gt->G[tok];
         const float a = gt->a[tok], at = gt->at[tok], be = gt->beta[tok], sa = q.scale * a, ba = be * a;
         const bool live = tok < nt;
-        float rowG = 0.f, rowB = 0.f, tail = 0.f;
+        float rowB = 0.f, tail = 0.f;
         mbar_wait_flag(&m->done[0], done_c & 1, &m->abort_flag, status, 2);
         __syncwarp();
         tc_fence_after();
+        // 16 columns: up, scale Gam o dP; down, D, and the rows' sums of dA o Gam o K K^T
         if (16 * cg > (tok | 31)) {                    // right of the diagonal for all of the warp
-            put16(smem, OFF_D, sw128(row, 2 * cg), 16384, make_uint4(0u, 0u, 0u, 0u));
-            put16(smem, OFF_D, sw128(row, 2 * cg + 1), 16384, make_uint4(0u, 0u, 0u, 0u));
-            if (lane < 16) m->col[quarter][16 * cg + lane] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                put16(smem, OFF_D + (j & 1) * 16384, sw128(row, 2 * cg + (j >> 1)), 16384, make_uint4(0u, 0u, 0u, 0u));
         } else {
-            // 16 columns: up, scale Gam o dP (dP of rows behind the end is that of zero rows of dY);
-            // down, D, and each side's part of E
-            float d[16], s[16], e[16];
-            tmem_ld16x2(tl + D_PA + 16 * cg, tl + D_QK + 16 * cg, d, s);
+            float d[16], s[16];
+            if (up) tmem_ld16(tl + D_PA + 16 * cg, d);
+            else tmem_ld16x2(tl + D_PA + 16 * cg, tl + D_QK + 16 * cg, d, s);
             float2 f[8];
+            const float f0 = up ? q.scale : -be;
 #pragma unroll
             for (int k2 = 0; k2 < 8; ++k2) {
                 const int j = 16 * cg + 2 * k2;
@@ -389,37 +389,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int k = 2 * k2 + x;
                     const float2 gj = x ? make_float2(Gj.z, Gj.w) : make_float2(Gj.x, Gj.y);
                     const bool in = live && (up ? j + x <= tok : j + x < tok);
-                    const float gam = in ? ex2(diff_pair(Gi, gj)) : 0.f;
-                    const float t = in ? d[k] * gam : 0.f;             // Gam o dP, or - Gam o dA
-                    const float ts = in ? t * s[k] : 0.f;
-                    if (up) {
-                        e[k] = q.scale * ts;
-                        v[x] = q.scale * t;
-                    } else {
-                        rowB -= ts;
-                        e[k] = -be * ts;
-                        v[x] = -be * t;
-                    }
-                    rowG += e[k];
+                    const float t = in ? d[k] * ex2(diff_pair(Gi, gj)) : 0.f;      // Gam o dP, or - Gam o dA
+                    if (!up) rowB -= in ? t * s[k] : 0.f;
+                    v[x] = f0 * t;
                 }
                 f[k2] = make_float2(v[0], v[1]);
             }
-            put16(smem, OFF_D, sw128(row, 2 * cg), 16384, round8(f));
-            put16(smem, OFF_D, sw128(row, 2 * cg + 1), 16384, round8(f + 4));
-            const float cs = column_sums(e);
-            if (lane < 16) m->col[quarter][16 * cg + lane] = cs;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                put16(smem, OFF_D, sw128(row, 2 * cg + j), 16384, take8(f + 4 * j));
+                put16(smem, OFF_D + 16384, sw128(row, 2 * cg + j), 16384, round8(f + 4 * j));
+            }
         }
+        // the last chunk's gradients have left their place in shared memory
+        if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
         arrived();
         if (warp == 0) {
             const uint64_t aD = sdesc(sb + OFF_D, 16, 1024), aDT = sdesc(sb + OFF_D - 8192, 8192, 1024);   // second atom: rows 64..127
             const uint64_t mK = sdesc(sb + OFF_QK + 8192, 16384, 1024), mQ = sdesc(sb + OFF_QK, 16384, 1024);
             constexpr uint32_t idL = idesc_bf16(128, 128, 0, 1), idT = idesc_bf16(128, 128, 1, 1);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_LAST, aD + kk * 2, mK + kk * 128, idL, kk > 0);
+            for (int x = 0; x < 2; ++x) {              // hi, lo
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_T, aDT + kk * 128, mQ + kk * 128, idT, kk > 0);
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_LAST, aD + x * 1024 + kk * 2, mK + kk * 128, idL, x + kk > 0);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_T, aDT + 512 + kk * 128, mK + kk * 128, idT, 1);
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_T, aDT + x * 1024 + kk * 128, mQ + kk * 128, idT, x + kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) umma_one(tmem + D_T, aDT + x * 1024 + 512 + kk * 128, mK + kk * 128, idT, 1);
+            }
             commit_one(&m->done[1]);
         }
         // 32 columns of Z (up) or X and Y (down)
@@ -438,38 +436,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 loaded = true;
             }
         }
-        float r[32];
+        auto own8 = [&](int ch, float* k) {            // 8 columns of q (up) or k (down)
+            const int col8 = 4 * cg + ch;
+            unpack8(*reinterpret_cast<const uint4*>(smem + OFF_QK + (col8 >> 3) * 16384 + sw128(row, col8 & 7)), k);
+        };
+        float r[32], rowG = 0.f;
         tmem_ld32(tl + D_ZX + 32 * cg, r);
-        {
-            float t0 = 0.f, t1 = 0.f;
-            float y[32];
-            if (!up) tmem_ld32(tl + D_Y + 32 * cg, y);
+        if (up) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] *= sa;
+        } else {
+            float y[32], t0 = 0.f, t1 = 0.f;
+            tmem_ld32(tl + D_Y + 32 * cg, y);
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch) {
-                const int col8 = 4 * cg + ch;
                 float k[8];
-                unpack8(*reinterpret_cast<const uint4*>(smem + OFF_QK + (col8 >> 3) * 16384 + sw128(row, col8 & 7)), k);
+                own8(ch, k);
+                t0 = dot8(r + 8 * ch, k, t0);
+                t1 = dot8(y + 8 * ch, k, t1);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    t0 = fmaf(r[8 * ch + j], k[j], t0);
-                    if (up) {
-                        r[8 * ch + j] *= sa;
-                    } else {
-                        t1 = fmaf(y[8 * ch + j], k[j], t1);
-                        r[8 * ch + j] = fmaf(at, y[8 * ch + j], -ba * r[8 * ch + j]);
-                    }
-                }
+                for (int j = 8 * ch; j < 8 * ch + 8; ++j) r[j] = fmaf(at, y[j], -ba * r[j]);
             }
-            if (up) {
-                rowG += sa * t0;
-            } else {
-                rowG += -ba * t0 - at * t1;
-                rowB -= a * t0;
-                tail = at * t1;
-            }
-        }
-        m->row[cg][row] = rowG;
-        if (!up) {
+            rowG = -2.f * ba * t0;
+            rowB -= a * t0;
+            tail = at * t1;
             m->beta[cg][tok] = rowB;
             m->tail[cg][tok] = tail;
         }
@@ -477,33 +467,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         tc_fence_after();
         {
-            float l[32];
+            float l[32], t0 = 0.f, t1 = 0.f;
             tmem_ld32(tl + D_LAST + 32 * cg, l);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] += l[j];
+            for (int ch = 0; ch < 4; ++ch) {
+                float k[8];
+                own8(ch, k);
+                if (!up) t1 = dot8(l + 8 * ch, k, t1);
+#pragma unroll
+                for (int j = 8 * ch; j < 8 * ch + 8; ++j) r[j] += l[j];
+                if (up) t0 = dot8(r + 8 * ch, k, t0);
+            }
             if (!up) {
                 tmem_ld32(tl + D_T + 32 * cg, l);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] += l[j];
+                for (int ch = 0; ch < 4; ++ch) {
+                    float k[8];
+                    own8(ch, k);
+#pragma unroll
+                    for (int j = 8 * ch; j < 8 * ch + 8; ++j) r[j] += l[j];
+                    t0 = dot8(r + 8 * ch, k, t0);
+                }
             }
-            if (tok < rows) {
-                if (!live)
+            rowG += up ? t0 : 2.f * t1 - t0;
+            m->row[cg][row] = rowG;
+            if (!live)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = 0.f;
-                if (hpg == 1) {
-                    const size_t o = ((row0 + tok) * q.ngroups + g) * kN + 32 * cg;
-                    if (M3_SPAN(10, o, 32, ext_k)) {
-                        uint4* dst = reinterpret_cast<uint4*>((up ? out_q : out_k) + o);
+                for (int j = 0; j < 32; ++j) r[j] = 0.f;
+            if (hpg == 1) {
 #pragma unroll
-                        for (int ch = 0; ch < 4; ++ch) dst[ch] = pack_chunk(r + 8 * ch);
-                    }
-                } else {
-                    const size_t o = (((row0 + tok) * H + h) * 2 + (up ? 0 : 1)) * kN + 32 * cg;
-                    if (M3_SPAN(11, o, 32, toks * 2 * kN)) {
-                        float4* dst = reinterpret_cast<float4*>(q.part_qk + o);
+                for (int ch = 0; ch < 4; ++ch) {
+                    const int col8 = 4 * cg + ch;
+                    put16(smem, OFF_OUT, (col8 >> 3) * 16384 + sw128(row, col8 & 7), 32768, pack_chunk(r + 8 * ch));
+                }
+                fence_async_smem();
+            } else {
+                // pieces of 4 columns, so that a warp writes 512 bytes together
+                const size_t o = ((size_t)n * 2 + (up ? 0 : 1)) * kC * kN + (8 * cg * kC + tok) * 4;
+                if (M3_SPAN(11, o, 7 * kC * 4 + 4, (long long)total_chunks * 2 * kC * kN)) {
+                    float4* dst = reinterpret_cast<float4*>(q.part_qk + o);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) dst[j] = make_float4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                    }
+                    for (int j = 0; j < 8; ++j) dst[j * kC] = make_float4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
                 }
             }
         }
@@ -512,6 +516,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         ++done_c;
         par ^= 1;
+        if (hpg == 1 && tid == 0) {                    // rows behind the tensor's end are left out
+            tma_store_5d(&tmDQ, sb + OFF_OUT, 0, 0, g, c * kC, b);
+            tma_store_5d(&tmDQ, sb + OFF_OUT + 16384, 64, 0, g, c * kC, b);
+            tma_store_5d(&tmDK, sb + OFF_OUT + 8192, 0, 0, g, c * kC, b);
+            tma_store_5d(&tmDK, sb + OFF_OUT + 24576, 64, 0, g, c * kC, b);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        __syncwarp();
         if (warp == 0) {
             // lane l has tokens 2 l, 2 l + 1; dg is the sum from a token to the chunk's end
             float d[2], tl2 = 0.f, total = 0.f;
@@ -521,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 d[e] = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    d[e] += m->row[j][i] + m->row[j][64 + i] - m->col[j][i];
+                    d[e] += m->row[j][i] + m->row[j][64 + i];
                     tl2 += m->tail[j][i];
                 }
             }
@@ -547,16 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 4; ++j) vb += m->drv[j][i] + m->beta[j][i];
                 const float vg = i < nt ? dg[e] : 0.f;
                 vb = i < nt ? vb : 0.f;
-                if (hpg == 1) {
-                    if (out_g) out_g[o] = __float2bfloat16_rn(vg);
-                    out_b[o] = __float2bfloat16_rn(vb);
-                } else {
-                    q.part_g[2 * o] = vg;
-                    q.part_g[2 * o + 1] = vb;
-                }
+                if (out_g) out_g[o] = __float2bfloat16_rn(vg);
+                out_b[o] = __float2bfloat16_rn(vb);
             }
         }
     }
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (stop && warp == 0) {                       // a wait ran out: what is still on its way has a second to end
         commit_one(&m->drain);
         mbar_wait_flag(&m->drain, 0, &m->drain_flag, nullptr, 0);
@@ -572,6 +580,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) tmem_dealloc(m->tmem_base, 512);
 }
 
+// dq, dk: the sum of a group's heads, in their order.  One CTA per chunk of a
+// group and half the columns of dq or dk; a thread adds 8 columns of a token, a
+// warp 8 tokens x 32 columns, so that what it reads and writes are whole sectors.
+__global__ void __launch_bounds__(256) delta_group_sum_kernel(DeltaParams q) {
+    const int H = q.nheads, hpg = H / q.ngroups;
+    const int c = blockIdx.x % q.nck, bg = blockIdx.x / q.nck, b = bg / q.ngroups, g = bg % q.ngroups;
+    const int side = blockIdx.y >> 1;
+    int len = q.seqlen;
+    if (q.lengths && M3_IN(15, b, q.batch)) len = min(max(q.lengths[b], 0), q.seqlen);
+    [[maybe_unused]] const long long ext = (long long)q.batch * H * q.nck * 2 * kC * kN;
+    for (int e = threadIdx.x; e < 8 * kC; e += 256) {
+        const int l = e & 31, tok = 8 * ((e >> 5) & 7) + (l & 7), col8 = (blockIdx.y & 1) * 8 + (e >> 8) * 4 + (l >> 3);
+        const int t = c * kC + tok;
+        if (t >= q.seqlen) continue;
+        float s[8] = {};
+        if (t < len)
+#pragma unroll 4
+            for (int hh = 0; hh < hpg; ++hh) {
+                const size_t o = ((((size_t)b * H + g * hpg + hh) * q.nck + c) * 2 + side) * kC * kN + (2 * col8 * kC + tok) * 4;
+                if (!M3_SPAN(16, o, 4 * kC + 4, ext)) continue;
+                const float4 x = *reinterpret_cast<const float4*>(q.part_qk + o);
+                const float4 y = *reinterpret_cast<const float4*>(q.part_qk + o + 4 * kC);
+                s[0] += x.x;
+                s[1] += x.y;
+                s[2] += x.z;
+                s[3] += x.w;
+                s[4] += y.x;
+                s[5] += y.y;
+                s[6] += y.z;
+                s[7] += y.w;
+            }
+        const size_t o = (((size_t)b * q.seqlen + t) * q.ngroups + g) * kN + 8 * col8;
+        if (M3_SPAN(17, o, 8, (long long)q.batch * q.seqlen * q.ngroups * kN))
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(side ? q.dk : q.dq) + o) = pack_chunk(s);
+    }
+}
+
 }  // namespace dbw
 
 cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st) {
@@ -585,15 +630,20 @@ cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* sta
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    CUtensorMap mK, mQ;
+    CUtensorMap mK, mQ, mDK, mDQ;
     if (!make_tile_map(&mK, q.k, kN, 1, d.ngroups, d.seqlen, d.batch, kC) ||
-        !make_tile_map(&mQ, q.q, kN, 1, d.ngroups, d.seqlen, d.batch, kC))
+        !make_tile_map(&mQ, q.q, kN, 1, d.ngroups, d.seqlen, d.batch, kC) ||
+        !make_tile_map(&mDK, q.dk, kN, 1, d.ngroups, d.seqlen, d.batch, kC) ||
+        !make_tile_map(&mDQ, q.dq, kN, 1, d.ngroups, d.seqlen, d.batch, kC))
         return cudaErrorInvalidValue;
     const long long total = (long long)d.batch * d.nheads * q.nck, sms = device_sm_count();
-    delta_grad_kernel<<<(unsigned)(total < sms ? total : sms), kThreads, SMEM_BYTES, st>>>(mK, mQ, q, (int)total, status);
+    delta_grad_kernel<<<(unsigned)(total < sms ? total : sms), kThreads, SMEM_BYTES, st>>>(mK, mQ, mDK, mDQ, q, (int)total,
+                                                                                         status);
     e = cudaGetLastError();
     if (e != cudaSuccess || d.nheads == d.ngroups) return e;
-    return launch_delta_reduce(d, q, 1, st);
+    const dim3 grid((unsigned)((long long)d.batch * d.ngroups * q.nck), 4);
+    delta_group_sum_kernel<<<grid, 256, 0, st>>>(q);
+    return cudaGetLastError();
 }
 
 }  // namespace m3

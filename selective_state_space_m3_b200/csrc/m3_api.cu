@@ -731,20 +731,19 @@ struct DeltaBwdLayout {
 
 // Token path: a state a checkpoint, and every column tile's parts of dq, dk,
 // dg, dbeta.  Chunked path: a record a chunk, and, where heads share keys,
-// every head's parts.
+// every head's parts of dq, dk.
 static DeltaBwdLayout delta_bwd_layout(const m3_dims& d) {
     DeltaBwdLayout l;
     l.chunked = delta_chunked(d);
     l.KB = l.chunked ? 64 : delta_block_tokens(d);
     l.nck = d.seqlen > 0 ? (int)(((long long)d.seqlen + l.KB - 1) / l.KB) : 0;
     const size_t units = (size_t)d.batch * d.nheads, NP = (size_t)d.dstate * d.headdim;
-    const size_t tiles = !l.chunked ? delta_tiles(d) : d.nheads == d.ngroups ? 0 : 1;
-    const size_t toks = units * d.seqlen * tiles;
+    const size_t rows = l.chunked ? (d.nheads == d.ngroups ? 0 : units * l.nck * l.KB) : units * d.seqlen * delta_tiles(d);
     size_t off = kWorkspaceHeaderBytes;
     l.ckpt = off;    off = round256(off + (l.chunked ? 0 : units * l.nck * NP * sizeof(float)));
     l.rec = off;     off = round256(off + (l.chunked ? units * l.nck * delta_record_bytes(d, true) : 0));
-    l.part_qk = off; off = round256(off + toks * 2 * d.dstate * sizeof(float));
-    l.part_g = off;  off = round256(off + toks * 2 * sizeof(float));
+    l.part_qk = off; off = round256(off + rows * 2 * d.dstate * sizeof(float));
+    l.part_g = off;  off = round256(off + (l.chunked ? 0 : rows * 2 * sizeof(float)));
     l.total = off;
     return l;
 }

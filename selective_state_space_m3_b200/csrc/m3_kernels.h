@@ -153,7 +153,7 @@ struct DeltaParams {
     float* d_init_h;           // nullable
     int KB, nck;               // tokens a checkpoint, checkpoints a sequence
     float* ckpt;               // [b][h][nck][n][p]
-    float* part_qk;            // [column tile][b][t][h][2][n]: parts of dq, dk
+    float* part_qk;            // [column tile][b][t][h][2][n]: parts of dq, dk; chunked: [b][h][chunk][2][n / 4][64][4]
     float* part_g;             // [column tile][b][t][h][2]: parts of dg, dbeta
     __nv_bfloat16* rec;        // chunked path: nck records a (b, h) (delta_tc.cuh)
 };
@@ -172,7 +172,6 @@ size_t delta_record_bytes(const m3_dims& d, bool grad);
 // chunked gradient (same shapes)
 cudaError_t launch_delta_rev(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st);
 cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st);
-cudaError_t launch_delta_reduce(const m3_dims& d, const DeltaParams& q, int tiles, cudaStream_t st);
 cudaError_t launch_delta_step(const m3_dims& d, const DeltaParams& q, cudaStream_t st);
 
 // root-mean-square norm (k_norm.cu)
