@@ -62,6 +62,7 @@ struct Stage {
     float* o;      // [kTB][kCols]: y (prefill), dy (gradient)
     float* a;      // [kTB] e^g
     float* beta;   // [kTB]
+    float* kq;     // [kTB] k . q (prefill)
 };
 __device__ __forceinline__ Stage stage_at(float* p, int N) {
     Stage s;
@@ -71,9 +72,10 @@ __device__ __forceinline__ Stage stage_at(float* p, int N) {
     s.o = s.v + kTB * kCols;
     s.a = s.o + kTB * kCols;
     s.beta = s.a + kTB;
+    s.kq = s.beta + kTB;
     return s;
 }
-__host__ __device__ constexpr int stage_floats(int N) { return kTB * (2 * N + 2 * kCols + 2); }
+__host__ __device__ constexpr int stage_floats(int N) { return kTB * (2 * N + 2 * kCols + 3); }
 
 template <typename T>
 __device__ __forceinline__ void stage_load(const DeltaParams& q, const Stage& s, int b, int h, int g, int p0, int t0,
@@ -129,6 +131,36 @@ __global__ void __launch_bounds__(kThreads) delta_seq_kernel(DeltaParams q) {
         if (q.init_h && n < N && p < P && M3_IN(6, hb + (size_t)n * P + p, ext_h)) S[i] = q.init_h[hb + (size_t)n * P + p];
     }
     T* yg = static_cast<T*>(q.y);
+    const T* kg = static_cast<const T*>(q.k);
+    const T* qg = static_cast<const T*>(q.q);
+    const T* vg = static_cast<const T*>(q.v);
+    [[maybe_unused]] const long long ext_k = (long long)q.batch * q.seqlen * q.ngroups * N;
+    [[maybe_unused]] const long long toks = (long long)q.batch * q.seqlen * q.nheads;
+    // a block's operands come through registers, asked for before the previous
+    // block is worked on: thread 16 t + j has rows j, j + 16, ... of token t
+    static_assert(kThreads == kTB * kRG && kCols == kRG);
+    const int tt = tid >> 4;
+    float fk[NR], fq[NR], fv = 0.f, fg = 0.f, fb = 0.f;
+    auto fetch = [&](int t0) {
+        const bool in = t0 + tt < len;
+        const size_t row = (size_t)b * q.seqlen + t0 + tt;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const int n = rg + kRG * i;
+            const size_t o = (row * q.ngroups + g) * N + n;
+            const bool ok = in && n < N && M3_IN(2, o, ext_k);
+            fk[i] = ok ? ld_io(kg + o) : 0.f;
+            fq[i] = ok ? ld_io(qg + o) : 0.f;
+        }
+        const size_t o = row * q.nheads + h;
+        fv = in && p0 + rg < P && M3_IN(3, o * P + p0 + rg, ext_v) ? ld_io(vg + o * P + p0 + rg) : 0.f;
+        if (rg == 0) {
+            const bool ok = in && M3_IN(4, o, toks);
+            fg = q.g && ok ? q.g[o] : 0.f;
+            fb = ok ? q.beta[o] : 0.f;
+        }
+    };
+    fetch(0);
     for (int t0 = 0; t0 < len; t0 += kTB) {
         const int nt = min(kTB, len - t0);
         if (q.ckpt && t0 % q.KB == 0 && p < P) {
@@ -141,8 +173,32 @@ __global__ void __launch_bounds__(kThreads) delta_seq_kernel(DeltaParams q) {
                     ck[(size_t)n * P + p] = S[i];
             }
         }
-        stage_load<T>(q, s, b, h, g, p0, t0, nt, nullptr);
+        float kq = 0.f;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const int n = rg + kRG * i;
+            if (n < N) {
+                s.k[tt * N + n] = fk[i];
+                s.q[tt * N + n] = fq[i];
+            }
+            kq = fmaf(fk[i], fq[i], kq);
+        }
+        s.v[tt * kCols + rg] = fv;
+        kq = group_sum<16>(kq);
+        if (rg == 0) {
+            s.kq[tt] = kq;
+            s.a[tt] = q.g ? expf(clamp_g(fg)) : 1.f;
+            s.beta[tt] = fb;
+        }
         __syncthreads();
+        if (t0 + kTB < len) fetch(t0 + kTB);
+        float kr[NR], qr[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const int n = rg + kRG * i;
+            kr[i] = n < N ? s.k[n] : 0.f;
+            qr[i] = n < N ? s.q[n] : 0.f;
+        }
         for (int t = 0; t < nt; ++t) {
             if (q.ckpt && t > 0 && (t0 + t) % q.KB == 0 && p < P) {
                 float* ck = q.ckpt + ((size_t)bh * q.nck + (t0 + t) / q.KB) * N * P;
@@ -154,33 +210,38 @@ __global__ void __launch_bounds__(kThreads) delta_seq_kernel(DeltaParams q) {
                         ck[(size_t)n * P + p] = S[i];
                 }
             }
-            float kr[NR], qr[NR], sk = 0.f, sq = 0.f, kq = 0.f;
+            float sk = 0.f, sq = 0.f;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                sk = fmaf(S[i], kr[i], sk);
+                sq = fmaf(S[i], qr[i], sq);
+            }
+            // the next token's k and q, while the sums go round
+            const int tn = min(t + 1, nt - 1);
+            float kn[NR], qn[NR];
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
                 const int n = rg + kRG * i;
-                kr[i] = n < N ? s.k[t * N + n] : 0.f;
-                qr[i] = n < N ? s.q[t * N + n] : 0.f;
-                sk = fmaf(S[i], kr[i], sk);
-                sq = fmaf(S[i], qr[i], sq);
-                kq = fmaf(kr[i], qr[i], kq);
+                kn[i] = n < N ? s.k[tn * N + n] : 0.f;
+                qn[i] = n < N ? s.q[tn * N + n] : 0.f;
             }
+            const float a = s.a[t], beta = s.beta[t], v = s.v[t * kCols + c], kq = s.kq[t];
             sk = group_sum<16>(sk);
-            sq = group_sum<16>(sq);
-            kq = group_sum<16>(kq);
-            const float a = s.a[t];
-            const float u = s.beta[t] * fmaf(-a, sk, s.v[t * kCols + c]);
+            const float u = beta * fmaf(-a, sk, v);
 #pragma unroll
-            for (int i = 0; i < NR; ++i) S[i] = fmaf(kr[i], u, a * S[i]);
+            for (int i = 0; i < NR; ++i) {
+                S[i] = fmaf(kr[i], u, a * S[i]);
+                kr[i] = kn[i];
+                qr[i] = qn[i];
+            }
+            sq = group_sum<16>(sq);
             if (rg == 0) s.o[t * kCols + c] = q.scale * fmaf(kq, u, a * sq);
         }
         __syncthreads();
-        if (yg)
-            for (int e = tid; e < nt * kCols; e += kThreads) {
-                const int t = e / kCols, cc = e - t * kCols;
-                const size_t o = (((size_t)b * q.seqlen + t0 + t) * q.nheads + h) * P + p0 + cc;
-                if (p0 + cc < P && M3_IN(9, o, ext_v)) st_io(yg + o, s.o[e]);
-            }
-        __syncthreads();
+        if (yg && tt < nt && p0 + rg < P) {
+            const size_t o = (((size_t)b * q.seqlen + t0 + tt) * q.nheads + h) * P + p0 + rg;
+            if (M3_IN(9, o, ext_v)) st_io(yg + o, s.o[tt * kCols + rg]);
+        }
     }
     if (q.final_h) {
 #pragma unroll
@@ -381,9 +442,13 @@ __global__ void __launch_bounds__(kThreads) delta_reduce_kernel(DeltaParams q, i
 // One CTA per (b, h): the state streams through registers once, 128 bits a
 // load, all loads issued before any arithmetic; row group rg of a thread holds
 // rows rg, rg + RG, ... at four columns.  Bound by the state's traffic (8 bytes
-// an element, 90 % of all bytes for N = 128, P = 64).
+// an element, 90 % of all bytes for N = 128, P = 64): 256 sequences of 32 heads,
+// 0.54 GB, take 105 us, 5.2 TB/s.  Four CTAs an SM are the best: 109 us without
+// the bound, 132 us with five, which leave too few registers for all loads at
+// once; two that stay and ask for the next state before they work on the present
+// one take 120 us.
 template <typename T, int NPT>
-__global__ void __launch_bounds__(256) delta_step_kernel(DeltaParams q) {
+__global__ void __launch_bounds__(256, NPT <= 8 ? 4 : 1) delta_step_kernel(DeltaParams q) {
     __shared__ float sk[256], sq[256], sv[256], red[8][2][256], skq[8];
     const int N = q.dstate, P = q.headdim, tid = threadIdx.x;
     const int PC = P >> 2, RG = 256 / PC;
