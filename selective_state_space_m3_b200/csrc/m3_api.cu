@@ -652,6 +652,17 @@ static m3_status check_delta(const m3_dims* d, bool need_seq) {
 // whether the chunked tensor-core kernels take these dims
 static bool delta_chunked(const m3_dims& d) { return delta_tc_eligible(d) && !env_is("M3_DELTA_PATH", "token"); }
 
+// The chunked prefill takes the same time for 1 to 64 tokens, the token kernel's
+// grows with them.  Measured, N = 128, P = 64 (us, chunked against token):
+//      8 states (32 CTAs of the token kernel): 10.4 : 7.1 at 16 tokens, 10.4 : 9.8 at 24
+//    256 states (1024 CTAs): 23.8 : 19.3 at 4, 23.8 : 27.6 at 12
+//   4096 states: 275 : 241 at 2, 276 : 277 at 4, 277 : 346 at 8
+// so few tokens go to the token kernel, more of them where its CTAs have an SM each.
+static bool delta_fwd_chunked(const m3_dims& d) {
+    const long long ctas = (long long)d.batch * d.nheads * delta_tiles(d);
+    return delta_chunked(d) && d.seqlen > (ctas <= 148 ? 16 : 4);
+}
+
 static int delta_chunks(const m3_dims& d) { return (int)((d.seqlen + 63LL) / 64); }
 
 static DeltaParams delta_params(const m3_dims& d, const void* q, const void* k, const void* v, const float* g,
@@ -678,7 +689,7 @@ m3_status m3_delta_workspace_size(const m3_dims* d, size_t* bytes) {
     if (s != M3_OK) return s;
     // the chunked path: a record a chunk
     *bytes = kWorkspaceHeaderBytes;
-    if (delta_chunked(*d))
+    if (delta_fwd_chunked(*d))
         *bytes += round256((size_t)d->batch * d->nheads * delta_chunks(*d) * delta_record_bytes(*d, false));
     return M3_OK;
 }
@@ -702,8 +713,8 @@ m3_status m3_delta_fwd(const m3_dims* d, const void* q, const void* k, const voi
     p.final_h = final_h;
     p.nck = delta_chunks(*d);
     p.rec = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(workspace) + kWorkspaceHeaderBytes);
-    const cudaError_t e = delta_chunked(*d) ? launch_delta_tc(*d, p, false, static_cast<int*>(workspace), st)
-                                            : launch_delta_seq(*d, p, st);
+    const cudaError_t e = delta_fwd_chunked(*d) ? launch_delta_tc(*d, p, false, static_cast<int*>(workspace), st)
+                                                : launch_delta_seq(*d, p, st);
     return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }
 
