@@ -12,6 +12,10 @@
 // Gram product, and their place takes the images: 37 KB a CTA, five an SM, whose
 // loads, products and substitutions overlap.
 //
+// Bound by memory: 32 KB in and 25 KB out a chunk; 4096 chunks take 51 us
+// (4.7 TB/s), 16384 chunks 186 us (5.1 TB/s).  In the chain itself this work
+// took half of every chunk's time (32768 tokens 1.45 ms instead of 0.85).
+//
 // Every wait on an mbarrier is bounded (1 s); on expiry the kernel records
 // M3_ERR_DEVICE_TIMEOUT in the workspace status word and runs out without
 // further waiting.

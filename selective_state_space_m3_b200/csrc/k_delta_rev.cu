@@ -16,6 +16,8 @@
 // Recorded for k_delta_bwd_tc.cu: dR and the gradient of the state behind every
 // chunk.  The transposed products read the images of T and P that the prefill
 // uses, as MN-major operands (64 of the 128 rows are other data and unused).
+// Bound by the chain's latency: 2.1 us a chunk with 32 columns a CTA, 1.7 with 16
+// (tensor pipe 22 and 14 % active).
 //
 // Every wait on an mbarrier is bounded (1 s); on expiry the kernel records
 // M3_ERR_DEVICE_TIMEOUT in the workspace status word and runs out without
@@ -380,9 +382,10 @@ cudaError_t launch_delta_rev(const m3_dims& d, const DeltaParams& q, int* status
         !make_tile_map(&mQ, q.q, kN, 1, d.ngroups, d.seqlen, d.batch, kC) ||
         !make_tile_map(&mY, q.dy, d.headdim, 1, d.nheads, d.seqlen, d.batch, kC))
         return cudaErrorInvalidValue;
-    // columns a CTA, as for the prefill's chain
+    // columns a CTA: the least time over the rounds that the CTAs make, as for the
+    // prefill's chain (2.1 us a chunk with 32, 1.7 with 16)
     const long long tiles = (long long)d.batch * d.nheads * (d.headdim / 64), sms = device_sm_count();
-    const long long t32 = 195 * ((2 * tiles + sms - 1) / sms), t16 = 145 * ((4 * tiles + sms - 1) / sms);
+    const long long t32 = 210 * ((2 * tiles + sms - 1) / sms), t16 = 170 * ((4 * tiles + sms - 1) / sms);
     return t32 <= t16 ? launch<32>(mK, mQ, mY, d, q, status, st) : launch<16>(mK, mQ, mY, d, q, status, st);
 }
 

@@ -74,6 +74,14 @@ template <> struct Vec8<float> {
     }
 };
 
+// elements j and j + 1 as a pair (two lanes of one float32x2 instruction)
+__device__ __forceinline__ float2 pair(const float* f, int j) { return make_float2(f[j], f[j + 1]); }
+__device__ __forceinline__ void put(float* f, int j, float2 v) {
+    f[j] = v.x;
+    f[j + 1] = v.y;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // NA arrays' elements of a row that a thread holds, NV vectors of each
 template <typename T, int NV, int NA>
 struct RowRegs {
@@ -163,8 +171,8 @@ __device__ __forceinline__ float2 row_reduce2(float2 v, int tpr, float2* buf) {
 
 // RES: a residual is added; Q8: an 8-bit output is written.  At most 40 registers
 // a thread (three CTAs of 512 an SM), so that enough loads are in flight:
-// measured 80 instead of 99 us for 32768 x 2048 with residual and 8-bit output
-// (90 % of the copy rate).
+// 32768 x 2048 with residual and 8-bit output takes 88 us (5.3 TB/s, 83 % of the
+// copy rate), 99 without the bound; arithmetic in pairs, 94 without.
 template <typename T, int NV, bool RES, bool Q8>
 __global__ void __launch_bounds__(512, NV <= 2 ? 3 : 1) norm_kernel(NormParams q, int tpr) {
     __shared__ float buf[16];
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 3 : 1) norm_kernel(NormParams q
     cur.fetch(src, q, row, lane, tpr);
     {
         float s[NV][8];
-        float ss = 0.f;
+        float2 ss2 = both(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             Vec8<T>::open(cur.r[0][i], s[i]);
@@ -188,12 +196,12 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 3 : 1) norm_kernel(NormParams q
                 float r[8];
                 Vec8<T>::open(cur.r[1][i], r);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[i][j] += r[j];
+                for (int j = 0; j < 8; j += 2) put(s[i], j, __fadd2_rn(pair(s[i], j), pair(r, j)));
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(s[i][j], s[i][j], ss);
+            for (int j = 0; j < 8; j += 2) ss2 = __ffma2_rn(pair(s[i], j), pair(s[i], j), ss2);
         }
-        ss = row_reduce<false>(ss, tpr, buf);
+        const float ss = row_reduce<false>(ss2.x + ss2.y, tpr, buf);
         const float rs = rsqrtf(ss / (float)q.width + q.eps);
         float top = 0.f;
 #pragma unroll
@@ -206,9 +214,9 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 3 : 1) norm_kernel(NormParams q
             for (int j = 0; j < 8; ++j) w[j] = 0.f;
             if (in) load_weight8(q.weight, c, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                s[i][j] = in ? s[i][j] * rs * w[j] : 0.f;
-                if (Q8) top = nmax(top, fabsf(s[i][j]));
+            for (int j = 0; j < 8; j += 2) {
+                put(s[i], j, __fmul2_rn(__fmul2_rn(pair(s[i], j), both(rs)), pair(w, j)));
+                if (Q8 && in) top = nmax(nmax(top, fabsf(s[i][j])), fabsf(s[i][j + 1]));
             }
             if (in && q.y) Vec8<T>::store(q.y, base + c, s[i]);
             if (Q8 && q.block) {          // 16 lanes hold the 128 columns of one scale
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormParams q, int tpr) {
         const bool live = row < q.rows;
         const size_t base = live ? (size_t)row * q.width : 0;
         const RowRegs<T, NV, 3> cur = next;
-        float2 sum = make_float2(0.f, 0.f);
+        float2 ss = both(0.f), sd = both(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + tpr * i) * 8;
@@ -312,13 +320,13 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormParams q, int tpr) {
             for (int j = 0; j < 8; ++j) w[j] = 0.f;
             if (c < q.width && M3_SPAN(15, c, 8, q.width)) load_weight8(q.weight, c, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sum.x = fmaf(s[j], s[j], sum.x);
-                sum.y = fmaf(s[j] * w[j], d[j], sum.y);
+            for (int j = 0; j < 8; j += 2) {
+                ss = __ffma2_rn(pair(s, j), pair(s, j), ss);
+                sd = __ffma2_rn(__fmul2_rn(pair(s, j), pair(w, j)), pair(d, j), sd);
             }
         }
         if (k + 1 < rounds) next.fetch(src, q, row + groups, lane, tpr);
-        sum = row_reduce2(sum, tpr, buf[k & 1]);
+        const float2 sum = row_reduce2(make_float2(ss.x + ss.y, sd.x + sd.y), tpr, buf[k & 1]);
         const float rs = rsqrtf(sum.x / (float)q.width + q.eps);
         const float m = sum.y * rs * rs / (float)q.width;          // mean(w dy s^) rs
 #pragma unroll
@@ -331,9 +339,10 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormParams q, int tpr) {
             Vec8<T>::open(cur.r[2][i], e);
             load_weight8(q.weight, c, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dw[i][j] = fmaf(d[j], s[j] * rs, dw[i][j]);
-                e[j] += rs * fmaf(w[j], d[j], -s[j] * m);
+            for (int j = 0; j < 8; j += 2) {
+                const float2 s2 = pair(s, j), d2 = pair(d, j);
+                put(dw[i], j, __ffma2_rn(d2, __fmul2_rn(s2, both(rs)), pair(dw[i], j)));
+                put(e, j, __ffma2_rn(both(rs), __ffma2_rn(pair(w, j), d2, __fmul2_rn(s2, both(-m))), pair(e, j)));
             }
             Vec8<T>::store(q.dx, base + c, e);
         }
@@ -398,7 +407,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(NormParams q) {
     const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5, c = blockIdx.x * 32 + cx;
     float v = 0.f;
     if (c < q.width)
-#pragma unroll 4
+#pragma unroll 16
         for (int i = ry; i < q.parts; i += 32)
             if (M3_IN(22, (long long)i * q.width + c, (long long)q.parts * q.width)) v += q.part[(size_t)i * q.width + c];
     t[ry][cx] = v;
@@ -455,7 +464,7 @@ static cudaError_t fwd(const NormParams& q, cudaStream_t st) {
 
 // CTAs of the gradient: as many as its 124 registers let run together, so that a
 // row's loads can go ahead of the row before and few parts are left to add
-// (16384 x 2048: 60 us with four an SM, 118 without loads ahead)
+// (16384 x 2048: 59 us with four an SM, 5 of them the parts' sums; 118 without loads ahead)
 static unsigned bwd_grid(long long rows, int width) {
     const long long sms = device_sm_count();
     if (!vec_ok(width)) return (unsigned)(rows < 4 * sms ? rows : 4 * sms);
