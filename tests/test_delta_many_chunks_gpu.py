@@ -1,0 +1,37 @@
+"""Batches with more chunks of 64 tokens than the GPU has multiprocessors, so
+that a block of the chunk gradients walks several chunks: full ones, part ones,
+and ones behind a sequence's end between them.  One sequence at a time against
+64 bits; tolerances as in test_delta_gpu.py."""
+import pytest
+import torch
+
+from tests._delta_ref import delta_inputs
+from tests.test_delta_gpu import _bwd, _check_bwd, _check_fwd, _fwd
+
+pytestmark = pytest.mark.gpu
+
+# batch, tokens, heads, groups, headdim
+CASES = [(24, 200, 4, 4, 64), (24, 200, 4, 2, 64), (12, 250, 4, 4, 128), (12, 250, 4, 1, 128)]
+
+
+@pytest.mark.parametrize("case", CASES, ids=["b%d_t%d_h%d_g%d_p%d" % c for c in CASES])
+def test_prefill_and_gradient(case):
+    b, t, h, g, p = case
+    x = delta_inputs(b, t, h, g, p, 128, torch.bfloat16, seed=31)
+    some = [t, 0, 64, 65, 1, 128, t - 1, 192, 130, 0, 63, t]
+    lengths = torch.tensor([some[i % 12] for i in range(b)])
+    for i, n in enumerate(lengths.tolist()):
+        for k in ("q", "k", "v", "dy"):
+            x[k][i, n:] = float("nan")
+    y, hn = _fwd(x, 0.2, lengths)
+    grads = _bwd(x, 0.2, lengths)
+    for i, n in enumerate(lengths.tolist()):
+        one = {k: torch.nan_to_num(v[i:i + 1], nan=0.0) for k, v in x.items()}
+        _check_fwd(one, y[i:i + 1], hn[i:i + 1], 0.2, lengths[i:i + 1])
+        got = {k: v[i:i + 1] for k, v in grads.items()}
+        if n:
+            _check_bwd(one, got, 0.2, lengths[i:i + 1])
+        for k in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert float(got[k][:, n:].float().abs().sum()) == 0.0, k
+        if not n:
+            assert torch.equal(got["dh0"].cpu(), x["dh"][i:i + 1])
