@@ -138,14 +138,16 @@ __device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
-// arrival that waits for a value loaded from shared memory (not negative, so its
-// sign bit, zero, can stand in the address): an arrival right behind a load does
-// not wait for it, and the next chunk's data may overtake the load
+// arrival that waits for a value loaded from shared memory: its sign bit goes
+// through the address, whose last three bits are cleared again (a barrier has 8
+// bytes).  An arrival right behind a load does not wait for it, and the next
+// chunk's data may overtake the load.
 __device__ __forceinline__ void arrive_after(uint64_t* b, uint32_t loaded) {
     asm volatile(
         "{\n\t.reg .b32 t;\n\t"
         "shr.u32 t, %1, 31;\n\t"
         "add.u32 t, t, %0;\n\t"
+        "and.b32 t, t, 0xfffffff8;\n\t"
         "mbarrier.arrive.shared::cta.b64 _, [t];\n\t}" ::"r"(su32(b)), "r"(loaded) : "memory");
 }
 

@@ -322,10 +322,11 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
     } else {
         // ------------------------------------------------------------- loads
         if (lane == 0) {
+            int asked = 0, asked_y = 0;            // (fewer than the chunks after a wait that ran out)
             for (int i = 0; i < nch; ++i) {
                 const int c = nch - 1 - i;
                 const uint32_t st = sbase + (i & 1) * kStage;
-                if (i >= 2) wait(&m->freed[i & 1], (i >> 1) - 1, m, status, 30);
+                if (i >= 2 && !wait(&m->freed[i & 1], (i >> 1) - 1, m, status, 30)) break;
                 // the chunk after next into L2: its load waits for a stage, and then finds it there
                 if (c >= 2) {
                     const int t = (c - 2) * kC;
@@ -338,22 +339,23 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
                 }
                 uint64_t* bar = &m->full[i & 1];
                 M3_NOTE(8, (bh * q.nck + c) * rec + kRecSlice - 1, ext_rec);
+                ++asked;
                 mbar_expect_tx(bar, 32768 + kRecBytes);
                 tma_load_5d(st, &tmK, bar, 0, 0, w.g, c * kC, w.b);
                 tma_load_5d(st + 16384, &tmK, bar, 64, 0, w.g, c * kC, w.b);
                 tma_load_5d(st + 8192, &tmQ, bar, 0, 0, w.g, c * kC, w.b);
                 tma_load_5d(st + 24576, &tmQ, bar, 64, 0, w.g, c * kC, w.b);
                 bulk_load(st + ST_X, q.rec + (bh * q.nck + c) * rec, kRecBytes, bar);
-                if (i >= 2) wait(&m->dy_free[i & 1], (i >> 1) - 1, m, status, 31);
+                if (i >= 2 && !wait(&m->dy_free[i & 1], (i >> 1) - 1, m, status, 31)) break;
+                ++asked_y;
                 bar = &m->dy_full[i & 1];
                 mbar_expect_tx(bar, 8192);
                 tma_load_5d(sbase + OFF_DY + (i & 1) * 8192, &tmY, bar, w.p0 & ~63, 0, w.h, c * kC, w.b);
             }
             // nothing may still be on its way into shared memory when the CTA ends
-            for (int i = max(0, nch - 2); i < nch; ++i) {
-                mbar_wait_flag(&m->full[i & 1], (i >> 1) & 1, &m->drain_flag, nullptr, 0);
+            for (int i = max(0, asked - 2); i < asked; ++i) mbar_wait_flag(&m->full[i & 1], (i >> 1) & 1, &m->drain_flag, nullptr, 0);
+            for (int i = max(0, asked_y - 2); i < asked_y; ++i)
                 mbar_wait_flag(&m->dy_full[i & 1], (i >> 1) & 1, &m->drain_flag, nullptr, 0);
-            }
         }
         __syncwarp();
     }

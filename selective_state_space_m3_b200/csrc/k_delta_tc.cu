@@ -391,9 +391,10 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
         // ------------------------------------------------------------- loads
         if (lane == 0) {
             const size_t rec = rec_elems(P, DUMP);
+            int asked = 0, asked_v = 0;            // (fewer than the chunks after a wait that ran out)
             for (int c = 0; c < w.nch; ++c) {
                 const uint32_t kq = sbase + OFF_KQ + (c % 3) * 32768, x = sbase + OFF_X + (c % 3) * kXBytes;
-                if (c >= 3) wait(&m->freed[c % 3], c / 3 - 1, m, status, 30);
+                if (c >= 3 && !wait(&m->freed[c % 3], c / 3 - 1, m, status, 30)) break;
                 // chunk c + 3 into L2: its load waits for a stage, and then finds it there
                 if (c + 3 < w.nch) {
                     const int t = (c + 3) * kC;
@@ -412,18 +413,20 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
                 tma_load_5d(kq + 16384, &tmK, bar, 64, 0, w.g, c * kC, w.b);
                 tma_load_5d(kq + 8192, &tmQ, bar, 0, 0, w.g, c * kC, w.b);
                 tma_load_5d(kq + 24576, &tmQ, bar, 64, 0, w.g, c * kC, w.b);
+                ++asked;
                 bulk_load(x, src + kRecX, kXBytes, bar);
                 bulk_load(sbase + OFF_GATES + (c % 3) * (int)sizeof(ChainGates), src + kRecGates, sizeof(ChainGates), bar);
-                if (c >= 2) wait(&m->v_free[c & 1], (c >> 1) - 1, m, status, 31);
+                if (c >= 2 && !wait(&m->v_free[c & 1], (c >> 1) - 1, m, status, 31)) break;
+                ++asked_v;
                 bar = &m->v_full[c & 1];
                 mbar_expect_tx(bar, 8192);
                 tma_load_5d(sbase + OFF_V + (c & 1) * 8192, &tmV, bar, w.p0 & ~63, 0, w.h, c * kC, w.b);
             }
             // nothing may still be on its way into shared memory when the CTA ends
-            for (int c = max(0, w.nch - 3); c < w.nch; ++c) {
+            for (int c = max(0, asked - 3); c < asked; ++c)
                 mbar_wait_flag(&m->full[c % 3], (c / 3) & 1, &m->drain_flag, nullptr, 0);
-                if (c >= w.nch - 2) mbar_wait_flag(&m->v_full[c & 1], (c >> 1) & 1, &m->drain_flag, nullptr, 0);
-            }
+            for (int c = max(0, asked_v - 2); c < asked_v; ++c)
+                mbar_wait_flag(&m->v_full[c & 1], (c >> 1) & 1, &m->drain_flag, nullptr, 0);
         }
         __syncwarp();
     }

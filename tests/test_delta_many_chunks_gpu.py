@@ -35,3 +35,25 @@ def test_prefill_and_gradient(case):
             assert float(got[k][:, n:].float().abs().sum()) == 0.0, k
         if not n:
             assert torch.equal(got["dh0"].cpu(), x["dh"][i:i + 1])
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_a_gate_that_is_no_number_stays_in_its_sequence(sign):
+    """NaN of either sign in one head's gate: that head's results are NaN from
+    there on, all others are the numbers they were."""
+    x = delta_inputs(3, 200, 2, 1, 64, 128, torch.bfloat16, seed=32)
+    y0, h0 = _fwd(x, 0.2)
+    g0 = _bwd(x, 0.2)
+    bad = {k: v.clone() for k, v in x.items()}
+    bad["g"][1, 70, 0] = torch.copysign(torch.tensor(float("nan")), torch.tensor(sign))
+    y1, h1 = _fwd(bad, 0.2)
+    g1 = _bwd(bad, 0.2)
+    assert bool(torch.isnan(h1[1, 0]).all()) and bool(torch.isnan(y1[1, 128:, 0]).all())
+    for b, h in ((0, 0), (0, 1), (1, 1), (2, 0), (2, 1)):
+        assert torch.equal(h1[b, h], h0[b, h]) and torch.equal(y1[b, :, h], y0[b, :, h])
+        for k in ("dv", "dg", "dbeta"):
+            assert torch.equal(g1[k][b, :, h], g0[k][b, :, h]), k
+        assert torch.equal(g1["dh0"][b, h], g0["dh0"][b, h])
+    for b in (0, 2):
+        assert torch.equal(g1["dq"][b], g0["dq"][b]) and torch.equal(g1["dk"][b], g0["dk"][b])
+    assert torch.equal(y1[1, :64, 0], y0[1, :64, 0])
