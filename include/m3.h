@@ -326,9 +326,10 @@ m3_status m3_scan_fwd_reflect(const m3_dims* dims, const void* u,
  * its final state is the one after its last token, rows of y behind it are left
  * as they were, and gradients behind it are zero.
  * Arithmetic is float32.  On bfloat16 layers with dstate 128 and headdim a
- * multiple of 64 the prefill and the gradient run chunked on the tensor cores;
- * their chains of states keep float32 values as sums of bfloat16 parts (16 bits
- * and more), and only products that end in y round an operand to bfloat16. */
+ * multiple of 64 the prefill (of more than 16 tokens, or of more than 4 where
+ * batch nheads headdim exceeds 148 x 16) and the gradient run chunked on the
+ * tensor cores; they keep float32 values as sums of bfloat16 parts (16 bits and
+ * more), and only the product that ends in y rounds an operand to bfloat16. */
 
 /* Bytes of device workspace m3_delta_fwd needs (host-only): 256, the status
  * word that m3_device_status reads, and on the chunked path 25 KB for every 64
