@@ -2,7 +2,9 @@
 
 The functions below carry the C ABI's names and only marshal arguments: they
 check tensor placement, dtype and contiguity, turn tensors into device
-pointers and call ``libm3.so`` through ctypes on the current torch stream.
+pointers and call ``libm3.so`` through ctypes on the current torch stream (the
+calls of the gated delta rule and the norm through a small native extension,
+which leaves unusual arguments to the Python code).
 Every step of the scan runs in the library's CUDA kernels; there is no
 PyTorch or CPU implementation behind these calls, and importing the package
 fails if the library has not been built (``python -m
@@ -18,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import importlib.util
 import os
 from typing import Optional
 
@@ -112,6 +115,22 @@ def _load():
 
 
 _lib = _load()
+
+
+def _load_call():
+    """The native argument handling of the calls below (csrc/m3_call.cpp), bound to the library's entry points."""
+    path = os.path.join(_PKG, "_m3_call.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: it must be built (python -m selective_state_space_m3_b200.build)")
+    spec = importlib.util.spec_from_file_location("_m3_call", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(*[ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in
+               ("m3_delta_step", "m3_delta_fwd", "m3_delta_bwd", "m3_rms_norm_fwd", "m3_rms_norm_bwd")])
+    return mod
+
+
+_native = _load_call()
 
 # every symbol include/m3.h declares (checked by the CPU test suite)
 ABI_SYMBOLS = ("m3_scan_workspace_size", "m3_scan_fwd", "m3_step", "m3_rope_bc",
@@ -426,6 +445,9 @@ def m3_delta_fwd(dims: Dims, q, k, v, g, beta, y, workspace, scale: float = 1.0,
     """Gated delta rule over whole sequences (see include/m3.h): writes ``y``
     and, if given, ``final_h``.  ``g`` may be None (no decay); ``lengths`` is
     an int32 device tensor [batch] or None."""
+    st = _native.delta_fwd(dims, q, k, v, g, beta, scale, lengths, init_h, y, final_h, workspace) if stream is None else None
+    if st is not None:
+        return _check(st, "m3_delta_fwd")
     dev, io, f32, tok = q.get_device(), _io_torch(dims), torch.float32, dims.batch * dims.seqlen
     nk, nv, ng = tok * dims.ngroups * dims.dstate, tok * dims.nheads * dims.headdim, tok * dims.nheads
     nh = dims.batch * dims.nheads * dims.dstate * dims.headdim
@@ -438,6 +460,9 @@ def m3_delta_fwd(dims: Dims, q, k, v, g, beta, y, workspace, scale: float = 1.0,
 def m3_delta_step(dims: Dims, h, q, k, v, g, beta, y, scale: float = 1.0, h_out=None, stream=None) -> None:
     """One decode token of the gated delta rule; the state ``h`` is updated in
     place, or left alone and the new one written to ``h_out`` if given."""
+    st = _native.delta_step(dims, h, h if h_out is None else h_out, q, k, v, g, beta, scale, y) if stream is None else None
+    if st is not None:
+        return _check(st, "m3_delta_step")
     dev, io, f32, b = q.get_device(), _io_torch(dims), torch.float32, dims.batch
     nk, ng = b * dims.ngroups * dims.dstate, b * dims.nheads
     nv = ng * dims.headdim
@@ -452,6 +477,10 @@ def m3_delta_bwd(dims: Dims, q, k, v, g, beta, dy, grads: dict, workspace, scale
                  init_h=None, d_final_h=None, d_init_h=None, stream=None) -> None:
     """Gradient of m3_delta_fwd (see include/m3.h).  ``grads`` holds the output
     tensors dq, dk, dv, dg, dbeta in the io dtype (dg may be absent)."""
+    st = _native.delta_bwd(dims, q, k, v, g, beta, scale, lengths, init_h, dy, d_final_h, grads["dq"], grads["dk"],
+                           grads["dv"], grads.get("dg"), grads["dbeta"], d_init_h, workspace) if stream is None else None
+    if st is not None:
+        return _check(st, "m3_delta_bwd")
     dev, io, f32, tok = q.get_device(), _io_torch(dims), torch.float32, dims.batch * dims.seqlen
     nk, nv, ng = tok * dims.ngroups * dims.dstate, tok * dims.nheads * dims.headdim, tok * dims.nheads
     nh = dims.batch * dims.nheads * dims.dstate * dims.headdim
@@ -469,6 +498,9 @@ def m3_rms_norm_fwd(x, eps: float, residual=None, weight=None, sum=None, y=None,
     """Root-mean-square norm of the rows (last axis) of ``x`` plus ``residual``
     (see include/m3.h): writes whichever of ``sum``, ``y`` (io dtype) and ``y8``
     with ``scale`` (float8_e4m3fn, float32) are given."""
+    st = _native.rms_norm_fwd(x, eps, residual, weight, sum, y, y8, scale, scale_block) if stream is None else None
+    if st is not None:
+        return _check(st, "m3_rms_norm_fwd")
     dev, io, f32, width, n = x.get_device(), x.dtype, torch.float32, x.shape[-1], x.numel()
     rows = n // width if width else 0
     blocks = -(-width // scale_block) if scale_block > 0 else 1
@@ -486,6 +518,9 @@ def m3_rms_norm_bwd_workspace_size(rows: int, width: int, io_dtype: int) -> int:
 def m3_rms_norm_bwd(s, dy, eps: float, dx, workspace, weight=None, d_sum=None, dweight=None, stream=None) -> None:
     """Gradient of m3_rms_norm_fwd at its input ``s`` (the stored sum): writes
     ``dx`` (io dtype) and, if given, ``dweight`` (float32)."""
+    st = _native.rms_norm_bwd(s, dy, eps, dx, workspace, weight, d_sum, dweight) if stream is None else None
+    if st is not None:
+        return _check(st, "m3_rms_norm_bwd")
     dev, io, f32, width, n = s.get_device(), s.dtype, torch.float32, s.shape[-1], s.numel()
     rows = n // width if width else 0
     _call(_lib.m3_rms_norm_bwd, "m3_rms_norm_bwd", dev, stream, rows, width, io_dtype_of(s), _arg(s, "s", io, n, dev),
