@@ -333,7 +333,8 @@ m3_status m3_scan_fwd_reflect(const m3_dims* dims, const void* u,
 
 /* Bytes of device workspace m3_delta_fwd needs (host-only): 256, the status
  * word that m3_device_status reads, and on the chunked path 25 KB for every 64
- * tokens of a (batch, head). */
+ * tokens of a (batch, head), and 4.9 MB where chains share blocks (batch nheads
+ * headdim above 16 times the number of multiprocessors). */
 m3_status m3_delta_workspace_size(const m3_dims* dims, size_t* bytes);
 
 /* Prefill: y for every token from `init_h` (NULL = zeros), and the state after

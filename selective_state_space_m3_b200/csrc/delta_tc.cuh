@@ -155,12 +155,13 @@ struct Where {
     int b, h, g, p0, len, nch;     // p0: first column of the CTA
 };
 
+// where chain `tile` (a (batch, head) and PC of its columns) is
 template <int PC>
-__device__ __forceinline__ Where where_am_i(const DeltaParams& q) {
+__device__ __forceinline__ Where where_is(const DeltaParams& q, int tile) {
     Where w;
     const int slices = q.headdim / PC;
-    const int bh = blockIdx.x / slices;
-    w.p0 = (blockIdx.x % slices) * PC;
+    const int bh = tile / slices;
+    w.p0 = (tile % slices) * PC;
     w.b = bh / q.nheads;
     w.h = bh % q.nheads;
     w.g = w.h / (q.nheads / q.ngroups);

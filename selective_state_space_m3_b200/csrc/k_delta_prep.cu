@@ -206,6 +206,8 @@ __global__ void __launch_bounds__(kThreads, 5)
     const int tid = threadIdx.x, quarter = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31, row = tid;
     const int bh = blockIdx.x / q.nck, c = blockIdx.x % q.nck;
     const int b = bh / q.nheads, h = bh % q.nheads, g = h / (q.nheads / q.ngroups);
+    if (q.flags && blockIdx.x == 0)                // no state has been handed over yet (the chain is the next kernel)
+        for (int e = tid; e < kDeltaSlots; e += kThreads) q.flags[e] = 0;
     int len = q.seqlen;
     if (q.lengths && M3_IN(3, b, q.batch)) len = min(max(q.lengths[b], 0), q.seqlen);
     const int nt = min(kC, len - c * kC);

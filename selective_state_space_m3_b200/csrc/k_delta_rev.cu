@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
     const uint32_t sbase = su32(smem);
     if (!M3_SPAN(1, smem - smem_raw, OFF_MISC + (int)sizeof(Misc), dyn_smem_bytes())) return;
     const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
-    const Where w = where_am_i<PC>(q);
+    const Where w = where_is<PC>(q, blockIdx.x);
     const int P = q.headdim;
     const size_t bh = (size_t)w.b * q.nheads + w.h, rec = rec_elems(P, true);
     [[maybe_unused]] const long long ext_rec = (long long)q.batch * q.nheads * q.nck * (long long)rec;

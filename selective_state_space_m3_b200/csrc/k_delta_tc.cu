@@ -11,7 +11,7 @@
 // them for all chunks at once (k_delta_prep.cu).  The chain of a chunk is the
 // three products K S, T R and K^T U.
 //
-// One CTA per (batch, head, PC columns) walks the chunks of its sequence:
+// A CTA walks the chunks of a chain, a (batch, head) and PC of its columns:
 //   warp 0       one elected lane issues the tcgen05.mma
 //   warps 1..    the arithmetic between them: S lives in registers in float32 (a
 //                thread has one state row and 8 or 16 columns)
@@ -22,6 +22,15 @@
 // P U (lower half); the unused half is never read.  The parts of a split
 // operand stand side by side as columns of one product (a 128 x 128 x 16 product
 // takes 64 cycles, a 128 x 64 x 16 one 47) and the epilogue adds the columns.
+//
+// Chains that outnumber the SMs are laid end to end and cut into equal shares, one
+// a CTA.  Where a cut goes through a chain, its first chunks belong to the CTA
+// behind the cut, which starts with them and hands the state over through the
+// workspace, and the rest to the CTA before the cut, which ends with them: a
+// share is at least a chain long, so the state is there when it is wanted.  CTAs
+// are numbered from the end of the line, so that one waits only for one that
+// the GPU has started before it.  256 chains of 64 chunks on 148 SMs: 13 % less
+// than two rounds.
 //
 // Precision.  K, Q, V are bfloat16 and enter the products as they are.  The
 // chain keeps float32: S, R, U and T are split into bfloat16 parts (hi + lo, 16
@@ -79,8 +88,47 @@ struct Misc {
 constexpr int SMEM_BYTES = OFF_MISC + (int)sizeof(Misc) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory of the delta kernel");
 
+// The k-th piece of this CTA's share: chunks from .. to of a chain
+struct Piece {
+    Where w;
+    int from, to;
+    int take, give;                    // slot of the state that it starts from, that it leaves (-1: none)
+    bool rest;                         // not the chain's first chunks
+};
+template <int PC>
+__device__ __forceinline__ bool piece_at(const DeltaParams& q, int k, Piece* p) {
+    const int cta = gridDim.x - 1 - blockIdx.x;
+    const long long nck = q.nck, all = (long long)q.batch * q.nheads * (q.headdim / PC) * nck;
+    const long long share = (all + gridDim.x - 1) / gridDim.x, lo = cta * share, hi = min(all, lo + share);
+    const long long tile = lo / nck + k;
+    if (tile * nck >= hi) return false;
+    const int a = (int)max(lo - tile * nck, 0ll), b = (int)min(hi - tile * nck, nck);
+    p->w = where_is<PC>(q, (int)tile);
+    const int c0 = (int)nck - b, c1 = (int)nck - a;    // (one of them is an end of the chain)
+    p->rest = c0 > 0;
+    p->from = min(c0, p->w.nch);
+    p->to = min(c1, p->w.nch);
+    p->take = c0 > 0 ? cta + 1 : -1;
+    p->give = p->w.nch > c1 ? cta : -1;
+    return true;
+}
+
 __device__ __forceinline__ bool wait(uint64_t* b, int phase, Misc* m, int* status, int where) {
     return mbar_wait_flag(b, (uint32_t)(phase & 1), &m->abort_flag, status, where);
+}
+// a state that another CTA leaves (one thread; the others wait at a barrier)
+__device__ __forceinline__ void wait_hand(const int* flag, Misc* m, int* status) {
+    const uint64_t t0 = globaltimer_ns();
+    int there = 0;
+    while (!*(volatile int*)&m->abort_flag) {
+        asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(there) : "l"(flag) : "memory");
+        if (there) return;
+        if (globaltimer_ns() - t0 > kWaitNs) {
+            *(volatile int*)&m->abort_flag = 1;
+            if (atomicCAS(status, 0, (int)M3_ERR_DEVICE_TIMEOUT) == 0) status[1] = 20;
+        }
+        __nanosleep(100);
+    }
 }
 // DUMP: also write the records that the gradient's passes read
 template <int PC, bool DUMP>
@@ -93,12 +141,11 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
     const uint32_t sbase = su32(smem);
     if (!M3_SPAN(5, smem - smem_raw, OFF_MISC + (int)sizeof(Misc), dyn_smem_bytes())) return;
     const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
-    const Where w = where_am_i<PC>(q);
     constexpr int kCols = PC / kGroups<PC>;        // state columns a thread
     constexpr int W = kCols < 16 ? kCols : 16;     // columns of a TMEM load
     constexpr int NH = kCols / W, NG = kCols / 8;  // loads; 16-byte groups
     const int P = q.headdim;
-    const size_t bh = (size_t)w.b * q.nheads + w.h;
+    Piece pc;
 
     if (tid == 0) {
         for (int i = 0; i < 3; ++i) { mbar_init(&m->full[i], 1); mbar_init(&m->freed[i], 1); }
@@ -134,7 +181,9 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
         constexpr uint32_t idTl = idesc_bf16(128, PC, 0, 1);
         constexpr uint32_t idS = idesc_bf16(128, 3 * PC, 1, 1);    // A MN-major (K^T)
         const uint64_t bS = sdesc(sbase + OFF_S, 16384, 1024), bU = sdesc(sbase + OFF_U, 8192, 1024);
-        for (int c = 0; c < w.nch; ++c) {
+        int total = 0;
+        for (int k = 0; piece_at<PC>(q, k, &pc); ++k) total += pc.to - pc.from;
+        for (int c = 0; c < total; ++c) {
             const uint32_t kq = sbase + OFF_KQ + (c % 3) * 32768;
             const uint64_t aKQ = sdesc(kq, 16, 1024), aKT = sdesc(kq, 16384, 1024);
             // (PC = 64: the lo part first, the hi part that many bytes behind it)
@@ -183,21 +232,15 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
         const int wk = tid - 32, wg = wk >> 7, quarter = warp & 3, row = quarter * 32 + lane, c0 = wg * kCols;
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
         const bool top = quarter < 2;              // holds a token's K S and U; else its Q S and y
-        const int tok = row & 63, ch0 = c0 / 8, vch = (w.p0 & 63) / 8 + ch0;
+        const int tok = row & 63, ch0 = c0 / 8;
         [[maybe_unused]] const long long ext_h = (long long)q.batch * q.nheads * kN * P;
-        const size_t ho = (bh * kN + row) * P + w.p0 + c0;
+        const Where& w = pc.w;
+        int i = 0;                                 // chunks so far, of all pieces
         float2 S[kCols / 2];
-#pragma unroll
-        for (int c4 = 0; c4 < kCols / 4; ++c4) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (q.init_h && M3_SPAN(6, ho + 4 * c4, 4, ext_h)) v = *reinterpret_cast<const float4*>(q.init_h + ho + 4 * c4);
-            S[2 * c4] = make_float2(v.x, v.y);
-            S[2 * c4 + 1] = make_float2(v.z, v.w);
-        }
         // 8 columns (group ch of this thread's) of row r of a recorded part with `rows` rows
         auto keep = [&](int c, size_t at, int rows, int r, int ch, uint4 v) {
-            const size_t o = (bh * q.nck + c) * rec_elems(P, true) + kRecSlice + (size_t)(w.p0 >> 6) * kSliceElems + at +
-                             rec_at(rows, r, (w.p0 & 63) + c0 + 8 * ch);
+            const size_t o = (((size_t)w.b * q.nheads + w.h) * q.nck + c) * rec_elems(P, true) + kRecSlice +
+                             (size_t)(w.p0 >> 6) * kSliceElems + at + rec_at(rows, r, (w.p0 & 63) + c0 + 8 * ch);
             if (M3_SPAN(10, o, 8, (long long)q.batch * q.nheads * q.nck * rec_elems(P, true)))
                 *reinterpret_cast<uint4*>(q.rec + o) = v;
         };
@@ -224,17 +267,18 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
         };
         // beta V of chunk c; rows behind the end (other data, possibly not numbers) count as zero
         float2 buf[kCols / 2];                     // top: beta V, R, then U; else Q S
-        auto load_v = [&](int c) {
-            wait(&m->v_full[c & 1], c >> 1, m, status, 10);
-            wait(&m->full[c % 3], c / 3, m, status, 11);
-            const float be = reinterpret_cast<const ChainGates*>(smem + OFF_GATES)[c % 3].beta[tok];
+        auto load_v = [&](int c, int i) {
+            wait(&m->v_full[i & 1], i >> 1, m, status, 10);
+            wait(&m->full[i % 3], i / 3, m, status, 11);
+            const float be = reinterpret_cast<const ChainGates*>(smem + OFF_GATES)[i % 3].beta[tok];
             const float2 be2 = make_float2(be, be);
+            const int vch = (w.p0 & 63) / 8 + ch0;
 #pragma unroll
             for (int ch = 0; ch < NG; ++ch) {
                 const uint32_t o = sw128(tok, vch + ch);
                 uint4 vv = make_uint4(0u, 0u, 0u, 0u);
                 if (c * kC + tok < w.len && M3_SPAN(7, o, 16, 8192))
-                    vv = *reinterpret_cast<const uint4*>(smem + OFF_V + (c & 1) * 8192 + o);
+                    vv = *reinterpret_cast<const uint4*>(smem + OFF_V + (i & 1) * 8192 + o);
                 const uint32_t u[4] = {vv.x, vv.y, vv.z, vv.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -242,185 +286,221 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
                                                                   __uint_as_float(u[j] & 0xffff0000u)));
             }
         };
-        if (w.nch > 0) {
-            store_state(0);
-            if (top) load_v(0);
-        }
 #pragma unroll 1
-        for (int c = 0; c < w.nch; ++c) {
-            const ChainGates* gt = reinterpret_cast<const ChainGates*>(smem + OFF_GATES) + c % 3;
-            const bool tail = (c + 1) * kC > w.len;
-            float whole;
-            if (top) {
-                const float ba = -gt->beta[tok] * gt->a[tok], at = gt->at[tok];
-                whole = gt->whole;
-                const bool in = c * kC + tok < w.len;
-                const float2 ba2 = make_float2(ba, ba), at2 = make_float2(at, at);
-                wait(&m->ks, c, m, status, 12);
+        for (int k = 0; piece_at<PC>(q, k, &pc); ++k) {
+            if (pc.rest && pc.from == pc.to) continue;             // (the sequence ends before this piece)
+            const size_t ho = (((size_t)w.b * q.nheads + w.h) * kN + row) * P + w.p0 + c0;
+            const float* src = q.init_h ? q.init_h + ho : nullptr;
+            if (pc.take >= 0) {
+                if (tid == 32) wait_hand(q.flags + pc.take, m, status);
+                __syncwarp();
+                asm volatile("bar.sync 1, %0;" ::"n"(kState<PC>) : "memory");
+                src = q.hand + ((size_t)pc.take * kN + row) * 64 + c0;
+            }
+            [[maybe_unused]] const long long off_s = pc.take >= 0 ? src - q.hand : (long long)ho;
+            [[maybe_unused]] const long long ext_s = pc.take >= 0 ? (long long)kDeltaSlots * kN * 64 : ext_h;
+#pragma unroll
+            for (int c4 = 0; c4 < kCols / 4; ++c4) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (src && M3_SPAN(6, off_s + 4 * c4, 4, ext_s)) v = __ldcg(reinterpret_cast<const float4*>(src + 4 * c4));
+                S[2 * c4] = make_float2(v.x, v.y);
+                S[2 * c4 + 1] = make_float2(v.z, v.w);
+            }
+            if (pc.from < pc.to) {
+                store_state(pc.from);
+                if (top) load_v(pc.from, i);
+            }
+#pragma unroll 1
+            for (int c = pc.from; c < pc.to; ++c, ++i) {
+                const ChainGates* gt = reinterpret_cast<const ChainGates*>(smem + OFF_GATES) + i % 3;
+                const bool tail = (c + 1) * kC > w.len;
+                float whole;
+                if (top) {
+                    const float ba = -gt->beta[tok] * gt->a[tok], at = gt->at[tok];
+                    whole = gt->whole;
+                    const bool in = c * kC + tok < w.len;
+                    const float2 ba2 = make_float2(ba, ba), at2 = make_float2(at, at);
+                    wait(&m->ks, i, m, status, 12);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll
+                    for (int hh = 0; hh < NH; ++hh) {
+                        float2 d[W / 2];
+                        tmem_sum<W, 2>(tl + D_KS + W * hh, PC, d);
+#pragma unroll
+                        for (int j = 0; j < W / 2; ++j) d[j] = buf[W / 2 * hh + j] = __ffma2_rn(ba2, d[j], buf[W / 2 * hh + j]);
+                        if (tail) {                    // K S of tokens behind the end may be anything
+#pragma unroll
+                            for (int j = 0; j < W / 2; ++j)
+                                if (!in) d[j] = buf[W / 2 * hh + j] = make_float2(0.f, 0.f);
+                        }
+#pragma unroll
+                        for (int ch = 0; ch < W / 8; ++ch) {
+                            put16(smem, OFF_U, part_at<PC>(tok, 0, ch0 + W / 8 * hh + ch, 8192), 24576, take8(d + 4 * ch));
+                            put16(smem, OFF_U, part_at<PC>(tok, 1, ch0 + W / 8 * hh + ch, 8192), 24576, round8(d + 4 * ch));
+                        }
+                    }
+                    fence_async_smem();
+                    tc_fence_before();
+                    mbar_arrive(&m->r);
+                    wait(&m->tr, i, m, status, 13);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll
+                    for (int hh = 0; hh < NH; ++hh) {
+                        float2 f[W / 2];
+                        tmem_sum<W, 2>(tl + D_TR + W * hh, PC, f);
+#pragma unroll
+                        for (int j = 0; j < W / 2; ++j) f[j] = __fadd2_rn(f[j], buf[W / 2 * hh + j]);
+#pragma unroll
+                        for (int ch = 0; ch < W / 8; ++ch) {
+                            const int cc = ch0 + W / 8 * hh + ch;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) buf[W / 2 * hh + 4 * ch + j] = f[4 * ch + j];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) f[4 * ch + j] = __fmul2_rn(at2, f[4 * ch + j]);
+                            put16(smem, OFF_U, part_at<PC>(tok, 0, cc, 8192), 24576, take8(f + 4 * ch));
+                            put16(smem, OFF_U, part_at<PC>(tok, 1, cc, 8192), 24576, take8(f + 4 * ch));
+                            put16(smem, OFF_U, part_at<PC>(tok, 2, cc, 8192), 24576, round8(f + 4 * ch));
+                        }
+                    }
+                    fence_async_smem();
+                    tc_fence_before();
+                    arrive_after(&m->u, __float_as_uint(whole));
+                    // U's parts for P U, while the state's update is made
+#pragma unroll
+                    for (int ch = 0; ch < NG; ++ch) {
+                        const uint4 hi = take8(buf + 4 * ch), lo = round8(buf + 4 * ch);
+                        if (DUMP) {
+                            keep(c, kSliceU, 64, tok, ch, hi);
+                            keep(c, kSliceU + kTok, 64, tok, ch, lo);
+                        } else {
+                            put16(smem, OFF_V + (i & 1) * 8192, sw128(tok, ch0 + ch), 8192, hi);
+                            if (PC == 64) put16(smem, OFF_X + (i % 3) * kXBytes + 16384, sw128(tok, ch0 + ch), 8192, lo);
+                            else put16(smem, OFF_V + (i & 1) * 8192, part_at<PC>(tok, 1, ch0 + ch, 8192), 8192, lo);
+                        }
+                    }
+                    if (!DUMP) {
+                        fence_async_smem();
+                        mbar_arrive(&m->ub);
+                    }
+                    if (c + 1 < pc.to) load_v(c + 1, i + 1);  // while the state's update is made
+                } else {
+                    wait(&m->full[i % 3], i / 3, m, status, 14);
+                    const float a = gt->a[tok];
+                    whole = gt->whole;
+                    const float sa = q.scale * a;
+                    const float2 sa2 = make_float2(sa, sa);
+                    wait(&m->ks, i, m, status, 15);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll
+                    for (int hh = 0; hh < NH; ++hh) {
+                        tmem_sum<W, 2>(tl + D_KS + W * hh, PC, buf + W / 2 * hh);
+#pragma unroll
+                        for (int j = 0; j < W / 2; ++j) buf[W / 2 * hh + j] = __fmul2_rn(sa2, buf[W / 2 * hh + j]);
+                    }
+                    if (tail) {
+                        // K rows behind the sequence's end (other data, possibly not numbers)
+                        // must be zeros: K^T U sums over all rows of the tile
+                        const int nt = w.len - c * kC;
+                        for (int e = wg * 64 + tok; e < (kC - nt) * 16; e += kState<PC> / 2) {
+                            const int r = nt + (e >> 4), ch = e & 15;
+                            put16(smem, OFF_KQ + (i % 3) * 32768 + (ch >> 3) * 16384, sw128(r, ch & 7), 16384, make_uint4(0u, 0u, 0u, 0u));
+                        }
+                        fence_async_smem();
+                    }
+                    tc_fence_before();
+                    arrive_after(&m->u, __float_as_uint(whole) | __float_as_uint(a));
+                }
+                const float2 w2 = make_float2(whole, whole);
+                wait(&m->s, i, m, status, 16);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
                 for (int hh = 0; hh < NH; ++hh) {
                     float2 d[W / 2];
-                    tmem_sum<W, 2>(tl + D_KS + W * hh, PC, d);
+                    tmem_sum<W, 3>(tl + D_S + W * hh, PC, d);
 #pragma unroll
-                    for (int j = 0; j < W / 2; ++j) d[j] = buf[W / 2 * hh + j] = __ffma2_rn(ba2, d[j], buf[W / 2 * hh + j]);
-                    if (tail) {                    // K S of tokens behind the end may be anything
-#pragma unroll
-                        for (int j = 0; j < W / 2; ++j)
-                            if (!in) d[j] = buf[W / 2 * hh + j] = make_float2(0.f, 0.f);
-                    }
-#pragma unroll
-                    for (int ch = 0; ch < W / 8; ++ch) {
-                        put16(smem, OFF_U, part_at<PC>(tok, 0, ch0 + W / 8 * hh + ch, 8192), 24576, take8(d + 4 * ch));
-                        put16(smem, OFF_U, part_at<PC>(tok, 1, ch0 + W / 8 * hh + ch, 8192), 24576, round8(d + 4 * ch));
-                    }
+                    for (int j = 0; j < W / 2; ++j) S[W / 2 * hh + j] = __ffma2_rn(w2, S[W / 2 * hh + j], d[j]);
                 }
-                fence_async_smem();
-                tc_fence_before();
-                mbar_arrive(&m->r);
-                wait(&m->tr, c, m, status, 13);
-                __syncwarp();
-                tc_fence_after();
+                if (c + 1 < pc.to) store_state(c + 1);
+                if (!DUMP && !top) {
+                    wait(&m->o, i, m, status, 17);
+                    __syncwarp();
+                    tc_fence_after();
+                    const size_t o = (((size_t)w.b * q.seqlen + c * kC + tok) * q.nheads + w.h) * P + w.p0 + c0;
+                    const bool in = c * kC + tok < w.len && M3_SPAN(8, o, kCols, (long long)q.batch * q.seqlen * q.nheads * P);
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(q.y) + o);
 #pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-                    float2 f[W / 2];
-                    tmem_sum<W, 2>(tl + D_TR + W * hh, PC, f);
+                    for (int hh = 0; hh < NH; ++hh) {
+                        float2 f[W / 2];
+                        tmem_sum<W, 2>(tl + D_O + W * hh, PC, f);
 #pragma unroll
-                    for (int j = 0; j < W / 2; ++j) f[j] = __fadd2_rn(f[j], buf[W / 2 * hh + j]);
+                        for (int j = 0; j < W / 2; ++j) f[j] = __fadd2_rn(buf[W / 2 * hh + j], f[j]);
+                        if (in) {
 #pragma unroll
-                    for (int ch = 0; ch < W / 8; ++ch) {
-                        const int cc = ch0 + W / 8 * hh + ch;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) buf[W / 2 * hh + 4 * ch + j] = f[4 * ch + j];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) f[4 * ch + j] = __fmul2_rn(at2, f[4 * ch + j]);
-                        put16(smem, OFF_U, part_at<PC>(tok, 0, cc, 8192), 24576, take8(f + 4 * ch));
-                        put16(smem, OFF_U, part_at<PC>(tok, 1, cc, 8192), 24576, take8(f + 4 * ch));
-                        put16(smem, OFF_U, part_at<PC>(tok, 2, cc, 8192), 24576, round8(f + 4 * ch));
-                    }
-                }
-                fence_async_smem();
-                tc_fence_before();
-                arrive_after(&m->u, __float_as_uint(whole));
-                // U's parts for P U, while the state's update is made
-#pragma unroll
-                for (int ch = 0; ch < NG; ++ch) {
-                    const uint4 hi = take8(buf + 4 * ch), lo = round8(buf + 4 * ch);
-                    if (DUMP) {
-                        keep(c, kSliceU, 64, tok, ch, hi);
-                        keep(c, kSliceU + kTok, 64, tok, ch, lo);
-                    } else {
-                        put16(smem, OFF_V + (c & 1) * 8192, sw128(tok, ch0 + ch), 8192, hi);
-                        if (PC == 64) put16(smem, OFF_X + (c % 3) * kXBytes + 16384, sw128(tok, ch0 + ch), 8192, lo);
-                        else put16(smem, OFF_V + (c & 1) * 8192, part_at<PC>(tok, 1, ch0 + ch, 8192), 8192, lo);
-                    }
-                }
-                if (!DUMP) {
-                    fence_async_smem();
-                    mbar_arrive(&m->ub);
-                }
-                if (c + 1 < w.nch) load_v(c + 1);  // while the state's update is made
-            } else {
-                wait(&m->full[c % 3], c / 3, m, status, 14);
-                const float a = gt->a[tok];
-                whole = gt->whole;
-                const float sa = q.scale * a;
-                const float2 sa2 = make_float2(sa, sa);
-                wait(&m->ks, c, m, status, 15);
-                __syncwarp();
-                tc_fence_after();
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-                    tmem_sum<W, 2>(tl + D_KS + W * hh, PC, buf + W / 2 * hh);
-#pragma unroll
-                    for (int j = 0; j < W / 2; ++j) buf[W / 2 * hh + j] = __fmul2_rn(sa2, buf[W / 2 * hh + j]);
-                }
-                if (tail) {
-                    // K rows behind the sequence's end (other data, possibly not numbers)
-                    // must be zeros: K^T U sums over all rows of the tile
-                    const int nt = w.len - c * kC;
-                    for (int e = wg * 64 + tok; e < (kC - nt) * 16; e += kState<PC> / 2) {
-                        const int r = nt + (e >> 4), ch = e & 15;
-                        put16(smem, OFF_KQ + (c % 3) * 32768 + (ch >> 3) * 16384, sw128(r, ch & 7), 16384, make_uint4(0u, 0u, 0u, 0u));
-                    }
-                    fence_async_smem();
-                }
-                tc_fence_before();
-                arrive_after(&m->u, __float_as_uint(whole) | __float_as_uint(a));
-            }
-            const float2 w2 = make_float2(whole, whole);
-            wait(&m->s, c, m, status, 16);
-            __syncwarp();
-            tc_fence_after();
-#pragma unroll
-            for (int hh = 0; hh < NH; ++hh) {
-                float2 d[W / 2];
-                tmem_sum<W, 3>(tl + D_S + W * hh, PC, d);
-#pragma unroll
-                for (int j = 0; j < W / 2; ++j) S[W / 2 * hh + j] = __ffma2_rn(w2, S[W / 2 * hh + j], d[j]);
-            }
-            if (c + 1 < w.nch) store_state(c + 1);
-            if (!DUMP && !top) {
-                wait(&m->o, c, m, status, 17);
-                __syncwarp();
-                tc_fence_after();
-                const size_t o = (((size_t)w.b * q.seqlen + c * kC + tok) * q.nheads + w.h) * P + w.p0 + c0;
-                const bool in = c * kC + tok < w.len && M3_SPAN(8, o, kCols, (long long)q.batch * q.seqlen * q.nheads * P);
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(q.y) + o);
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-                    float2 f[W / 2];
-                    tmem_sum<W, 2>(tl + D_O + W * hh, PC, f);
-#pragma unroll
-                    for (int j = 0; j < W / 2; ++j) f[j] = __fadd2_rn(buf[W / 2 * hh + j], f[j]);
-                    if (in) {
-#pragma unroll
-                        for (int ch = 0; ch < W / 8; ++ch) dst[W / 8 * hh + ch] = round8(f + 4 * ch);
+                            for (int ch = 0; ch < W / 8; ++ch) dst[W / 8 * hh + ch] = round8(f + 4 * ch);
+                        }
                     }
                 }
             }
-        }
-        if (q.final_h && M3_SPAN(9, ho, kCols, ext_h)) {
+            float* dst = pc.give >= 0 ? q.hand + ((size_t)pc.give * kN + row) * 64 + c0 : q.final_h ? q.final_h + ho : nullptr;
+            [[maybe_unused]] const long long off_d = pc.give >= 0 ? dst - q.hand : (long long)ho;
+            [[maybe_unused]] const long long ext_d = pc.give >= 0 ? (long long)kDeltaSlots * kN * 64 : ext_h;
+            if (dst && M3_SPAN(9, off_d, kCols, ext_d)) {
 #pragma unroll
-            for (int c4 = 0; c4 < kCols / 4; ++c4)
-                *reinterpret_cast<float4*>(q.final_h + ho + 4 * c4) =
-                    make_float4(S[2 * c4].x, S[2 * c4].y, S[2 * c4 + 1].x, S[2 * c4 + 1].y);
+                for (int c4 = 0; c4 < kCols / 4; ++c4)
+                    *reinterpret_cast<float4*>(dst + 4 * c4) =
+                        make_float4(S[2 * c4].x, S[2 * c4].y, S[2 * c4 + 1].x, S[2 * c4 + 1].y);
+            }
+            if (pc.give >= 0) {
+                __threadfence();
+                asm volatile("bar.sync 1, %0;" ::"n"(kState<PC>) : "memory");
+                if (tid == 32) asm volatile("st.release.gpu.global.b32 [%0], 1;" ::"l"(q.flags + pc.give) : "memory");
+            }
         }
     } else {
         // ------------------------------------------------------------- loads
         if (lane == 0) {
             const size_t rec = rec_elems(P, DUMP);
             int asked = 0, asked_v = 0;            // (fewer than the chunks after a wait that ran out)
-            for (int c = 0; c < w.nch; ++c) {
-                const uint32_t kq = sbase + OFF_KQ + (c % 3) * 32768, x = sbase + OFF_X + (c % 3) * kXBytes;
-                if (c >= 3 && !wait(&m->freed[c % 3], c / 3 - 1, m, status, 30)) break;
-                // chunk c + 3 into L2: its load waits for a stage, and then finds it there
-                if (c + 3 < w.nch) {
-                    const int t = (c + 3) * kC;
-                    tma_prefetch_5d(&tmK, 0, 0, w.g, t, w.b);
-                    tma_prefetch_5d(&tmK, 64, 0, w.g, t, w.b);
-                    tma_prefetch_5d(&tmQ, 0, 0, w.g, t, w.b);
-                    tma_prefetch_5d(&tmQ, 64, 0, w.g, t, w.b);
-                    tma_prefetch_5d(&tmV, w.p0 & ~63, 0, w.h, t, w.b);
-                    bulk_prefetch(q.rec + (bh * q.nck + c + 3) * rec, kXBytes + sizeof(ChainGates));
+            const Where& w = pc.w;
+            bool go = true;
+            for (int k = 0, i = 0; go && piece_at<PC>(q, k, &pc); ++k) {
+                const size_t bh = (size_t)w.b * q.nheads + w.h;
+                for (int c = pc.from; c < pc.to; ++c, ++i) {
+                    const uint32_t kq = sbase + OFF_KQ + (i % 3) * 32768, x = sbase + OFF_X + (i % 3) * kXBytes;
+                    go = i < 3 || wait(&m->freed[i % 3], i / 3 - 1, m, status, 30);
+                    if (!go) break;
+                    // chunk c + 3 into L2: its load waits for a stage, and then finds it there
+                    if (c + 3 < pc.to) {
+                        const int t = (c + 3) * kC;
+                        tma_prefetch_5d(&tmK, 0, 0, w.g, t, w.b);
+                        tma_prefetch_5d(&tmK, 64, 0, w.g, t, w.b);
+                        tma_prefetch_5d(&tmQ, 0, 0, w.g, t, w.b);
+                        tma_prefetch_5d(&tmQ, 64, 0, w.g, t, w.b);
+                        tma_prefetch_5d(&tmV, w.p0 & ~63, 0, w.h, t, w.b);
+                        bulk_prefetch(q.rec + (bh * q.nck + c + 3) * rec, kXBytes + sizeof(ChainGates));
+                    }
+                    uint64_t* bar = &m->full[i % 3];
+                    const __nv_bfloat16* src = q.rec + (bh * q.nck + c) * rec;
+                    M3_NOTE(13, (bh * q.nck + c) * rec + kRecPL - 1, (long long)q.batch * q.nheads * q.nck * (long long)rec);
+                    mbar_expect_tx(bar, 32768 + kXBytes + sizeof(ChainGates));
+                    tma_load_5d(kq, &tmK, bar, 0, 0, w.g, c * kC, w.b);
+                    tma_load_5d(kq + 16384, &tmK, bar, 64, 0, w.g, c * kC, w.b);
+                    tma_load_5d(kq + 8192, &tmQ, bar, 0, 0, w.g, c * kC, w.b);
+                    tma_load_5d(kq + 24576, &tmQ, bar, 64, 0, w.g, c * kC, w.b);
+                    ++asked;
+                    bulk_load(x, src + kRecX, kXBytes, bar);
+                    bulk_load(sbase + OFF_GATES + (i % 3) * (int)sizeof(ChainGates), src + kRecGates, sizeof(ChainGates), bar);
+                    go = i < 2 || wait(&m->v_free[i & 1], (i >> 1) - 1, m, status, 31);
+                    if (!go) break;
+                    ++asked_v;
+                    bar = &m->v_full[i & 1];
+                    mbar_expect_tx(bar, 8192);
+                    tma_load_5d(sbase + OFF_V + (i & 1) * 8192, &tmV, bar, w.p0 & ~63, 0, w.h, c * kC, w.b);
                 }
-                uint64_t* bar = &m->full[c % 3];
-                const __nv_bfloat16* src = q.rec + (bh * q.nck + c) * rec;
-                M3_NOTE(13, (bh * q.nck + c) * rec + kRecPL - 1, (long long)q.batch * q.nheads * q.nck * (long long)rec);
-                mbar_expect_tx(bar, 32768 + kXBytes + sizeof(ChainGates));
-                tma_load_5d(kq, &tmK, bar, 0, 0, w.g, c * kC, w.b);
-                tma_load_5d(kq + 16384, &tmK, bar, 64, 0, w.g, c * kC, w.b);
-                tma_load_5d(kq + 8192, &tmQ, bar, 0, 0, w.g, c * kC, w.b);
-                tma_load_5d(kq + 24576, &tmQ, bar, 64, 0, w.g, c * kC, w.b);
-                ++asked;
-                bulk_load(x, src + kRecX, kXBytes, bar);
-                bulk_load(sbase + OFF_GATES + (c % 3) * (int)sizeof(ChainGates), src + kRecGates, sizeof(ChainGates), bar);
-                if (c >= 2 && !wait(&m->v_free[c & 1], (c >> 1) - 1, m, status, 31)) break;
-                ++asked_v;
-                bar = &m->v_full[c & 1];
-                mbar_expect_tx(bar, 8192);
-                tma_load_5d(sbase + OFF_V + (c & 1) * 8192, &tmV, bar, w.p0 & ~63, 0, w.h, c * kC, w.b);
             }
             // nothing may still be on its way into shared memory when the CTA ends
             for (int c = max(0, asked - 3); c < asked; ++c)
@@ -438,6 +518,16 @@ __global__ void __launch_bounds__(kThreads<PC>, 1)
 
 }  // namespace dtc
 
+static long long chain_ctas() {
+    const int sms = device_sm_count();
+    return sms < kDeltaSlots ? sms : kDeltaSlots;
+}
+// (0 where even chains of 16 columns have a CTA each)
+size_t delta_hand_bytes(const m3_dims& d) {
+    if ((long long)d.batch * d.nheads * (d.headdim / 16) <= chain_ctas()) return 0;
+    return kDeltaFlagBytes + sizeof(float) * kDeltaSlots * dtc::kN * dtc::kP;
+}
+
 size_t delta_record_bytes(const m3_dims& d, bool grad) { return dtc::rec_elems(d.headdim, grad) * 2; }
 
 bool delta_tc_eligible(const m3_dims& d) {
@@ -450,7 +540,8 @@ static cudaError_t launch_pc(const CUtensorMap& mK, const CUtensorMap& mQ, const
     using namespace dtc;
     const cudaError_t e = cudaFuncSetAttribute(delta_tc_kernel<PC, DUMP>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((long long)d.batch * d.nheads * (d.headdim / PC));
+    const long long chains = (long long)d.batch * d.nheads * (d.headdim / PC), most = chain_ctas();
+    const unsigned grid = (unsigned)(chains < most ? chains : most);
     delta_tc_kernel<PC, DUMP><<<grid, kThreads<PC>, SMEM_BYTES, st>>>(mK, mQ, mV, q, status);
     return cudaGetLastError();
 }
@@ -466,11 +557,11 @@ cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, bool grad, i
     if (e != cudaSuccess) return e;
     // Columns a CTA.  A chunk of a chain takes 3.2 us with 64 columns, 1.95 with 32
     // and 1.45 with 16 (measured; the products' latency stays, the arithmetic
-    // shrinks): the choice is the least time over the rounds that the CTAs make on
-    // this GPU's SMs, so that few sequences are spread over them.
-    const long long tiles = (long long)d.batch * d.nheads * (d.headdim / kP), sms = device_sm_count();
-    auto rounds = [&](int split) { return (tiles * split + sms - 1) / sms; };
-    const long long t64 = 320 * rounds(1), t32 = 195 * rounds(2), t16 = 145 * rounds(4);
+    // shrinks): the choice is the least time of a CTA's share, a chain or more, so
+    // that few sequences are spread over the SMs.
+    const long long tiles = (long long)d.batch * d.nheads * (d.headdim / kP), most = chain_ctas();
+    auto share = [&](int split) { return tiles * split > most ? tiles * split : most; };
+    const long long t64 = 320 * share(1), t32 = 195 * share(2), t16 = 145 * share(4);
     const int pc = t64 <= t32 && t64 <= t16 ? 64 : t32 <= t16 ? 32 : 16;
     if (grad)
         return pc == 64 ? launch_pc<64, true>(mK, mQ, mV, d, q, status, st)

@@ -675,6 +675,13 @@ static DeltaParams delta_params(const m3_dims& d, const void* q, const void* k, 
     return p;
 }
 
+// the place of the states that CTAs of the prefill hand over, if they do
+static void set_hand(const m3_dims& d, DeltaParams* p, char* at) {
+    if (!delta_hand_bytes(d)) return;
+    p->flags = reinterpret_cast<int*>(at);
+    p->hand = reinterpret_cast<float*>(at + kDeltaFlagBytes);
+}
+
 // a call without tokens: the state (or its gradient) passes through
 static m3_status state_passthrough(const m3_dims& d, const float* in, float* out, cudaStream_t st) {
     if (!out || d.batch == 0 || in == out) return M3_OK;
@@ -690,7 +697,7 @@ m3_status m3_delta_workspace_size(const m3_dims* d, size_t* bytes) {
     // the chunked path: a record a chunk
     *bytes = kWorkspaceHeaderBytes;
     if (delta_fwd_chunked(*d))
-        *bytes += round256((size_t)d->batch * d->nheads * delta_chunks(*d) * delta_record_bytes(*d, false));
+        *bytes += delta_hand_bytes(*d) + round256((size_t)d->batch * d->nheads * delta_chunks(*d) * delta_record_bytes(*d, false));
     return M3_OK;
 }
 
@@ -712,7 +719,9 @@ m3_status m3_delta_fwd(const m3_dims* d, const void* q, const void* k, const voi
     p.y = y;
     p.final_h = final_h;
     p.nck = delta_chunks(*d);
-    p.rec = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(workspace) + kWorkspaceHeaderBytes);
+    char* ws = static_cast<char*>(workspace) + kWorkspaceHeaderBytes;
+    set_hand(*d, &p, ws);
+    p.rec = reinterpret_cast<__nv_bfloat16*>(ws + (delta_fwd_chunked(*d) ? delta_hand_bytes(*d) : 0));
     const cudaError_t e = delta_fwd_chunked(*d) ? launch_delta_tc(*d, p, false, static_cast<int*>(workspace), st)
                                                 : launch_delta_seq(*d, p, st);
     return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
@@ -737,7 +746,7 @@ m3_status m3_delta_step(const m3_dims* d, const float* h_in, float* h_out, const
 struct DeltaBwdLayout {
     bool chunked;
     int KB, nck;
-    size_t ckpt, rec, part_qk, part_g, total;
+    size_t ckpt, hand, rec, part_qk, part_g, total;
 };
 
 // Token path: a state a checkpoint, and every column tile's parts of dq, dk,
@@ -752,6 +761,7 @@ static DeltaBwdLayout delta_bwd_layout(const m3_dims& d) {
     const size_t rows = l.chunked ? (d.nheads == d.ngroups ? 0 : units * l.nck * l.KB) : units * d.seqlen * delta_tiles(d);
     size_t off = kWorkspaceHeaderBytes;
     l.ckpt = off;    off = round256(off + (l.chunked ? 0 : units * l.nck * NP * sizeof(float)));
+    l.hand = off;    off += l.chunked ? delta_hand_bytes(d) : 0;
     l.rec = off;     off = round256(off + (l.chunked ? units * l.nck * delta_record_bytes(d, true) : 0));
     l.part_qk = off; off = round256(off + rows * 2 * d.dstate * sizeof(float));
     l.part_g = off;  off = round256(off + (l.chunked ? 0 : rows * 2 * sizeof(float)));
@@ -794,6 +804,7 @@ m3_status m3_delta_bwd(const m3_dims* d, const void* q, const void* k, const voi
     p.part_qk = reinterpret_cast<float*>(ws + l.part_qk);
     p.part_g = reinterpret_cast<float*>(ws + l.part_g);
     p.rec = reinterpret_cast<__nv_bfloat16*>(ws + l.rec);
+    if (l.chunked) set_hand(*d, &p, ws + l.hand);
     const cudaError_t e = l.chunked ? launch_delta_bwd_tc(*d, p, static_cast<int*>(workspace), st)
                                     : launch_delta_seq_bwd(*d, p, st);
     return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;

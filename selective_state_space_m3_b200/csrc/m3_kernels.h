@@ -156,7 +156,13 @@ struct DeltaParams {
     float* part_qk;            // [column tile][b][t][h][2][n]: parts of dq, dk; chunked: [b][h][chunk][2][n / 4][64][4]
     float* part_g;             // [column tile][b][t][h][2]: parts of dg, dbeta
     __nv_bfloat16* rec;        // chunked path: nck records a (b, h) (delta_tc.cuh)
+    float* hand;               // states handed from CTA to CTA [kDeltaSlots][128][64]
+    int* flags;                // ... and whether they are there [kDeltaSlots]
 };
+constexpr int kDeltaSlots = 148;   // most CTAs of the prefill's chains that share chains
+// bytes of `hand` and `flags` (0: a CTA each for all chains)
+size_t delta_hand_bytes(const m3_dims& d);
+constexpr size_t kDeltaFlagBytes = 1024;
 int delta_block_tokens(const m3_dims& d);
 int delta_tiles(const m3_dims& d);
 cudaError_t launch_delta_seq(const m3_dims& d, const DeltaParams& q, cudaStream_t st);

@@ -57,3 +57,21 @@ def test_a_gate_that_is_no_number_stays_in_its_sequence(sign):
     for b in (0, 2):
         assert torch.equal(g1["dq"][b], g0["dq"][b]) and torch.equal(g1["dk"][b], g0["dk"][b])
     assert torch.equal(y1[1, :64, 0], y0[1, :64, 0])
+
+
+# batch, tokens, heads, headdim: chains that are cut between blocks, of 64 and of 32 columns a block
+CUT = [(40, 200, 4, 64), (60, 130, 5, 64), (21, 330, 5, 64), (19, 70, 2, 256), (300, 65, 1, 64)]
+
+
+@pytest.mark.parametrize("init", [False, True])
+@pytest.mark.parametrize("case", CUT, ids=["b%d_t%d_h%d_p%d" % c for c in CUT])
+def test_chains_cut_between_blocks(case, init):
+    """More chains than multiprocessors: a chain's first and last part are made
+    by different blocks, whatever the sequences' lengths."""
+    b, t, h, p = case
+    x = delta_inputs(b, t, h, 1, p, 128, torch.bfloat16, seed=33)
+    for lengths in (None, torch.tensor([(37 * i) % (t + 40) for i in range(b)])):
+        y, hn = _fwd(x, 0.2, lengths, init=init)
+        again, hn2 = _fwd(x, 0.2, lengths, init=init)
+        assert torch.equal(hn, hn2) and torch.equal(torch.nan_to_num(y), torch.nan_to_num(again))
+        _check_fwd(x, y, hn, 0.2, lengths, init=init)
