@@ -441,31 +441,43 @@ __global__ void __launch_bounds__(kThreads) delta_reduce_kernel(DeltaParams q, i
 }
 
 // -------------------------------------------------------------- one token --
-// One CTA per (b, h): the state streams through registers once, 128 bits a
-// load, all loads issued before any arithmetic; row group rg of a thread holds
-// rows rg, rg + RG, ... at four columns.  Bound by the state's traffic (8 bytes
-// an element, 90 % of all bytes for N = 128, P = 64): 256 sequences of 32 heads,
-// 0.54 GB, take 105 us, 5.2 TB/s.  Four CTAs an SM are the best: 109 us without
-// the bound, 132 us with five, which leave too few registers for all loads at
-// once; two that stay and ask for the next state before they work on the present
-// one take 120 us.
+// One CTA per (b, h).  The state comes into shared memory by asynchronous copies
+// of 16 bytes, all issued before anything else; row group rg of a thread copies
+// and uses rows rg, rg + RG, ... at four columns, so no thread waits for
+// another's.  Bound by the state's traffic (8 bytes an element, 90 % of all bytes
+// for N = 128, P = 64): 256 sequences of 32 heads, 0.54 GB, take 104 us, 5.2 TB/s.
+// Five CTAs an SM.  The state in registers instead: 107 us with three or four
+// CTAs, 132 with five, which leave too few registers for all loads at once; two
+// CTAs that stay and ask for the next state before they work on the present one
+// take 120 us.
+__host__ __device__ constexpr int step_floats(int N, int P, int NPT) { return NPT * 1024 + 2 * N + P + 16 * P; }
+
 template <typename T, int NPT>
-__global__ void __launch_bounds__(256, NPT <= 8 ? 4 : 1) delta_step_kernel(DeltaParams q) {
-    __shared__ float sk[256], sq[256], sv[256], red[8][2][256], skq[8];
+__global__ void __launch_bounds__(256, NPT <= 8 ? 5 : 2) delta_step_kernel(DeltaParams q) {
+    extern __shared__ __align__(16) float step_smem[];
+    __shared__ float skq[8];
     const int N = q.dstate, P = q.headdim, tid = threadIdx.x;
+    if (!M3_SPAN(29, 0, step_floats(N, P, NPT) * 4, dyn_smem_bytes())) return;
+    float4* st = reinterpret_cast<float4*>(step_smem);         // [NPT][256]
+    float* sk = step_smem + NPT * 1024;
+    float* sq = sk + N;
+    float* sv = sq + N;
+    float* red = sv + P;                                       // [8][2][P]
     const int PC = P >> 2, RG = 256 / PC;
     const int pc = tid % PC, rg = tid / PC;
     const int bh = blockIdx.x, b = bh / q.nheads, h = bh % q.nheads, g = h / (q.nheads / q.ngroups);
     const long long ext_h = (long long)q.batch * q.nheads * N * P;
     const size_t hb = (size_t)bh * N * P;
     const float4* src = reinterpret_cast<const float4*>(q.init_h + hb);
-    float4 S[NPT];
 #pragma unroll
     for (int i = 0; i < NPT; ++i) {
         const int n = rg + RG * i;
-        S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (n < N && M3_SPAN(23, hb + (size_t)n * P + 4 * pc, 4, ext_h)) S[i] = __ldcs(src + (size_t)n * PC + pc);
+        if (n < N && M3_SPAN(23, hb + (size_t)n * P + 4 * pc, 4, ext_h))
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                         ::"r"((uint32_t)__cvta_generic_to_shared(st + i * 256 + tid)), "l"(src + (size_t)n * PC + pc)
+                         : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     const size_t ko = ((size_t)b * q.ngroups + g) * N;
     float kq = 0.f;
     if (tid < N && M3_IN(24, ko + tid, (long long)q.batch * q.ngroups * N)) {
@@ -480,16 +492,19 @@ __global__ void __launch_bounds__(256, NPT <= 8 ? 4 : 1) delta_step_kernel(Delta
     if ((tid & 31) == 0) skq[tid >> 5] = kq;
     const bool okt = M3_IN(26, bh, (long long)q.batch * q.nheads);
     const float a = q.g && okt ? expf(clamp_g(q.g[bh])) : 1.f, beta = okt ? q.beta[bh] : 0.f;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     float rk[4] = {0.f, 0.f, 0.f, 0.f}, rq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NPT; ++i) {
         const int n = rg + RG * i;
-        const float kv = n < N ? sk[n] : 0.f, qv = n < N ? sq[n] : 0.f;
-        rk[0] = fmaf(S[i].x, kv, rk[0]); rk[1] = fmaf(S[i].y, kv, rk[1]);
-        rk[2] = fmaf(S[i].z, kv, rk[2]); rk[3] = fmaf(S[i].w, kv, rk[3]);
-        rq[0] = fmaf(S[i].x, qv, rq[0]); rq[1] = fmaf(S[i].y, qv, rq[1]);
-        rq[2] = fmaf(S[i].z, qv, rq[2]); rq[3] = fmaf(S[i].w, qv, rq[3]);
+        if (n >= N) continue;
+        const float kv = sk[n], qv = sq[n];
+        const float4 S = st[i * 256 + tid];
+        rk[0] = fmaf(S.x, kv, rk[0]); rk[1] = fmaf(S.y, kv, rk[1]);
+        rk[2] = fmaf(S.z, kv, rk[2]); rk[3] = fmaf(S.w, kv, rk[3]);
+        rq[0] = fmaf(S.x, qv, rq[0]); rq[1] = fmaf(S.y, qv, rq[1]);
+        rq[2] = fmaf(S.z, qv, rq[2]); rq[3] = fmaf(S.w, qv, rq[3]);
     }
     // over the row groups: lanes of a warp that share a column group (PC < 32),
     // then the warps; a column's value is the sum of the warps that hold it
@@ -507,8 +522,8 @@ __global__ void __launch_bounds__(256, NPT <= 8 ? 4 : 1) delta_step_kernel(Delta
     if (lane < PC) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            red[slot][0][4 * pc + j] = rk[j];
-            red[slot][1][4 * pc + j] = rq[j];
+            red[(2 * slot) * P + 4 * pc + j] = rk[j];
+            red[(2 * slot + 1) * P + 4 * pc + j] = rq[j];
         }
     }
     __syncthreads();
@@ -520,8 +535,8 @@ __global__ void __launch_bounds__(256, NPT <= 8 ? 4 : 1) delta_step_kernel(Delta
     for (int j = 0; j < 4; ++j) {
         float k2 = 0.f, q2 = 0.f;
         for (int w = 0; w < slots; ++w) {
-            k2 += red[w][0][4 * pc + j];
-            q2 += red[w][1][4 * pc + j];
+            k2 += red[(2 * w) * P + 4 * pc + j];
+            q2 += red[(2 * w + 1) * P + 4 * pc + j];
         }
         u[j] = beta * fmaf(-a, k2, sv[4 * pc + j]);
         if (rg == 0 && M3_IN(27, (size_t)bh * P + 4 * pc + j, (long long)q.batch * q.nheads * P))
@@ -533,16 +548,17 @@ __global__ void __launch_bounds__(256, NPT <= 8 ? 4 : 1) delta_step_kernel(Delta
         const int n = rg + RG * i;
         if (n < N && M3_SPAN(28, hb + (size_t)n * P + 4 * pc, 4, ext_h)) {
             const float kv = sk[n];
+            const float4 S = st[i * 256 + tid];
             __stcs(dst + (size_t)n * PC + pc,
-                   make_float4(fmaf(kv, u[0], a * S[i].x), fmaf(kv, u[1], a * S[i].y), fmaf(kv, u[2], a * S[i].z),
-                               fmaf(kv, u[3], a * S[i].w)));
+                   make_float4(fmaf(kv, u[0], a * S.x), fmaf(kv, u[1], a * S.y), fmaf(kv, u[2], a * S.z),
+                               fmaf(kv, u[3], a * S.w)));
         }
     }
 }
 
 template <typename K>
 static cudaError_t launch(K* kernel, unsigned grid, int smem, cudaStream_t st, const DeltaParams& q) {
-    if (smem > 48 * 1024) {
+    if (smem > 40 * 1024) {              // (the kernels have a little static shared memory too)
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
@@ -571,9 +587,9 @@ static cudaError_t seq_bwd(const DeltaParams& q, unsigned grid, cudaStream_t st)
 template <typename T>
 static cudaError_t step(const DeltaParams& q, unsigned grid, cudaStream_t st) {
     const int RG = 256 / (q.headdim / 4), npt = (q.dstate + RG - 1) / RG;
-    if (npt <= 4) return launch(delta_step_kernel<T, 4>, grid, 0, st, q);
-    if (npt <= 8) return launch(delta_step_kernel<T, 8>, grid, 0, st, q);
-    return launch(delta_step_kernel<T, 16>, grid, 0, st, q);
+    if (npt <= 4) return launch(delta_step_kernel<T, 4>, grid, step_floats(q.dstate, q.headdim, 4) * 4, st, q);
+    if (npt <= 8) return launch(delta_step_kernel<T, 8>, grid, step_floats(q.dstate, q.headdim, 8) * 4, st, q);
+    return launch(delta_step_kernel<T, 16>, grid, step_floats(q.dstate, q.headdim, 16) * 4, st, q);
 }
 
 }  // namespace delta
