@@ -362,7 +362,9 @@ m3_status m3_delta_bwd_workspace_size(const m3_dims* dims, size_t* bytes);
  * projections' backward products take them; sums are float32 and rounded once
  * at the end.  dg may be NULL; d_final_h and d_init_h (float32) may be NULL.
  * Results do not depend on the order in which blocks run.  Outputs must not
- * overlap inputs. */
+ * overlap inputs.  Part of the work may run on a second stream that the library
+ * keeps for the calling thread; it is forked off `stream` and joined to it by
+ * events, also in a capture. */
 m3_status m3_delta_bwd(const m3_dims* dims, const void* q, const void* k, const void* v,
                        const float* g, const float* beta, float scale, const int* lengths,
                        const float* init_h, const void* dy, const float* d_final_h,

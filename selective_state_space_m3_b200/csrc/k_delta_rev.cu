@@ -377,7 +377,7 @@ static cudaError_t launch(const CUtensorMap& mK, const CUtensorMap& mQ, const CU
 
 }  // namespace drev
 
-cudaError_t launch_delta_rev(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st) {
+cudaError_t launch_delta_rev(const m3_dims& d, const DeltaParams& q, int columns, int* status, cudaStream_t st) {
     using namespace drev;
     CUtensorMap mK, mQ, mY;
     if (!make_tile_map(&mK, q.k, kN, 1, d.ngroups, d.seqlen, d.batch, kC) ||
@@ -388,7 +388,8 @@ cudaError_t launch_delta_rev(const m3_dims& d, const DeltaParams& q, int* status
     // prefill's chain (2.1 us a chunk with 32, 1.7 with 16)
     const long long tiles = (long long)d.batch * d.nheads * (d.headdim / 64), sms = device_sm_count();
     const long long t32 = 210 * ((2 * tiles + sms - 1) / sms), t16 = 170 * ((4 * tiles + sms - 1) / sms);
-    return t32 <= t16 ? launch<32>(mK, mQ, mY, d, q, status, st) : launch<16>(mK, mQ, mY, d, q, status, st);
+    return columns == 32 || (!columns && t32 <= t16) ? launch<32>(mK, mQ, mY, d, q, status, st)
+                                                     : launch<16>(mK, mQ, mY, d, q, status, st);
 }
 
 }  // namespace m3

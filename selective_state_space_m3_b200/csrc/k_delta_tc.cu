@@ -564,23 +564,26 @@ static cudaError_t launch_pc(const CUtensorMap& mK, const CUtensorMap& mQ, const
     return cudaGetLastError();
 }
 
-cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, bool grad, int* status, cudaStream_t st) {
+// Columns a CTA.  A chunk of a chain takes 3.2 us with 64 columns, 1.95 with 32
+// and 1.45 with 16 (measured; the products' latency stays, the arithmetic
+// shrinks): the choice is the least time of a CTA's share, a chain or more, so
+// that few sequences are spread over the SMs.
+static int chain_columns(long long tiles) {
+    const long long most = chain_ctas();
+    auto share = [&](int split) { return tiles * split > most ? tiles * split : most; };
+    const long long t64 = 320 * share(1), t32 = 195 * share(2), t16 = 145 * share(4);
+    return t64 <= t32 && t64 <= t16 ? 64 : t32 <= t16 ? 32 : 16;
+}
+
+cudaError_t launch_delta_chain(const m3_dims& d, const DeltaParams& q, bool grad, int columns, int* status, cudaStream_t st) {
     using namespace dtc;
     CUtensorMap mK, mQ, mV;
     if (!make_tile_map(&mK, q.k, kN, 1, d.ngroups, d.seqlen, d.batch, kC) ||
         !make_tile_map(&mQ, q.q, kN, 1, d.ngroups, d.seqlen, d.batch, kC) ||
         !make_tile_map(&mV, q.v, d.headdim, 1, d.nheads, d.seqlen, d.batch, kC))
         return cudaErrorInvalidValue;
-    const cudaError_t e = launch_delta_prep(d, q, grad, status, st);
-    if (e != cudaSuccess) return e;
-    // Columns a CTA.  A chunk of a chain takes 3.2 us with 64 columns, 1.95 with 32
-    // and 1.45 with 16 (measured; the products' latency stays, the arithmetic
-    // shrinks): the choice is the least time of a CTA's share, a chain or more, so
-    // that few sequences are spread over the SMs.
     const long long tiles = (long long)d.batch * d.nheads * (d.headdim / kP), most = chain_ctas();
-    auto share = [&](int split) { return tiles * split > most ? tiles * split : most; };
-    const long long t64 = 320 * share(1), t32 = 195 * share(2), t16 = 145 * share(4);
-    const int pc = t64 <= t32 && t64 <= t16 ? 64 : t32 <= t16 ? 32 : 16;
+    const int pc = columns ? columns : chain_columns(tiles);
     const bool cut = tiles * (kP / pc) > most;
     auto go = [&](auto dump, auto cuts) {
         constexpr bool D = decltype(dump)::value, C = decltype(cuts)::value;
@@ -591,6 +594,11 @@ cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, bool grad, i
     using Yes = std::true_type;
     using No = std::false_type;
     return grad ? (cut ? go(Yes(), Yes()) : go(Yes(), No())) : (cut ? go(No(), Yes()) : go(No(), No()));
+}
+
+cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st) {
+    const cudaError_t e = launch_delta_prep(d, q, false, status, st);
+    return e == cudaSuccess ? launch_delta_chain(d, q, false, 0, status, st) : e;
 }
 
 }  // namespace m3

@@ -722,7 +722,7 @@ m3_status m3_delta_fwd(const m3_dims* d, const void* q, const void* k, const voi
     char* ws = static_cast<char*>(workspace) + kWorkspaceHeaderBytes;
     set_hand(*d, &p, ws);
     p.rec = reinterpret_cast<__nv_bfloat16*>(ws + (delta_fwd_chunked(*d) ? delta_hand_bytes(*d) : 0));
-    const cudaError_t e = delta_fwd_chunked(*d) ? launch_delta_tc(*d, p, false, static_cast<int*>(workspace), st)
+    const cudaError_t e = delta_fwd_chunked(*d) ? launch_delta_tc(*d, p, static_cast<int*>(workspace), st)
                                                 : launch_delta_seq(*d, p, st);
     return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }

@@ -170,13 +170,15 @@ cudaError_t launch_delta_seq_bwd(const m3_dims& d, const DeltaParams& q, cudaStr
 // chunked prefill on the tensor cores (bf16, N = 128, P a multiple of 64);
 // `status` is the workspace status word its bounded waits report to
 bool delta_tc_eligible(const m3_dims& d);
-// (the records of k_delta_prep.cu, then the chain; grad: records for the gradient, no y)
+cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st);
+// its parts: the records of k_delta_prep.cu and the chain (`columns` a CTA, 0: the
+// choice is the kernel's; grad: records for the gradient, no y)
 cudaError_t launch_delta_prep(const m3_dims& d, const DeltaParams& q, bool grad, int* status, cudaStream_t st);
-cudaError_t launch_delta_tc(const m3_dims& d, const DeltaParams& q, bool grad, int* status, cudaStream_t st);
+cudaError_t launch_delta_chain(const m3_dims& d, const DeltaParams& q, bool grad, int columns, int* status, cudaStream_t st);
 // bytes of a record, one a chunk of 64 tokens of a (batch, head)
 size_t delta_record_bytes(const m3_dims& d, bool grad);
 // chunked gradient (same shapes)
-cudaError_t launch_delta_rev(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st);
+cudaError_t launch_delta_rev(const m3_dims& d, const DeltaParams& q, int columns, int* status, cudaStream_t st);
 cudaError_t launch_delta_bwd_tc(const m3_dims& d, const DeltaParams& q, int* status, cudaStream_t st);
 cudaError_t launch_delta_step(const m3_dims& d, const DeltaParams& q, cudaStream_t st);
 
