@@ -559,7 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float vb = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) vb += m->drv[j][i] + m->beta[j][i];
-                const float vg = i < nt ? dg[e] : 0.f;
+                // (before the first token the state is zero: its gate has no gradient, where the sums leave a rounding)
+                const float vg = i < nt && (c > 0 || i > 0 || q.init_h) ? dg[e] : 0.f;
                 vb = i < nt ? vb : 0.f;
                 if (out_g) out_g[o] = __float2bfloat16_rn(vg);
                 out_b[o] = __float2bfloat16_rn(vb);

@@ -14,8 +14,10 @@
 // so 8-bit output needs no second pass.  The weight's gradient stays in
 // registers over the rows that a thread group walks; the CTAs' parts are added
 // by a second kernel in a fixed order.  Rows whose width is not a multiple of 8
-// (or too wide for registers) take scalar kernels that read the row again from
-// cache.
+// start anywhere: their threads load single elements, a warp 32 neighbours, and a
+// warp has whole blocks of 128 columns, so that scales and the weight's gradient
+// need no other layout.  Rows too wide for registers take kernels that read the
+// row again from cache.
 #include <cuda_fp8.h>
 
 #define M3_BOUNDS_FILE 11
@@ -241,7 +243,70 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 3 : 1) norm_kernel(NormParams q
     }
 }
 
-// any width: one CTA a row, elements strided over the threads
+// Rows of any width up to 8192.  Warp w of the WPR warps of a row has the blocks
+// of 128 columns w, w + WPR, ... (NB of them), lane l the columns l, l + 32, l + 64
+// and l + 96 of each; all loads go out before any arithmetic.
+template <typename T, int NB>
+__global__ void __launch_bounds__(512) norm_odd_kernel(NormParams q, int wpr) {
+    __shared__ float buf[16];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp & (wpr - 1), tpr = 32 * wpr;
+    const long long row = (long long)blockIdx.x * (blockDim.x / tpr) + warp / wpr;
+    const long long ext = q.rows * q.width;
+    const bool live = row < q.rows;
+    const size_t base = live ? (size_t)row * q.width : 0;
+    const T* x = static_cast<const T*>(q.x);
+    const T* r = static_cast<const T*>(q.residual);
+    float s[4 * NB], v[4 * NB];
+    auto col = [&](int e) { return (w0 + wpr * (e >> 2)) * 128 + (e & 3) * 32 + lane; };
+#pragma unroll
+    for (int e = 0; e < 4 * NB; ++e) {
+        const bool in = live && col(e) < q.width && M3_IN(30, base + col(e), ext);
+        s[e] = in ? ld_io(x + base + col(e)) : 0.f;
+        v[e] = in && r ? ld_io(r + base + col(e)) : 0.f;
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4 * NB; ++e) {
+        s[e] += v[e];
+        ss = fmaf(s[e], s[e], ss);
+    }
+    ss = row_reduce<false>(ss, tpr, buf);
+    const float rs = rsqrtf(ss / (float)q.width + q.eps);
+#pragma unroll
+    for (int e = 0; e < 4 * NB; ++e) {
+        const bool in = live && col(e) < q.width && M3_IN(31, base + col(e), ext);
+        v[e] = in ? s[e] * rs * (q.weight ? __ldg(q.weight + col(e)) : 1.f) : 0.f;
+        if (in && q.sum) st_io(static_cast<T*>(q.sum) + base + col(e), s[e]);
+        if (in && q.y) st_io(static_cast<T*>(q.y) + base + col(e), v[e]);
+    }
+    if (!q.y8) return;
+    const int nb = q.block ? (q.width + 127) >> 7 : 1;
+    float top = 0.f;
+    if (!q.block) {
+#pragma unroll
+        for (int e = 0; e < 4 * NB; ++e) top = nmax(top, fabsf(v[e]));
+        top = nmax(row_reduce<true>(top, tpr, buf), kTiny);
+        if (live && w0 == 0 && lane == 0 && M3_IN(32, row, q.rows)) q.scale[row] = top * (1.f / kE4M3Max);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        if (q.block) {
+            top = nmax(nmax(fabsf(v[4 * b]), fabsf(v[4 * b + 1])), nmax(fabsf(v[4 * b + 2]), fabsf(v[4 * b + 3])));
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = nmax(top, __shfl_xor_sync(kFull, top, o));
+            top = nmax(top, kTiny);
+            const int k = w0 + wpr * b;
+            if (live && lane == 0 && k < nb && M3_IN(33, row * nb + k, q.rows * nb)) q.scale[row * nb + k] = top * (1.f / kE4M3Max);
+        }
+        const float inv = __fdiv_rn(kE4M3Max, top);
+#pragma unroll
+        for (int e = 4 * b; e < 4 * b + 4; ++e)
+            if (live && col(e) < q.width && M3_IN(34, base + col(e), ext))
+                q.y8[base + col(e)] = __nv_cvt_float_to_fp8(v[e] * inv, __NV_SATFINITE, __NV_E4M3);
+    }
+}
+
+// wider rows: one CTA a row, elements strided over the threads
 template <typename T>
 __global__ void __launch_bounds__(256) norm_any_kernel(NormParams q) {
     __shared__ float buf[16];
@@ -367,6 +432,66 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormParams q, int tpr) {
             q.part[(size_t)blockIdx.x * q.width + c] = sums[c];
 }
 
+// Rows of any width up to 8192, in the layout of norm_odd_kernel
+template <typename T, int NB>
+__global__ void __launch_bounds__(512) norm_bwd_odd_kernel(NormParams q, int wpr) {
+    extern __shared__ float sums[];
+    __shared__ float2 buf[2][16];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp & (wpr - 1), tpr = 32 * wpr;
+    const int per = blockDim.x / tpr, sub = warp / wpr;
+    const long long group = (long long)blockIdx.x * per + sub, groups = (long long)gridDim.x * per;
+    const long long ext = q.rows * q.width, rounds = (q.rows + groups - 1) / groups;
+    const T* x = static_cast<const T*>(q.x);
+    const T* dy = static_cast<const T*>(q.dy);
+    const T* ds = static_cast<const T*>(q.d_sum);
+    auto col = [&](int e) { return (w0 + wpr * (e >> 2)) * 128 + (e & 3) * 32 + lane; };
+    float w[4 * NB], dw[4 * NB];
+#pragma unroll
+    for (int e = 0; e < 4 * NB; ++e) {
+        w[e] = col(e) >= q.width ? 0.f : q.weight ? __ldg(q.weight + col(e)) : 1.f;
+        dw[e] = 0.f;
+    }
+    for (long long k = 0; k < rounds; ++k) {
+        const long long row = k * groups + group;
+        const bool live = row < q.rows;
+        const size_t base = live ? (size_t)row * q.width : 0;
+        float s[4 * NB], d[4 * NB], g[4 * NB];
+#pragma unroll
+        for (int e = 0; e < 4 * NB; ++e) {
+            const bool in = live && col(e) < q.width && M3_IN(35, base + col(e), ext);
+            s[e] = in ? ld_io(x + base + col(e)) : 0.f;
+            d[e] = in ? ld_io(dy + base + col(e)) : 0.f;
+            g[e] = in && ds ? ld_io(ds + base + col(e)) : 0.f;
+        }
+        float2 sum = both(0.f);
+#pragma unroll
+        for (int e = 0; e < 4 * NB; ++e) {
+            sum.x = fmaf(s[e], s[e], sum.x);
+            sum.y = fmaf(s[e] * w[e], d[e], sum.y);
+        }
+        sum = row_reduce2(sum, tpr, buf[k & 1]);
+        const float rs = rsqrtf(sum.x / (float)q.width + q.eps);
+        const float m = sum.y * rs * rs / (float)q.width;
+#pragma unroll
+        for (int e = 0; e < 4 * NB; ++e) {
+            if (!(live && col(e) < q.width && M3_IN(36, base + col(e), ext))) continue;
+            dw[e] = fmaf(d[e], s[e] * rs, dw[e]);
+            st_io(static_cast<T*>(q.dx) + base + col(e), fmaf(rs, fmaf(w[e], d[e], -s[e] * m), g[e]));
+        }
+    }
+    if (!q.dweight) return;
+    for (int g = 0; g < per; ++g) {                // group by group into the CTA's sums
+        if (sub == g)
+#pragma unroll
+            for (int e = 0; e < 4 * NB; ++e)
+                if (col(e) < q.width && M3_IN(37, col(e), dyn_smem_bytes() / 4)) sums[col(e)] = g ? sums[col(e)] + dw[e] : dw[e];
+        __syncthreads();
+    }
+    for (int c = threadIdx.x; c < q.width; c += blockDim.x)
+        if (M3_IN(38, (long long)blockIdx.x * q.width + c, (long long)q.parts * q.width))
+            q.part[(size_t)blockIdx.x * q.width + c] = sums[c];
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) norm_bwd_any_kernel(NormParams q) {
     __shared__ float buf[16];
@@ -442,6 +567,29 @@ static Shape shape_of(long long rows, int width, int most_nv) {
 }
 static bool vec_ok(int width) { return width % 8 == 0 && width <= 512 * 4 * 8; }
 
+// Warps a row and blocks of 128 columns a warp, for widths that vec_ok leaves: as
+// few warps as have at most `most` blocks each, so that CTAs are small and many
+// rows are on their way (5070 x 2340 bfloat16: 25 us with 4 warps, 97 with 16);
+// few rows: a block a warp.
+struct OddShape {
+    int wpr, nb, threads;
+    long long groups;
+};
+static OddShape odd_shape_of(long long rows, int width, int most) {
+    const int blocks = (width + 127) / 128;
+    OddShape s;
+    if (rows < 256) most = 1;
+    s.wpr = 1;
+    while (s.wpr < 16 && (blocks + s.wpr - 1) / s.wpr > most) s.wpr *= 2;
+    s.nb = (blocks + s.wpr - 1) / s.wpr;
+    s.threads = s.wpr > 4 ? 32 * s.wpr : 128;
+    const int per = s.threads / (32 * s.wpr);
+    s.groups = (rows + per - 1) / per;
+    return s;
+}
+constexpr int kOddFwd = 5, kOddBwd = 4;
+static bool odd_ok(int width) { return width <= 8192; }
+
 template <typename T, int NV>
 static cudaError_t fwd_nv(const NormParams& q, const Shape& s, cudaStream_t st) {
     const unsigned grid = (unsigned)s.groups;
@@ -455,7 +603,18 @@ static cudaError_t fwd_nv(const NormParams& q, const Shape& s, cudaStream_t st) 
 template <typename T>
 static cudaError_t fwd(const NormParams& q, cudaStream_t st) {
     if (!vec_ok(q.width)) {
-        norm_any_kernel<T><<<(unsigned)q.rows, 256, 0, st>>>(q);
+        if (!odd_ok(q.width)) {
+            norm_any_kernel<T><<<(unsigned)q.rows, 256, 0, st>>>(q);
+            return cudaGetLastError();
+        }
+        const OddShape s = odd_shape_of(q.rows, q.width, kOddFwd);
+        switch (s.nb) {
+            case 1: norm_odd_kernel<T, 1><<<(unsigned)s.groups, s.threads, 0, st>>>(q, s.wpr); break;
+            case 2: norm_odd_kernel<T, 2><<<(unsigned)s.groups, s.threads, 0, st>>>(q, s.wpr); break;
+            case 3: norm_odd_kernel<T, 3><<<(unsigned)s.groups, s.threads, 0, st>>>(q, s.wpr); break;
+            case 4: norm_odd_kernel<T, 4><<<(unsigned)s.groups, s.threads, 0, st>>>(q, s.wpr); break;
+            default: norm_odd_kernel<T, 5><<<(unsigned)s.groups, s.threads, 0, st>>>(q, s.wpr);
+        }
         return cudaGetLastError();
     }
     const Shape s = shape_of(q.rows, q.width, q.residual ? 2 : 4);
@@ -467,7 +626,12 @@ static cudaError_t fwd(const NormParams& q, cudaStream_t st) {
 // (16384 x 2048: 59 us with four an SM, 5 of them the parts' sums; 118 without loads ahead)
 static unsigned bwd_grid(long long rows, int width) {
     const long long sms = device_sm_count();
-    if (!vec_ok(width)) return (unsigned)(rows < 4 * sms ? rows : 4 * sms);
+    if (!vec_ok(width)) {
+        if (!odd_ok(width)) return (unsigned)(rows < 4 * sms ? rows : 4 * sms);
+        const OddShape s = odd_shape_of(rows, width, kOddBwd);     // (loads of one row at a time: more CTAs)
+        const long long most = (s.threads <= 128 ? 8 : s.threads <= 256 ? 4 : 2) / (s.nb <= 2 ? 1 : 2) * sms;
+        return (unsigned)(s.groups < most ? s.groups : most);
+    }
     const Shape s = shape_of(rows, width, 2);
     const long long most = (s.threads <= 128 ? 4 : s.threads <= 256 ? 2 : 1) * sms;
     return (unsigned)(s.groups < most ? s.groups : most);
@@ -487,7 +651,16 @@ static cudaError_t bwd_nv(const NormParams& q, const Shape& s, cudaStream_t st) 
 template <typename T>
 static cudaError_t bwd(const NormParams& q, cudaStream_t st) {
     cudaError_t e;
-    if (!vec_ok(q.width)) {
+    if (!vec_ok(q.width) && odd_ok(q.width)) {
+        const OddShape s = odd_shape_of(q.rows, q.width, kOddBwd);
+        const unsigned grid = bwd_grid(q.rows, q.width);
+        const int smem = q.dweight ? q.width * 4 : 0;      // (32 KB at most)
+        if (s.nb == 1) norm_bwd_odd_kernel<T, 1><<<grid, s.threads, smem, st>>>(q, s.wpr);
+        else if (s.nb == 2) norm_bwd_odd_kernel<T, 2><<<grid, s.threads, smem, st>>>(q, s.wpr);
+        else if (s.nb == 3) norm_bwd_odd_kernel<T, 3><<<grid, s.threads, smem, st>>>(q, s.wpr);
+        else norm_bwd_odd_kernel<T, 4><<<grid, s.threads, smem, st>>>(q, s.wpr);
+        e = cudaGetLastError();
+    } else if (!vec_ok(q.width)) {
         norm_bwd_any_kernel<T><<<bwd_grid(q.rows, q.width), 256, 0, st>>>(q);
         e = cudaGetLastError();
     } else {

@@ -75,3 +75,14 @@ def test_chains_cut_between_blocks(case, init):
         again, hn2 = _fwd(x, 0.2, lengths, init=init)
         assert torch.equal(hn, hn2) and torch.equal(torch.nan_to_num(y), torch.nan_to_num(again))
         _check_fwd(x, y, hn, 0.2, lengths, init=init)
+
+
+@pytest.mark.parametrize("shape", [(2, 1, 12, 1, 128), (3, 70, 2, 2, 64), (160, 2, 4, 1, 64)])
+def test_the_first_gate_has_no_gradient_without_a_state(shape):
+    """dg_0 = a_0 <dS, S before the first token>: exactly zero where that state is."""
+    b, t, h, g, p = shape
+    x = delta_inputs(b, t, h, g, p, 128, torch.bfloat16, seed=34)
+    x["h0"] = torch.zeros_like(x["h0"])
+    got = _bwd(x, 0.2, init=False)
+    assert float(got["dg"][:, 0].float().abs().sum()) == 0.0
+    _check_bwd(x, got, 0.2, init=False)
