@@ -569,8 +569,10 @@ static bool vec_ok(int width) { return width % 8 == 0 && width <= 512 * 4 * 8; }
 
 // Warps a row and blocks of 128 columns a warp, for widths that vec_ok leaves: as
 // few warps as have at most `most` blocks each, so that CTAs are small and many
-// rows are on their way (5070 x 2340 bfloat16: 25 us with 4 warps, 97 with 16);
-// few rows: a block a warp.
+// rows are on their way; few rows: a block a warp.  Many rows without an 8-bit output go
+// to norm_any_kernel from 385 columns on: 10256 x 2340 bfloat16 take 55 us there and 174
+// here (float32 72 and 92), 46601 x 515 take 100 and 186, 203389 x 118 313 and 75; with
+// scales a block of 128 columns 10256 x 2340 take 224 and 188, and the gradient 189 and 127.
 struct OddShape {
     int wpr, nb, threads;
     long long groups;
@@ -587,7 +589,7 @@ static OddShape odd_shape_of(long long rows, int width, int most) {
     s.groups = (rows + per - 1) / per;
     return s;
 }
-constexpr int kOddFwd = 5, kOddBwd = 4;
+constexpr int kOddFwd = 4, kOddBwd = 4;
 static bool odd_ok(int width) { return width <= 8192; }
 
 template <typename T, int NV>
@@ -603,7 +605,7 @@ static cudaError_t fwd_nv(const NormParams& q, const Shape& s, cudaStream_t st) 
 template <typename T>
 static cudaError_t fwd(const NormParams& q, cudaStream_t st) {
     if (!vec_ok(q.width)) {
-        if (!odd_ok(q.width)) {
+        if (!odd_ok(q.width) || (!q.y8 && q.rows >= 256 && q.width > 384)) {
             norm_any_kernel<T><<<(unsigned)q.rows, 256, 0, st>>>(q);
             return cudaGetLastError();
         }
@@ -612,8 +614,7 @@ static cudaError_t fwd(const NormParams& q, cudaStream_t st) {
             case 1: norm_odd_kernel<T, 1><<<(unsigned)s.groups, s.threads, 0, st>>>(q, s.wpr); break;
             case 2: norm_odd_kernel<T, 2><<<(unsigned)s.groups, s.threads, 0, st>>>(q, s.wpr); break;
             case 3: norm_odd_kernel<T, 3><<<(unsigned)s.groups, s.threads, 0, st>>>(q, s.wpr); break;
-            case 4: norm_odd_kernel<T, 4><<<(unsigned)s.groups, s.threads, 0, st>>>(q, s.wpr); break;
-            default: norm_odd_kernel<T, 5><<<(unsigned)s.groups, s.threads, 0, st>>>(q, s.wpr);
+            default: norm_odd_kernel<T, 4><<<(unsigned)s.groups, s.threads, 0, st>>>(q, s.wpr);
         }
         return cudaGetLastError();
     }

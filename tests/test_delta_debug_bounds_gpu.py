@@ -14,7 +14,8 @@ pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
-@pytest.mark.parametrize("path", ["tests/test_delta_gpu.py", "tests/test_norm_gpu.py"])
+@pytest.mark.parametrize("path", ["tests/test_delta_gpu.py", "tests/test_delta_many_chunks_gpu.py",
+                                  "tests/test_delta_streams_gpu.py", "tests/test_norm_gpu.py", "tests/test_norm_odd_gpu.py"])
 def test_parity_under_the_checked_library(path):
     env = dict(os.environ, M3_DEBUG_BOUNDS="1", PYTHONPATH=ROOT)
     code = ("import selective_state_space_m3_b200 as m3\n"
