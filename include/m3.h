@@ -383,7 +383,8 @@ m3_status m3_delta_bwd(const m3_dims* dims, const void* q, const void* k, const 
  * max|y| / 448 over `scale_block` columns, 0 = the whole row
  * (scale [rows], float32) or 128 (scale [rows][ceil(width/128)]); other values
  * return M3_ERR_UNSUPPORTED.  A block of zeros has the scale 1e-30 / 448.
- * Pointers 16-byte aligned; no workspace.  rows = 0 is a valid empty call. */
+ * Pointers 16-byte aligned; no workspace.  rows = 0 is a valid empty call; rows
+ * above 2^31 - 1 and widths above 2^31 - 256 return M3_ERR_UNSUPPORTED. */
 m3_status m3_rms_norm_fwd(long long rows, int width, int io_dtype, const void* x, const void* residual,
                           const float* weight, float eps, void* sum, void* y,
                           void* y8, float* scale, int scale_block, void* stream);

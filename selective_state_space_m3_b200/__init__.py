@@ -432,6 +432,13 @@ def _size_query(fn, what: str, *args) -> int:
     return int(n.value)
 
 
+def _int(v: int, what: str) -> int:
+    """``v`` as the C int that ctypes would otherwise cut it to."""
+    if not -0x80000000 <= v <= 0x7fffffff:
+        raise M3Error(M3_ERR_UNSUPPORTED, what)
+    return int(v)
+
+
 def m3_delta_workspace_size(dims: Dims) -> int:
     return _size_query(_lib.m3_delta_workspace_size, "m3_delta_workspace_size", ctypes.byref(dims.c()))
 
@@ -504,15 +511,16 @@ def m3_rms_norm_fwd(x, eps: float, residual=None, weight=None, sum=None, y=None,
     dev, io, f32, width, n = x.get_device(), x.dtype, torch.float32, x.shape[-1], x.numel()
     rows = n // width if width else 0
     blocks = -(-width // scale_block) if scale_block > 0 else 1
-    _call(_lib.m3_rms_norm_fwd, "m3_rms_norm_fwd", dev, stream, rows, width, io_dtype_of(x), _arg(x, "x", io, n, dev),
+    _call(_lib.m3_rms_norm_fwd, "m3_rms_norm_fwd", dev, stream, rows, _int(width, "m3_rms_norm_fwd"), io_dtype_of(x),
+          _arg(x, "x", io, n, dev),
           _arg(residual, "residual", io, n, dev), _arg(weight, "weight", f32, width, dev), eps,
           _arg(sum, "sum", io, n, dev), _arg(y, "y", io, n, dev), _arg(y8, "y8", torch.float8_e4m3fn, n, dev),
-          _arg(scale, "scale", f32, rows * blocks, dev), scale_block)
+          _arg(scale, "scale", f32, rows * blocks, dev), _int(scale_block, "m3_rms_norm_fwd"))
 
 
 def m3_rms_norm_bwd_workspace_size(rows: int, width: int, io_dtype: int) -> int:
-    return _size_query(_lib.m3_rms_norm_bwd_workspace_size, "m3_rms_norm_bwd_workspace_size", int(rows), int(width),
-                       int(io_dtype))
+    return _size_query(_lib.m3_rms_norm_bwd_workspace_size, "m3_rms_norm_bwd_workspace_size", int(rows),
+                       _int(width, "m3_rms_norm_bwd_workspace_size"), int(io_dtype))
 
 
 def m3_rms_norm_bwd(s, dy, eps: float, dx, workspace, weight=None, d_sum=None, dweight=None, stream=None) -> None:
@@ -523,7 +531,8 @@ def m3_rms_norm_bwd(s, dy, eps: float, dx, workspace, weight=None, d_sum=None, d
         return _check(st, "m3_rms_norm_bwd")
     dev, io, f32, width, n = s.get_device(), s.dtype, torch.float32, s.shape[-1], s.numel()
     rows = n // width if width else 0
-    _call(_lib.m3_rms_norm_bwd, "m3_rms_norm_bwd", dev, stream, rows, width, io_dtype_of(s), _arg(s, "s", io, n, dev),
+    _call(_lib.m3_rms_norm_bwd, "m3_rms_norm_bwd", dev, stream, rows, _int(width, "m3_rms_norm_bwd"), io_dtype_of(s),
+          _arg(s, "s", io, n, dev),
           _arg(weight, "weight", f32, width, dev), eps, _arg(dy, "dy", io, n, dev), _arg(d_sum, "d_sum", io, n, dev),
           _arg(dx, "dx", io, n, dev), _arg(dweight, "dweight", f32, width, dev), *_ws(workspace, dev))
 

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormParams q) {
     ss = row_reduce<false>(ss, 256, buf);
     const float rs = rsqrtf(ss / (float)q.width + q.eps);
     const int block = q.block ? q.block : q.width;
-    const int nb = (q.width + block - 1) / block;
+    const int nb = (q.width - 1) / block + 1;
     for (int k = 0; k < nb; ++k) {
         const int c1 = min(q.width, (k + 1) * block);
         float top = 0.f;

@@ -811,9 +811,13 @@ m3_status m3_delta_bwd(const m3_dims* d, const void* q, const void* k, const voi
 }
 
 // -------------------------------------------------- root-mean-square norm --
+// widths up to kNormMaxWidth: the kernels walk a row's columns in steps of up to
+// 256 with 32-bit counters
+constexpr int kNormMaxWidth = 0x7fffff00;
+
 static m3_status check_norm(long long rows, int width, int io_dtype) {
     if (rows < 0 || width < 1 || (io_dtype != M3_F32 && io_dtype != M3_BF16)) return M3_ERR_INVALID_ARG;
-    if (rows > 0x7fffffffLL) return M3_ERR_UNSUPPORTED;
+    if (rows > 0x7fffffffLL || width > kNormMaxWidth) return M3_ERR_UNSUPPORTED;
     return M3_OK;
 }
 
