@@ -360,7 +360,9 @@ m3_status m3_delta_bwd_workspace_size(const m3_dims* dims, size_t* bytes);
  * as gradient) with respect to every input.  dq, dk (summed over the heads of
  * a group), dv, dg and dbeta are written in the io dtype, in which the
  * projections' backward products take them; sums are float32 and rounded once
- * at the end.  dg may be NULL; d_final_h and d_init_h (float32) may be NULL.
+ * at the end.  dg_t has the factor e^{g_t} and keeps its relative accuracy
+ * where that is small; it is zero where g_t resets the state, and at the first
+ * token of a sequence without init_h.  dg may be NULL; d_final_h and d_init_h (float32) may be NULL.
  * Results do not depend on the order in which blocks run.  Outputs must not
  * overlap inputs.  Part of the work may run on a second stream that the library
  * keeps for the calling thread; it is forked off `stream` and joined to it by

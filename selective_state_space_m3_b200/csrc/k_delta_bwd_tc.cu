@@ -9,12 +9,14 @@
 //   dQ  = scale e^G o Z + (scale Gam o dP) K
 //   dK  = (scale Gam o dP)^T Q + D K + D^T K + e^{G_C-G} o Y - beta e^G o X,   D = beta Gam o dA
 //   dbeta_i = dR_i . v_i - e^{G_i} k_i . X_i + sum_j dA_ij Gam_ij k_i.k_j
-//   dG_i = q_i.dQ_i - k_i.dK_i + 2 k_i.(D K)_i - 2 beta_i e^{G_i} k_i.X_i
-//   dG_C += e^{G_C} <S, dS'> + sum_j e^{G_C-G_j} k_j.Y_j;    dg_t = sum_{i >= t} dG_i
-// (dG_i: e^{G_i} multiplies whatever q_i and the row of D meet, and divides what
-// k_i's other uses meet, so the sums of rows less columns of dP o P + dA o A and
-// the terms of Z, X and Y are the inner products of q and k with their gradients,
-// but for the sign of D K and X.)
+//   dg_t = sum_{i >= t > j} W_ij + sum_{i >= t} z_i + sum_{j < t} e^{G_C-G_j} k_j.Y_j + e^{G_C} <S, dS'>,
+//     W = dP o P + dA o A (j < i),   z_i = scale e^{G_i} q_i.Z_i - beta_i e^{G_i} k_i.X_i
+// (dg_t is the sum of all that crosses from the tokens before t to t and those behind
+// it, and every term of it has the factor e^{g_t}: nothing is taken off again, so a
+// strongly decaying gate's small gradient keeps its relative accuracy, and that of a
+// gate that resets the state is zero.  As suffix sums of dG_i = q_i.dQ_i - k_i.dK_i
+// + .. it is a small remainder of large numbers: an absolute error of 1e-8 to 1e-6,
+// all of dg from mean gates of -16 on.)
 //
 // Three passes.  The prefill runs once more and records T, P, the state before
 // every chunk and U.  k_delta_rev.cu carries dS from the last chunk to the first
@@ -69,7 +71,8 @@ constexpr uint32_t D_PA = 0, D_QK = 64, D_ZX = 128, D_Y = 256, D_LAST = 384, D_T
 
 struct Misc {
     Gates gates[2];
-    float row[4][2 * kC], beta[4][kC], tail[4][kC];    // by column group (row: dq's and dk's rows)
+    float row[4][2 * kC], beta[4][kC], tail[4][kC];    // by column group (row: z, from dq's and dk's rows)
+    float left[3][2 * kC], cross[4][kC];               // W: sums of rows by column group, of what crosses by row quarter
     float drv[4][kC], dot[16];
     uint64_t full[4], done[3], drain;
     uint32_t tmem_base;
@@ -375,12 +378,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 put16(smem, OFF_D + (j & 1) * 16384, sw128(row, 2 * cg + (j >> 1)), 16384, make_uint4(0u, 0u, 0u, 0u));
+            if (lane < 16) m->cross[quarter][16 * cg + lane] = 0.f;
+            if (cg < 3) m->left[cg][row] = 0.f;
         } else {
             float d[16], s[16];
-            if (up) tmem_ld16(tl + D_PA + 16 * cg, d);
-            else tmem_ld16x2(tl + D_PA + 16 * cg, tl + D_QK + 16 * cg, d, s);
+            tmem_ld16x2(tl + D_PA + 16 * cg, tl + D_QK + 16 * cg, d, s);
             float2 f[8];
             const float f0 = up ? q.scale : -be;
+            float w = 0.f;                             // sum of W's row up to here
 #pragma unroll
             for (int k2 = 0; k2 < 8; ++k2) {
                 const int j = 16 * cg + 2 * k2;
@@ -392,8 +397,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 gj = x ? make_float2(Gj.z, Gj.w) : make_float2(Gj.x, Gj.y);
                     const bool in = live && (up ? j + x <= tok : j + x < tok);
                     const float t = in ? d[k] * ex2(diff_pair(Gi, gj)) : 0.f;      // Gam o dP, or - Gam o dA
-                    if (!up) rowB -= in ? t * s[k] : 0.f;
+                    const float ts = in ? t * s[k] : 0.f;
+                    if (!up) rowB -= ts;
                     v[x] = f0 * t;
+                    if (j + x < tok) w = fmaf(f0, ts, w);
+                    s[k] = j + x < tok ? w : 0.f;      // what crosses from the group's columns up to this one to this row
                 }
                 f[k2] = make_float2(v[0], v[1]);
             }
@@ -402,6 +410,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 put16(smem, OFF_D, sw128(row, 2 * cg + j), 16384, take8(f + 4 * j));
                 put16(smem, OFF_D + 16384, sw128(row, 2 * cg + j), 16384, round8(f + 4 * j));
             }
+            if (cg < 3) m->left[cg][row] = w;
+            // sums over the warp's rows, half of the columns going to the other half of the lanes at each step:
+            // lanes 2 j and 2 j + 1 end with column j
+#pragma unroll
+            for (int o = 16; o > 1; o >>= 1) {
+                const bool high = lane & o;
+#pragma unroll
+                for (int j = 0; j < o / 2; ++j) {
+                    const float keep = high ? s[j + o / 2] : s[j], give = high ? s[j] : s[j + o / 2];
+                    s[j] = keep + __shfl_xor_sync(kFull, give, o);
+                }
+            }
+            s[0] += __shfl_xor_sync(kFull, s[0], 1);
+            if (!(lane & 1)) m->cross[quarter][16 * cg + (lane >> 1)] = s[0];
         }
         // the last chunk's gradients have left their place in shared memory
         if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -442,11 +464,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int col8 = 4 * cg + ch;
             unpack8(*reinterpret_cast<const uint4*>(smem + OFF_QK + (col8 >> 3) * 16384 + sw128(row, col8 & 7)), k);
         };
-        float r[32], rowG = 0.f;
+        float r[32];
         tmem_ld32(tl + D_ZX + 32 * cg, r);
         if (up) {
+            float t0 = 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] *= sa;
+            for (int ch = 0; ch < 4; ++ch) {
+                float k[8];
+                own8(ch, k);
+#pragma unroll
+                for (int j = 8 * ch; j < 8 * ch + 8; ++j) r[j] *= sa;
+                t0 = dot8(r + 8 * ch, k, t0);
+            }
+            m->row[cg][row] = t0;
         } else {
             float y[32], t0 = 0.f, t1 = 0.f;
             tmem_ld32(tl + D_Y + 32 * cg, y);
@@ -459,8 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 8 * ch; j < 8 * ch + 8; ++j) r[j] = fmaf(at, y[j], -ba * r[j]);
             }
-            rowG = -2.f * ba * t0;
             rowB -= a * t0;
+            m->row[cg][row] = -ba * t0;
             tail = at * t1;
             m->beta[cg][tok] = rowB;
             m->tail[cg][tok] = tail;
@@ -469,30 +499,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         tc_fence_after();
         {
-            float l[32], t0 = 0.f, t1 = 0.f;
+            float l[32];
             tmem_ld32(tl + D_LAST + 32 * cg, l);
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                float k[8];
-                own8(ch, k);
-                if (!up) t1 = dot8(l + 8 * ch, k, t1);
-#pragma unroll
-                for (int j = 8 * ch; j < 8 * ch + 8; ++j) r[j] += l[j];
-                if (up) t0 = dot8(r + 8 * ch, k, t0);
-            }
+            for (int j = 0; j < 32; ++j) r[j] += l[j];
             if (!up) {
                 tmem_ld32(tl + D_T + 32 * cg, l);
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    float k[8];
-                    own8(ch, k);
-#pragma unroll
-                    for (int j = 8 * ch; j < 8 * ch + 8; ++j) r[j] += l[j];
-                    t0 = dot8(r + 8 * ch, k, t0);
-                }
+                for (int j = 0; j < 32; ++j) r[j] += l[j];
             }
-            rowG += up ? t0 : 2.f * t1 - t0;
-            m->row[cg][row] = rowG;
             if (!live)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) r[j] = 0.f;
@@ -527,30 +542,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (warp == 0) {
-            // lane l has tokens 2 l, 2 l + 1; dg is the sum from a token to the chunk's end
-            float d[2], tl2 = 0.f, total = 0.f;
+            // lane l has tokens 2 l, 2 l + 1.  suf[0]: sums of z from a token to the end; suf[x]:
+            // of W's rows in the column groups before x; before: sums of Y's terms before a token
+            float own[4][2], suf[4], tl2[2], before, total = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
-                d[e] = 0.f;
+                own[0][e] = tl2[e] = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    d[e] += m->row[j][i] + m->row[j][64 + i];
-                    tl2 += m->tail[j][i];
+                    own[0][e] += m->row[j][i] + m->row[j][64 + i];
+                    tl2[e] += m->tail[j][i];
                 }
+#pragma unroll
+                for (int x = 1; x < 4; ++x)
+                    own[x][e] = (x > 1 ? own[x - 1][e] : 0.f) + (m->left[x - 1][i] + m->left[x - 1][64 + i]);
             }
 #pragma unroll
-            for (int o = 16; o; o >>= 1) tl2 += __shfl_xor_sync(kFull, tl2, o);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) total += m->dot[j];
-            tl2 += gt->whole * total;
-            float sum = d[0] + d[1];
+            for (int x = 0; x < 4; ++x) suf[x] = own[x][0] + own[x][1];
+            before = tl2[0] + tl2[1];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float u = __shfl_down_sync(kFull, sum, o);
-                if (lane + o < 32) sum += u;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float u = __shfl_down_sync(kFull, suf[x], o);
+                    if (lane + o < 32) suf[x] += u;
+                }
+                const float u = __shfl_up_sync(kFull, before, o);
+                if (lane >= o) before += u;
             }
-            const float dg[2] = {sum + tl2, sum - d[0] + tl2};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {              // the tokens behind this lane's
+                suf[x] = __shfl_down_sync(kFull, suf[x], 1);
+                if (lane == 31) suf[x] = 0.f;
+            }
+            before = __shfl_up_sync(kFull, before, 1);
+            if (lane == 0) before = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) total += m->dot[j];
+            total *= gt->whole;
+            float dg[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e, grp = i > 0 ? (i - 1) >> 4 : 0;
+                float s[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[x] = suf[x] + own[x][1] + (e ? 0.f : own[x][0]);
+                float v = s[0] + (grp == 1 ? s[1] : grp == 2 ? s[2] : grp == 3 ? s[3] : 0.f);
+                if (i > 0)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v += m->cross[j][i - 1];
+                dg[e] = v + (e ? before + tl2[0] : before) + total;
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
@@ -559,8 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float vb = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) vb += m->drv[j][i] + m->beta[j][i];
-                // (before the first token the state is zero: its gate has no gradient, where the sums leave a rounding)
-                const float vg = i < nt && (c > 0 || i > 0 || q.init_h) ? dg[e] : 0.f;
+                const float vg = i < nt ? dg[e] : 0.f;
                 vb = i < nt ? vb : 0.f;
                 if (out_g) out_g[o] = __float2bfloat16_rn(vg);
                 out_b[o] = __float2bfloat16_rn(vb);
