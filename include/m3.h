@@ -319,8 +319,9 @@ m3_status m3_scan_fwd_reflect(const m3_dims* dims, const void* u,
  *   g, beta  [batch][seqlen][nheads]              float32
  *   states   [batch][nheads][dstate][headdim]     float32
  *   lengths  [batch]                              int32, device memory
- * dims->rank must be 1 and dstate at most 256 (M3_ERR_UNSUPPORTED otherwise);
- * dims->chunk is ignored.  `g` may be NULL (no decay).
+ * dims->rank must be 1, dstate at most 256 and seqlen at most 2^31 - 256
+ * (M3_ERR_UNSUPPORTED otherwise); dims->chunk is ignored.  `g` may be NULL (no
+ * decay).
  * `lengths` may be NULL (every sequence has seqlen tokens).  Otherwise sequence
  * b has lengths[b] tokens (values outside 0..seqlen count as the nearer bound):
  * its final state is the one after its last token, rows of y behind it are left

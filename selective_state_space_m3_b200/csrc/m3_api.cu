@@ -636,7 +636,11 @@ m3_status m3_selftest_bounded_wait(void* workspace, size_t workspace_bytes, void
 }
 
 // ------------------------------------------------------- gated delta rule --
-// shape checks that the delta rule adds to check_dims
+// shape checks that the delta rule adds to check_dims.  Sequences have up to
+// kDeltaMaxTokens: the kernels walk the tokens in blocks of up to 64 with 32-bit
+// counters, which must not pass 2^31 - 1 behind the last block.
+constexpr int kDeltaMaxTokens = 0x7fffff00;
+
 static m3_status check_delta(const m3_dims* d, bool need_seq) {
     m3_status s = check_dims(d, need_seq);
     if (s != M3_OK) return s;
@@ -644,6 +648,7 @@ static m3_status check_delta(const m3_dims* d, bool need_seq) {
     // launch grids are one-dimensional
     const long long kMax = 0x7fffffffLL, bh = (long long)d->batch * d->nheads;
     if (bh > kMax || bh * delta_tiles(*d) > kMax) return M3_ERR_UNSUPPORTED;
+    if (need_seq && d->seqlen > kDeltaMaxTokens) return M3_ERR_UNSUPPORTED;
     if (need_seq && ((long long)d->batch * d->seqlen * d->ngroups > kMax || bh * ((d->seqlen + 63LL) / 64) > kMax))
         return M3_ERR_UNSUPPORTED;
     return M3_OK;
