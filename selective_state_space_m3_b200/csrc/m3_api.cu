@@ -1,5 +1,6 @@
 // m3_api.cu -- the C ABI of include/m3.h: argument checks, the launch plan,
 // the workspace layout and the dispatch to the kernels.
+#include <cuda.h>
 #include <stdint.h>
 #include <stdlib.h>
 #include <string.h>
@@ -106,6 +107,24 @@ int device_sm_count() {
         cached[dev].store(n, std::memory_order_relaxed);
     }
     return n;
+}
+
+// The kernels that load by TMA take tensor maps, which the driver encodes for its
+// current context.  A host thread that has made no CUDA runtime call on a device has
+// none yet: the runtime's current device then becomes it, as its first launch would.
+static void bind_context() {
+    using Call = CUresult (*)(CUcontext*);
+    static const Call current = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const bool ok = cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &found) == cudaSuccess &&
+                        found == cudaDriverEntryPointSuccess;
+        return reinterpret_cast<Call>(ok ? p : nullptr);
+    }();
+    CUcontext ctx = nullptr;
+    int dev = 0;
+    if (current && current(&ctx) == CUDA_SUCCESS && ctx) return;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaSetDevice(dev);      // (if it fails, so does the launch)
 }
 
 // Path and chunking.  tcgen05 path: a chunk is one 128-row UMMA tile
@@ -322,6 +341,7 @@ m3_status m3_scan_fwd(const m3_dims* d, const void* x, const void* B, const void
     q.ws_sin = reinterpret_cast<float*>(ws + w.sin);
     int* status = reinterpret_cast<int*>(workspace);
     cudaError_t e;
+    if (pl.path == 1) bind_context();
     if (pl.kernel == 2) {
         e = cudaSuccess;
         if (pl.wmode == 1 && pl.nseg > 1) e = launch_scan_tc_summary(*d, q, status, st);
@@ -727,6 +747,7 @@ m3_status m3_delta_fwd(const m3_dims* d, const void* q, const void* k, const voi
     char* ws = static_cast<char*>(workspace) + kWorkspaceHeaderBytes;
     set_hand(*d, &p, ws);
     p.rec = reinterpret_cast<__nv_bfloat16*>(ws + (delta_fwd_chunked(*d) ? delta_hand_bytes(*d) : 0));
+    if (delta_fwd_chunked(*d)) bind_context();
     const cudaError_t e = delta_fwd_chunked(*d) ? launch_delta_tc(*d, p, static_cast<int*>(workspace), st)
                                                 : launch_delta_seq(*d, p, st);
     return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
@@ -809,7 +830,10 @@ m3_status m3_delta_bwd(const m3_dims* d, const void* q, const void* k, const voi
     p.part_qk = reinterpret_cast<float*>(ws + l.part_qk);
     p.part_g = reinterpret_cast<float*>(ws + l.part_g);
     p.rec = reinterpret_cast<__nv_bfloat16*>(ws + l.rec);
-    if (l.chunked) set_hand(*d, &p, ws + l.hand);
+    if (l.chunked) {
+        bind_context();
+        set_hand(*d, &p, ws + l.hand);
+    }
     const cudaError_t e = l.chunked ? launch_delta_bwd_tc(*d, p, static_cast<int*>(workspace), st)
                                     : launch_delta_seq_bwd(*d, p, st);
     return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
