@@ -40,7 +40,7 @@
  * dims/carry structs and m3_scan_fwd_phase's perm / freq arrays, which are
  * host memory read during the call).  The library allocates no
  * device memory, keeps no state between calls apart from cached device
- * attributes, and never synchronises the stream except in m3_device_status
+ * attributes and the second streams of m3_delta_bwd, and never synchronises the stream except in m3_device_status
  * and in m3_scan_fwd_phase's copy of its host arrays (SHUFFLE / FIXED modes:
  * a copy from pageable host memory may wait for the stream).
  * Work is enqueued on `stream` (a cudaStream_t; NULL = the legacy default
@@ -365,9 +365,10 @@ m3_status m3_delta_bwd_workspace_size(const m3_dims* dims, size_t* bytes);
  * where that is small; it is zero where g_t resets the state, and at the first
  * token of a sequence without init_h.  dg may be NULL; d_final_h and d_init_h (float32) may be NULL.
  * Results do not depend on the order in which blocks run.  Outputs must not
- * overlap inputs.  Part of the work may run on a second stream that the library
- * keeps for the calling thread; it is forked off `stream` and joined to it by
- * events, also in a capture. */
+ * overlap inputs.  Part of the work may run on a second stream; it is forked off
+ * `stream` and joined to it by events, also in a capture.  The library keeps one
+ * for each stream that it is called with (64 in all; further streams share them,
+ * and calls on streams that share one may wait for one another). */
 m3_status m3_delta_bwd(const m3_dims* dims, const void* q, const void* k, const void* v,
                        const float* g, const float* beta, float scale, const int* lengths,
                        const float* init_h, const void* dy, const float* d_final_h,

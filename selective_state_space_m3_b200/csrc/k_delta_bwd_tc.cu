@@ -46,6 +46,7 @@
 #define M3_BOUNDS_FILE 13
 #include "m3_bounds.cuh"
 #include "delta_tc.cuh"
+#include "side_stream.h"
 
 namespace m3 {
 
@@ -664,32 +665,7 @@ __global__ void __launch_bounds__(256) delta_group_sum_kernel(DeltaParams q) {
 
 }  // namespace dbw
 
-// A second stream of this thread for a device, with the events that fork it off a
-// call's stream and join it again.
-struct Side {
-    cudaStream_t stream;
-    cudaEvent_t fork, join;
-    bool ready;
-};
-static thread_local Side sides[64];
-
-static Side* side_of(cudaStream_t st) {
-    int dev = 0;
-    cudaStreamCaptureStatus main_cap, side_cap;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-    if (cudaStreamIsCapturing(st, &main_cap) != cudaSuccess) return nullptr;
-    Side* s = &sides[dev];
-    if (!s->ready) {
-        if (main_cap != cudaStreamCaptureStatusNone) return nullptr;       // (nothing is made while a graph is captured)
-        if (cudaStreamCreateWithFlags(&s->stream, cudaStreamNonBlocking) != cudaSuccess) return nullptr;
-        if (cudaEventCreateWithFlags(&s->fork, cudaEventDisableTiming) != cudaSuccess) return nullptr;
-        if (cudaEventCreateWithFlags(&s->join, cudaEventDisableTiming) != cudaSuccess) return nullptr;
-        s->ready = true;
-    }
-    // still in a capture that was broken off, or gone with its context: not used
-    if (cudaStreamIsCapturing(s->stream, &side_cap) != cudaSuccess || side_cap != cudaStreamCaptureStatusNone) return nullptr;
-    return s;
-}
+static SideStreams side_streams;
 
 // Both chains: the prefill's and the reverse one need the chunk matrices, not each
 // other.  Where both fit the SMs they run side by side (32 chains with 32
@@ -701,7 +677,8 @@ static cudaError_t launch_chains(const m3_dims& d, const DeltaParams& f, const D
     if (tiles * (4 + 4) <= sms) fwd = 16, rev = 16;
     else if (tiles * (2 + 2) <= sms) fwd = 32, rev = 32;
     else if (tiles * (1 + 2) <= sms) fwd = 64, rev = 32;
-    Side* side = fwd ? side_of(st) : nullptr;
+    std::unique_lock<std::mutex> use;
+    SideStream* side = fwd ? side_streams.take(st, &use) : nullptr;
     if (side && (cudaEventRecord(side->fork, st) != cudaSuccess ||
                  cudaStreamWaitEvent(side->stream, side->fork, 0) != cudaSuccess))
         side = nullptr;
