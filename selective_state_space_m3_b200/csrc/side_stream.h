@@ -88,15 +88,21 @@ class SideStreams {
 
 public:
     // The second stream for a call on the current context's stream `st`, kept for the
-    // caller as long as it holds `use`; null if there is none that can be used (one
-    // that is still in a capture is not).
+    // caller as long as it holds `use`; null if there is none that can be used.  One
+    // that an earlier call forked off the same capture stays in it until that ends,
+    // and is forked off it again; one in another capture, or a broken one, is not used.
     SideStream* take(cudaStream_t st, std::unique_lock<std::mutex>* use) noexcept {
         try {
-            cudaStreamCaptureStatus its;
             SideStream* s = find(st);
             if (!s) return nullptr;
             *use = std::unique_lock<std::mutex>(s->use);
-            if (cudaStreamIsCapturing(s->stream, &its) == cudaSuccess && its == cudaStreamCaptureStatusNone) return s;
+            cudaStreamCaptureStatus mine, its;
+            unsigned long long my_id = 0, its_id = 0;
+            if (cudaStreamGetCaptureInfo(s->stream, &its, &its_id) == cudaSuccess &&
+                (its == cudaStreamCaptureStatusNone ||
+                 (its == cudaStreamCaptureStatusActive && cudaStreamGetCaptureInfo(st, &mine, &my_id) == cudaSuccess &&
+                  mine == cudaStreamCaptureStatusActive && my_id == its_id)))
+                return s;
             use->unlock();
         } catch (...) {}               // (a lock that could not be had)
         return nullptr;

@@ -12,6 +12,7 @@
 static int streams, events, stream_frees, event_frees, fail_at = -1, made;   // fail_at: the n-th creation fails
 static unsigned long long context = 7;
 static cudaStreamCaptureStatus captured[4096];
+static unsigned long long capture_id[4096];
 static cudaStreamCaptureMode thread_mode = cudaStreamCaptureModeGlobal;
 static int number(cudaStream_t s) { return (int)((uintptr_t)s >> 4); }
 static bool fails() { return made++ == fail_at || thread_mode != cudaStreamCaptureModeRelaxed; }
@@ -42,8 +43,10 @@ cudaError_t cudaThreadExchangeStreamCaptureMode(cudaStreamCaptureMode* m) {
 }
 cudaError_t cudaStreamDestroy(cudaStream_t) { return ++stream_frees, cudaSuccess; }
 cudaError_t cudaEventDestroy(cudaEvent_t) { return ++event_frees, cudaSuccess; }
-cudaError_t cudaStreamIsCapturing(cudaStream_t s, cudaStreamCaptureStatus* c) {
+cudaError_t cudaStreamGetCaptureInfo(cudaStream_t s, cudaStreamCaptureStatus* c, unsigned long long* id, cudaGraph_t*,
+                                     const cudaGraphNode_t**, size_t*) {
     *c = captured[number(s)];
+    *id = capture_id[number(s)];
     return cudaSuccess;
 }
 }
@@ -76,6 +79,15 @@ int main() {
         check(!take(t, 1), "not one that is in a broken capture");
         captured[number(first->stream)] = cudaStreamCaptureStatusNone;
         check(take(t, 1) == first, "the same once the capture has ended");
+        const int side = number(first->stream);        // forked off a capture by an earlier call
+        captured[1] = captured[side] = cudaStreamCaptureStatusActive;
+        capture_id[1] = capture_id[side] = 5;
+        check(take(t, 1) == first && take(t, 1) == first, "again in the same capture");
+        capture_id[1] = 6;
+        check(!take(t, 1), "not in another one");
+        captured[1] = cudaStreamCaptureStatusNone;
+        check(!take(t, 1), "nor beside one");
+        captured[side] = cudaStreamCaptureStatusNone;
         captured[3] = cudaStreamCaptureStatusActive;
         check(take(t, 3) && thread_mode == cudaStreamCaptureModeGlobal, "made for a caller that is captured, whose mode comes back");
         context = 8;                                   // a device reset

@@ -20,7 +20,8 @@ SHAPE = (2, 200, 4, 2, 64, 128, torch.bfloat16)
 
 
 def _forks(graph):
-    """Nodes of a captured graph on which more than one other node depends, and the number of nodes."""
+    """Nodes of a captured graph on which more than one other node depends (not counting
+    dependencies that follow from the others), and the number of nodes."""
     from cuda.bindings import runtime as rt
     g = rt.cudaGraph_t(init_value=graph.raw_cuda_graph())
     err, _, nodes = rt.cudaGraphGetNodes(g)
@@ -31,8 +32,20 @@ def _forks(graph):
         return 0, nodes
     out = rt.cudaGraphGetEdges(g, n)
     assert int(out[0]) == 0
-    starts = [int(v) for v in out[1]]
-    return sum(starts.count(v) > 1 for v in set(starts)), nodes
+    after = {}
+    for u, v in zip(out[1], out[2]):
+        after.setdefault(int(u), set()).add(int(v))
+
+    def reached(u):
+        seen, todo = set(), list(after.get(u, ()))
+        while todo:
+            v = todo.pop()
+            if v not in seen:
+                seen.add(v)
+                todo.extend(after.get(v, ()))
+        return seen
+
+    return sum(len(vs - set().union(*(reached(v) for v in vs))) > 1 for vs in after.values()), nodes
 
 
 def _state(seed):
@@ -90,6 +103,30 @@ def test_a_first_call_that_is_captured():
             forks, nodes = _capture([_state(71)])
         assert forks == 1 and nodes == 5, (forks, nodes)
     _in_a_thread(work)
+
+
+@pytest.mark.parametrize("calls", [1, 2, 3, 7])
+def test_several_calls_in_a_capture(calls):
+    """As the layers of a training step: every call has its fork."""
+    forks, nodes = _capture([_state(73 + i) for i in range(calls)])
+    assert forks == calls and nodes == 5 * calls, (forks, nodes)
+
+
+def test_captures_after_one_another_and_one_that_was_broken_off():
+    s = _state(72)
+    for _ in range(2):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            _call(s)
+        with pytest.raises(RuntimeError):
+            with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=stream):
+                _call(s)
+                stream.synchronize()                 # not allowed in a capture, which breaks it off
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            _call(s)
+        torch.cuda.synchronize()
+        assert _capture([s, s])[0] == 2
 
 
 def test_threads_that_come_and_go():
