@@ -4,7 +4,8 @@ The functions below carry the C ABI's names and only marshal arguments: they
 check tensor placement, dtype and contiguity, turn tensors into device
 pointers and call ``libm3.so`` through ctypes on the current torch stream (the
 calls of the gated delta rule and the norm through a small native extension,
-which leaves unusual arguments to the Python code).
+which leaves unusual arguments to the Python code; where no extension was built
+for this PyTorch and Python, the Python code takes every call).
 Every step of the scan runs in the library's CUDA kernels; there is no
 PyTorch or CPU implementation behind these calls, and importing the package
 fails if the library has not been built (``python -m
@@ -22,6 +23,7 @@ import ctypes
 import dataclasses
 import importlib.util
 import os
+import sysconfig
 from typing import Optional
 
 import numpy as np
@@ -117,14 +119,27 @@ def _load():
 _lib = _load()
 
 
+def native_call_name() -> str:
+    """File name of the native extension for the running PyTorch and Python, whose ABIs it is bound to."""
+    return f"_m3_call.torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+class _PythonCall:
+    """In the extension's place: every call goes to the Python code."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _load_call():
     """The native argument handling of the calls below (csrc/m3_call.cpp), bound to the library's entry points."""
-    path = os.path.join(_PKG, "_m3_call.so")
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: it must be built (python -m selective_state_space_m3_b200.build)")
-    spec = importlib.util.spec_from_file_location("_m3_call", path)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
+    path = os.path.join(_PKG, native_call_name())
+    try:
+        spec = importlib.util.spec_from_file_location("_m3_call", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except ImportError:
+        return _PythonCall()
     mod.bind(*[ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in
                ("m3_delta_step", "m3_delta_fwd", "m3_delta_bwd", "m3_rms_norm_fwd", "m3_rms_norm_bwd")])
     return mod

@@ -6,7 +6,8 @@ With debug=True the same sources are compiled with -DM3_DEBUG_BOUNDS=1 into
 libm3_debug.so (every kernel index checked; include/m3.h,
 m3_debug_bounds_report), which the package loads instead of libm3.so when
 M3_DEBUG_BOUNDS=1 is set in the environment.  csrc/m3_call.cpp, the binding's
-native argument handling, is compiled by the host compiler into _m3_call.so.
+native argument handling, is compiled by the host compiler into
+_m3_call.torch-<version>.<Python's suffix>.so, named by the ABIs it is bound to.
 """
 from __future__ import annotations
 
@@ -24,7 +25,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libm3.so")
 OUT_DEBUG = os.path.join(PKG, "libm3_debug.so")
-OUT_CALL = os.path.join(PKG, "_m3_call.so")
 OBJ = os.path.join(PKG, "_build")
 OBJ_DEBUG = os.path.join(PKG, "_build", "debug")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -83,24 +83,33 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     return out
 
 
+def call_path(torch_dir: str) -> str:
+    """The extension for the PyTorch in `torch_dir` and this Python (as the package looks for it), without importing torch."""
+    names = {}
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        exec(f.read(), names)
+    return os.path.join(PKG, f"_m3_call.torch-{names['__version__']}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_call(force: bool = False) -> str:
     """Compile the binding's extension against the installed PyTorch; returns its path."""
     src = os.path.join(CSRC, "m3_call.cpp")
     torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     version = os.path.join(torch_dir, "version.py")
-    if force or _stale(OUT_CALL, [src, os.path.join(ROOT, "include", "m3.h"), version]):
+    out = call_path(torch_dir)
+    if force or _stale(out, [src, os.path.join(ROOT, "include", "m3.h"), version]):
         cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
         inc = [os.path.join(ROOT, "include"), os.path.join(torch_dir, "include"),
                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-        tmp = OUT_CALL + f".tmp{os.getpid()}"
+        tmp = out + f".tmp{os.getpid()}"
         cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *[f for i in inc for f in ("-isystem", i)],
                src, "-o", tmp, "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"{cmd[0]} failed on {src}:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, OUT_CALL)
-    return OUT_CALL
+        os.replace(tmp, out)
+    return out
 
 
 def build_all(force: bool = False, verbose: bool = False) -> tuple:
