@@ -3,6 +3,7 @@
 // records that the gradient's passes hand on.
 #pragma once
 
+#include "m3_delta.h"
 #include "m3_kernels.h"
 #include "tc_ptx.cuh"
 

@@ -28,6 +28,7 @@
 #define M3_BOUNDS_FILE 10
 #include "m3_bounds.cuh"
 #include "m3_common.cuh"
+#include "m3_delta.h"
 #include "m3_kernels.h"
 
 namespace m3 {

@@ -24,6 +24,7 @@
 #include "m3_bounds.cuh"
 #include "m3_common.cuh"
 #include "m3_kernels.h"
+#include "m3_norm.h"
 
 namespace m3 {
 namespace norm {

@@ -11,7 +11,9 @@
 #define M3_BOUNDS_FILE 9
 #include "m3_bounds.cuh"
 #include "m3_common.cuh"
+#include "m3_delta.h"
 #include "m3_kernels.h"
+#include "m3_norm.h"
 #include "m3_nvtx.h"
 
 namespace m3 {
