@@ -909,11 +909,10 @@ m3_status m3_debug_bounds_report(m3_bounds_report* out, int clear) {
 #if M3_DEBUG_BOUNDS
     using Take = cudaError_t (*)(BoundsRecord*, bool);
     // in file order (site = file * 1000 + check)
-    const Take takes[] = {bounds_take_scan_tc, bounds_take_scan_simt, bounds_take_step,
-                          bounds_take_rope,    bounds_take_seq,       bounds_take_bwd,
-                          bounds_take_phase,   bounds_take_scan_ws,   bounds_take_delta,
-                          bounds_take_delta_tc, bounds_take_delta_bwd_tc, bounds_take_delta_prep, bounds_take_delta_rev,
-                          bounds_take_norm,    bounds_take_api};
+    const Take takes[] = {bounds_take_scan_tc,  bounds_take_scan_simt,    bounds_take_step,       bounds_take_rope,
+                          bounds_take_seq,      bounds_take_bwd,          bounds_take_phase,      bounds_take_scan_ws,
+                          bounds_take_api,      bounds_take_delta,        bounds_take_norm,       bounds_take_delta_tc,
+                          bounds_take_delta_bwd_tc, bounds_take_delta_prep, bounds_take_delta_rev};
     out->enabled = 1;
     if (cudaDeviceSynchronize() != cudaSuccess) return M3_ERR_CUDA;
     for (Take take : takes) {
