@@ -687,7 +687,7 @@ static bool delta_chunked(const m3_dims& d) { return delta_tc_eligible(d) && !en
 // so few tokens go to the token kernel, more of them where its CTAs have an SM each.
 static bool delta_fwd_chunked(const m3_dims& d) {
     const long long ctas = (long long)d.batch * d.nheads * delta_tiles(d);
-    return delta_chunked(d) && d.seqlen > (ctas <= 148 ? 16 : 4);
+    return delta_chunked(d) && d.seqlen > (ctas <= device_sm_count() ? 16 : 4);
 }
 
 static int delta_chunks(const m3_dims& d) { return (int)((d.seqlen + 63LL) / 64); }
