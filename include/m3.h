@@ -310,8 +310,8 @@ m3_status m3_scan_fwd_reflect(const m3_dims* dims, const void* u,
  * The transition is a contraction for |k_t| <= 1, 0 <= beta_t <= 2 and
  * g_t <= 0 (keys normalised by the caller, for example by m3_rms_norm_fwd);
  * other values are computed as written and may grow.
- * g_t = -infinity resets the state before the token (log decays below -1e4
- * count as -1e4, where e^g is zero in float32).
+ * g_t = -infinity resets a state of finite values before the token (log decays
+ * below -1e4 count as -1e4, where e^g is zero in float32).
  *
  * Layouts (C order, densely packed, 16-byte aligned):
  *   q, k     [batch][seqlen][ngroups][dstate]     io dtype
@@ -326,11 +326,19 @@ m3_status m3_scan_fwd_reflect(const m3_dims* dims, const void* u,
  * b has lengths[b] tokens (values outside 0..seqlen count as the nearer bound):
  * its final state is the one after its last token, rows of y behind it are left
  * as they were, and gradients behind it are zero.
- * Arithmetic is float32.  On bfloat16 layers with dstate 128 and headdim a
- * multiple of 64 the prefill (of more than 16 tokens, or of more than 4 where
- * batch nheads headdim exceeds 148 x 16) and the gradient run chunked on the
- * tensor cores; they keep float32 values as sums of bfloat16 parts (16 bits and
- * more), and only the product that ends in y rounds an operand to bfloat16. */
+ * Token by token, arithmetic is float32.  On bfloat16 layers with dstate 128 and
+ * headdim a multiple of 64 the prefill (of more than 16 tokens, or of more than 4
+ * where batch nheads headdim exceeds 16 times the number of multiprocessors) and
+ * the gradient run chunked on the tensor cores.  There the state, its gradient
+ * and everything between them enter products as sums of bfloat16 parts (16 bits
+ * and more; the accumulators are float32), and one operand of the product that
+ * ends in y, the masked k.q, is rounded to bfloat16.  Relative errors (2-norm)
+ * measured against the token path for unit keys: of states 1e-6 to 5e-6 with
+ * beta <= 1 and keys as good as independent, 3e-5 with keys nearly alike
+ * (cosines of 0.9 and more), up to 3e-3 where such keys also have beta = 2 (the
+ * transitions then lose nothing of an error); of y, where 1.7e-3 is its own
+ * rounding, 2.3e-3, 4e-3 and up to 1e-2.
+ * Outputs must not overlap inputs except where this file says so. */
 
 /* Bytes of device workspace m3_delta_fwd needs (host-only): 256, the status
  * word that m3_device_status reads, and on the chunked path 25 KB for every 64
@@ -353,7 +361,15 @@ m3_status m3_delta_step(const m3_dims* dims, const float* h_in, float* h_out,
                         const void* q, const void* k, const void* v,
                         const float* g, const float* beta, float scale, void* y, void* stream);
 
-/* Bytes of device workspace m3_delta_bwd needs (host-only). */
+/* Bytes of device workspace m3_delta_bwd needs (host-only).  Besides 256 bytes:
+ *  - on the chunked path, for every 64 tokens of a (batch, head), 33 KB and 96 KB
+ *    for every 64 columns of headdim, another 64 KB where heads share keys, and
+ *    the 4.9 MB of the prefill where chains share blocks;
+ *  - token by token, a float32 state for every 16 tokens (8 with dstate above
+ *    128) of a (batch, head), and 2 (dstate + 1) floats for every token, head and
+ *    16 columns of headdim.  That grows with seqlen: 8 x 4096 tokens of 32 heads
+ *    of 128 x 128 in float32 need 4.3 GB and 8.7 GB.  Longer batches are cut by
+ *    the caller (over the batch, or over tokens: init_h, d_final_h, d_init_h). */
 m3_status m3_delta_bwd_workspace_size(const m3_dims* dims, size_t* bytes);
 
 /* Gradient of m3_delta_fwd: of J = sum <dy_t, y_t> + <d_final_h, final state>
@@ -364,8 +380,7 @@ m3_status m3_delta_bwd_workspace_size(const m3_dims* dims, size_t* bytes);
  * at the end.  dg_t has the factor e^{g_t} and keeps its relative accuracy
  * where that is small; it is zero where g_t resets the state, and at the first
  * token of a sequence without init_h.  dg may be NULL; d_final_h and d_init_h (float32) may be NULL.
- * Results do not depend on the order in which blocks run.  Outputs must not
- * overlap inputs.  Part of the work may run on a second stream; it is forked off
+ * Results do not depend on the order in which blocks run.  Part of the work may run on a second stream; it is forked off
  * `stream` and joined to it by events, also in a capture.  The library keeps one
  * for each stream that it is called with (64 in all; further streams share them,
  * and calls on streams that share one may wait for one another). */

@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads) delta_reduce_kernel(DeltaParams q, i
 // One CTA per (b, h).  The state comes into shared memory by asynchronous copies
 // of 16 bytes, all issued before anything else; row group rg of a thread copies
 // and uses rows rg, rg + RG, ... at four columns, so no thread waits for
-// another's.  Bound by the state's traffic (8 bytes an element, 90 % of all bytes
+// another's.  Bound by the state's traffic (8 bytes an element, 99 % of all bytes
 // for N = 128, P = 64): 256 sequences of 32 heads, 0.54 GB, take 104 us, 5.2 TB/s.
 // Five CTAs an SM.  The state in registers instead: 107 us with three or four
 // CTAs, 132 with five, which leave too few registers for all loads at once; two

@@ -16,8 +16,8 @@
 // by a second kernel in a fixed order.  Rows whose width is not a multiple of 8
 // start anywhere: their threads load single elements, a warp 32 neighbours, and a
 // warp has whole blocks of 128 columns, so that scales and the weight's gradient
-// need no other layout.  Rows too wide for registers take kernels that read the
-// row again from cache.
+// need no other layout.  Rows too wide for registers, and most rows of odd width
+// above 384 columns, take kernels that read the row again from cache.
 #include <cuda_fp8.h>
 
 #define M3_BOUNDS_FILE 11
@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(512) norm_odd_kernel(NormParams q, int wpr) {
     }
 }
 
-// wider rows: one CTA a row, elements strided over the threads
+// Rows of any width (which ones: odd_shape_of's comment): one CTA a row, elements
+// strided over the threads
 template <typename T>
 __global__ void __launch_bounds__(256) norm_any_kernel(NormParams q) {
     __shared__ float buf[16];
@@ -570,10 +571,18 @@ static bool vec_ok(int width) { return width % 8 == 0 && width <= 512 * 4 * 8; }
 
 // Warps a row and blocks of 128 columns a warp, for widths that vec_ok leaves: as
 // few warps as have at most `most` blocks each, so that CTAs are small and many
-// rows are on their way; few rows: a block a warp.  Many rows without an 8-bit output go
-// to norm_any_kernel from 385 columns on: 10256 x 2340 bfloat16 take 55 us there and 174
-// here (float32 72 and 92), 46601 x 515 take 100 and 186, 203389 x 118 313 and 75; with
-// scales a block of 128 columns 10256 x 2340 take 224 and 188, and the gradient 189 and 127.
+// rows are on their way; few rows: a block a warp.  Rows (256 and more) without an 8-bit
+// output go to norm_any_kernel from 385 columns on.  Measured with residual and sum, us there
+// and here:
+//   24 M elements, bfloat16: 118 columns 317 and 78, 250 184 and 84, 380 131 and 121, 450
+//     119 and 119, 515 104 and 139, 1026 66 and 139, 2340 62 and 148;
+//   24 M elements, float32: 118 columns 334 and 76, 386 135 and 76, 700 88 and 76, 902 80
+//     and 84, 2340 78 and 86;
+//   4000 rows: 386 columns 14 and 14, 700 16 and 25 (float32 20), 1026 18 and 32 (24);
+//   300 rows: 386 columns 6 and 14, 1026 7 and 12.
+// (So float32 rows of 386 to 800 columns would be better off here where there are tens of
+// thousands of them, up to 1.8 times, and worse where there are fewer.)  With scales a block
+// of 128 columns 10256 x 2340 take 224 and 188, and the gradient 189 and 127.
 struct OddShape {
     int wpr, nb, threads;
     long long groups;
@@ -623,7 +632,7 @@ static cudaError_t fwd(const NormParams& q, cudaStream_t st) {
     return s.nv == 1 ? fwd_nv<T, 1>(q, s, st) : s.nv == 2 ? fwd_nv<T, 2>(q, s, st) : fwd_nv<T, 4>(q, s, st);
 }
 
-// CTAs of the gradient: as many as its 124 registers let run together, so that a
+// CTAs of the gradient: as many as its 120 registers let run together, so that a
 // row's loads can go ahead of the row before and few parts are left to add
 // (16384 x 2048: 59 us with four an SM, 5 of them the parts' sums; 118 without loads ahead)
 static unsigned bwd_grid(long long rows, int width) {
