@@ -337,7 +337,9 @@ m3_status m3_scan_fwd_reflect(const m3_dims* dims, const void* u,
  * beta <= 1 and keys as good as independent, 3e-5 with keys nearly alike
  * (cosines of 0.9 and more), up to 3e-3 where such keys also have beta = 2 (the
  * transitions then lose nothing of an error); of y, where 1.7e-3 is its own
- * rounding, 2.3e-3, 4e-3 and up to 1e-2.
+ * rounding, 2.3e-3 with independent keys, 4e-3 with cosines of 0.9, up to 1e-2
+ * with 0.99; of gradients at most 5e-4 more than their own rounding with beta
+ * below 2 throughout.
  * Outputs must not overlap inputs except where this file says so. */
 
 /* Bytes of device workspace m3_delta_fwd needs (host-only): 256, the status
